@@ -387,6 +387,138 @@ int fp8_pad_varlen(const void* x, const int64_t* cu_seqlens, int32_t nseq, int64
 int fp8_unpad_varlen(const void* x_pad, const int64_t* cu_seqlens, const int64_t* cu_seqlens_pad,
                      int32_t nseq, int64_t cols, void* x, void* stream);
 
+/*
+ * The operators around the linear: layer norm before it, and the exchange of tokens in an
+ * expert block, where each expert's linear sees only the rows routed to it and FP8 GEMMs
+ * need their count to be a multiple of 16.
+ *
+ * Source: [NeMo] (the mixture-of-experts runs, dp=2 ep=2, and the padding review thread:
+ * token counts have to be padded before FP8 GEMMs); [SpecForge] Constraints bullet.
+ *
+ * These calls take rows of bf16, f16 or f32 of any width, and an input's rows may be a cut
+ * out of a wider tensor (a row stride `ld` in elements, at least the width). Unlike the
+ * entry points above, pointers need the alignment of their elements only. Outputs are dense.
+ * All sums are float32; each output element is rounded once, to nearest even.
+ */
+typedef enum fp8_dtype { FP8_DT_BF16 = 0, FP8_DT_F16 = 1, FP8_DT_F32 = 2 } fp8_dtype;
+
+/*
+ * fp8_layernorm_fwd -- y = (x - mean) * rstd * gamma + beta over each row.
+ *
+ *   x            [rows, cols] of `dtype`, row stride ldx; 1 <= cols <= 32768.
+ *   gamma, beta  [cols] of `param_dtype` (dtype itself, or FP8_DT_F32), each may be NULL
+ *                (1 and 0).
+ *   eps          finite, >= 0: rstd = 1 / sqrt(var + eps), var the mean of (x - mean)^2.
+ *   y            [rows, cols] of `dtype`, not aliasing x.
+ *   mean, rstd   float32 [rows] out, each may be NULL; the backward needs both.
+ * A row with a NaN or an infinity gives NaN in that row only.
+ * Errors: FP8_ERR_SHAPE, FP8_ERR_UNSUPPORTED (dtypes, cols > 32768), FP8_ERR_NULL,
+ * FP8_ERR_ALIGN, FP8_ERR_HIP.
+ */
+int fp8_layernorm_fwd(const void* x, int64_t ldx, const void* gamma, const void* beta,
+                      int64_t rows, int64_t cols, int dtype, int param_dtype, float eps, void* y,
+                      float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace fp8_layernorm_bwd needs (host arithmetic; may be 0). */
+int fp8_layernorm_bwd_workspace(int64_t rows, int64_t cols, int64_t* bytes);
+
+/*
+ * fp8_layernorm_bwd -- the gradient: with xh = (x - mean) * rstd and g = dy * gamma,
+ *   dx = rstd * (g - mean_c(g) - xh * mean_c(g * xh)),
+ *   dgamma = sum over rows of dy * xh, dbeta = sum over rows of dy,
+ * in one pass over dy and x. The sums over rows run in a fixed order (the same result on
+ * every call).
+ *
+ *   dy, x        [rows, cols] of `dtype`, row strides lddy and ldx.
+ *   mean, rstd   float32 [rows], of the forward.
+ *   gamma        [cols] of `param_dtype` or NULL (1).
+ *   dx           [rows, cols] of `dtype`, not aliasing dy or x, or NULL.
+ *   dgamma, dbeta  [cols] of `param_dtype`, each may be NULL; with no rows they are 0.
+ *   workspace    at least fp8_layernorm_bwd_workspace() bytes, 4-byte aligned, for this
+ *                call until it has run; NULL if that is 0.
+ * Errors as fp8_layernorm_fwd.
+ */
+int fp8_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean,
+                      const float* rstd, const void* gamma, int64_t rows, int64_t cols, int dtype,
+                      int param_dtype, void* dx, void* dgamma, void* dbeta, void* workspace,
+                      int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8_moe_rows -- rows of the buffer that holds `tokens` tokens sorted to `topk` experts
+ * each, whatever the routing: every expert's rows are rounded up to a multiple of `multiple`,
+ * and at most min(experts, tokens * topk) experts have any. Host arithmetic.
+ *   tokens >= 0, 1 <= topk <= 64, 1 <= experts <= 512, multiple >= 1; tokens * topk and the
+ *   result must be below 2^31.
+ */
+int fp8_moe_rows(int64_t tokens, int32_t topk, int32_t experts, int32_t multiple, int64_t* rows);
+
+/* Bytes of workspace fp8_moe_sort needs (host arithmetic; 0 for small batches). */
+int fp8_moe_sort_workspace(int64_t tokens, int32_t topk, int32_t experts, int64_t* bytes);
+
+/*
+ * fp8_moe_sort -- the (token, choice) pairs sorted by expert, on the device.
+ *
+ *   expert_idx   [tokens, topk] of int32 (idx_bytes 4) or int64 (idx_bytes 8). An index
+ *                outside [0, experts), such as -1, drops its pair.
+ *   slot         int32 [tokens, topk] out: the pair's row in the sorted buffer, or -1.
+ *   source       int32 [rows] out, rows = fp8_moe_rows(): the row's pair t * topk + j, or -1
+ *                for a padding row.
+ *   counts       int32 [experts] out: the expert's pairs.
+ *   offsets      int32 [experts + 1] out: the expert's first row, a multiple of `multiple`;
+ *                offsets[experts] is the end of the last expert's padded rows.
+ *   workspace    at least fp8_moe_sort_workspace() bytes, 4-byte aligned; NULL if 0.
+ * The sort is stable: an expert's pairs keep their order. Nothing is copied to the host.
+ * Errors: FP8_ERR_NULL, FP8_ERR_SHAPE, FP8_ERR_UNSUPPORTED, FP8_ERR_ALIGN, FP8_ERR_HIP.
+ */
+int fp8_moe_sort(const void* expert_idx, int idx_bytes, int64_t tokens, int32_t topk,
+                 int32_t experts, int32_t multiple, int32_t* slot, int32_t* source,
+                 int32_t* counts, int32_t* offsets, void* workspace, int64_t workspace_bytes,
+                 void* stream);
+
+/*
+ * fp8_moe_dispatch -- xs[slot[t, j]] = x[t] for the kept pairs, 0 in the padding rows.
+ *
+ *   x       [tokens, cols] of `dtype`, row stride ldx.
+ *   slot    int32 [tokens, topk]; source int32 [rows] (of fp8_moe_sort). Entries of slot
+ *           outside [0, rows) are skipped.
+ *   xs      [rows, cols] out, not aliasing x.
+ * (tokens + rows) * ceil(row bytes / 2048) must be below 2^24 (the same for the calls below).
+ */
+int fp8_moe_dispatch(const void* x, int64_t ldx, const int32_t* slot, const int32_t* source,
+                     int64_t tokens, int32_t topk, int64_t rows, int64_t cols, int dtype, void* xs,
+                     void* stream);
+
+/*
+ * fp8_moe_dispatch_bwd -- the dispatch's gradient: dx[t] = sum over kept j of dxs[slot[t, j]],
+ * in the order of the choices; 0 for a token that kept none.
+ *   dxs  [rows, cols] of `dtype`, row stride lddxs; dx [tokens, cols] out. Padding rows are
+ *        not read.
+ */
+int fp8_moe_dispatch_bwd(const void* dxs, int64_t lddxs, const int32_t* slot, int64_t tokens,
+                         int32_t topk, int64_t rows, int64_t cols, int dtype, void* dx,
+                         void* stream);
+
+/*
+ * fp8_moe_combine -- y[t] = sum over kept j of weights[t, j] * ys[slot[t, j]], in the order of
+ * the choices; 0 for a token that kept none. A dropped pair adds nothing, whatever its weight.
+ *   ys  [rows, cols] of `dtype`, row stride ldys; weights float32 [tokens, topk];
+ *   y   [tokens, cols] out, not aliasing ys.
+ */
+int fp8_moe_combine(const void* ys, int64_t ldys, const int32_t* slot, const float* weights,
+                    int64_t tokens, int32_t topk, int64_t rows, int64_t cols, int dtype, void* y,
+                    void* stream);
+
+/*
+ * fp8_moe_combine_bwd -- the combine's gradient: dys[slot[t, j]] = weights[t, j] * dy[t], 0 in
+ * the padding rows; dw[t, j] = sum_c dy[t, c] * ys[slot[t, j], c], 0 for a dropped pair.
+ *   dy  [tokens, cols] of `dtype`, row stride lddy; ys as in the combine; dys [rows, cols] and
+ *   dw float32 [tokens, topk] out; dys aliases neither input.
+ */
+int fp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ldys,
+                        const int32_t* slot, const int32_t* source, const float* weights,
+                        int64_t tokens, int32_t topk, int64_t rows, int64_t cols, int dtype,
+                        void* dys, float* dw, void* stream);
+
 /* Message for the last error returned on the calling thread ("" if none). */
 const char* fp8_last_error(void);
 

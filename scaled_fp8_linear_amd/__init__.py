@@ -12,7 +12,11 @@ from ._abi import (FP8_A_E5M2, FP8_AMAX_ACCUMULATE, FP8_BLOCK_1x128, FP8_E5M2, F
                    fp8_bias_grad, fp8_last_error, fp8_pad_varlen, fp8_unpad_varlen,
                    fp8_linear_dgrad, fp8_linear_fwd, fp8_linear_fwd_current, fp8_linear_wgrad,
                    fp8_pad_tokens,
-                   fp8_quantize_amax, fp8_scale_update, fp8_version, load)
+                   fp8_quantize_amax, fp8_scale_update, fp8_version, load,
+                   FP8_DT_BF16, FP8_DT_F16, FP8_DT_F32, fp8_layernorm_fwd, fp8_layernorm_bwd,
+                   fp8_layernorm_bwd_workspace, fp8_moe_rows, fp8_moe_sort,
+                   fp8_moe_sort_workspace, fp8_moe_dispatch, fp8_moe_dispatch_bwd,
+                   fp8_moe_combine, fp8_moe_combine_bwd)
 from .autograd import Fp8Linear, fp8_autocast, fp8_state
 from .state import DelayedScalingLinear
 
@@ -25,4 +29,7 @@ __all__ = ["fp8_quantize_amax", "fp8_scale_update", "fp8_linear_fwd", "fp8_linea
            "FP8_AMAX_ACCUMULATE", "FP8_SCALE_CLEAR_AMAX", "FP8_E5M2", "FP8_A_E5M2",
            "Fp8Linear", "fp8_autocast", "fp8_align_multiple", "fp8_pad_varlen",
            "fp8_unpad_varlen", "FP8_LAYOUT_THD", "FP8_LAYOUT_BSHD",
-           "fp8_state"]
+           "fp8_state", "FP8_DT_BF16", "FP8_DT_F16", "FP8_DT_F32",
+           "fp8_layernorm_fwd", "fp8_layernorm_bwd", "fp8_layernorm_bwd_workspace",
+           "fp8_moe_rows", "fp8_moe_sort", "fp8_moe_sort_workspace", "fp8_moe_dispatch",
+           "fp8_moe_dispatch_bwd", "fp8_moe_combine", "fp8_moe_combine_bwd"]

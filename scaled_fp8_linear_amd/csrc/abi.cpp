@@ -398,4 +398,280 @@ int fp8_unpad_varlen(const void* x_pad, const int64_t* cu_seqlens, const int64_t
                     fn);
 }
 
+namespace {
+
+int64_t elem_bytes(int dtype) { return dtype == FP8_DT_F32 ? 4 : 2; }
+
+bool aligned_to(const void* p, int64_t n) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0;
+}
+
+int check_dtype(const char* fn, int dtype) {
+  if (dtype != FP8_DT_BF16 && dtype != FP8_DT_F16 && dtype != FP8_DT_F32)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: unknown dtype %d", fn, dtype);
+  return FP8_OK;
+}
+
+// A [rows, cols] input with row stride ld.
+int check_rows(const char* fn, const char* what, const void* p, int64_t ld, int64_t rows,
+               int64_t cols, int dtype) {
+  if (ld < cols)
+    return fail(FP8_ERR_SHAPE, "%s: row stride %lld of %s is below its %lld columns", fn,
+                (long long)ld, what, (long long)cols);
+  if (rows > 1 && ld > (INT64_MAX >> 3) / rows)
+    return fail(FP8_ERR_SHAPE, "%s: %s does not fit 64-bit addresses", fn, what);
+  if (rows * cols > 0 && !p) return fail(FP8_ERR_NULL, "%s: %s is NULL", fn, what);
+  if (!aligned_to(p, elem_bytes(dtype)))
+    return fail(FP8_ERR_ALIGN, "%s: %s is not aligned to its elements", fn, what);
+  return FP8_OK;
+}
+
+int check_layernorm(const char* fn, int64_t rows, int64_t cols, int dtype, int param_dtype) {
+  if (rows < 0 || cols < 1)
+    return fail(FP8_ERR_SHAPE, "%s: needs rows >= 0 and cols >= 1 (got %lld x %lld)", fn,
+                (long long)rows, (long long)cols);
+  if (cols > fp8lin::kLayerNormMaxCols)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: %lld columns, the limit is %lld", fn, (long long)cols,
+                (long long)fp8lin::kLayerNormMaxCols);
+  if (rows >= ((int64_t)1 << 31))
+    return fail(FP8_ERR_UNSUPPORTED, "%s: 2^31 rows or more", fn);
+  if (int e = check_dtype(fn, dtype)) return e;
+  if (param_dtype != dtype && param_dtype != FP8_DT_F32)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: parameters must have the rows' dtype or be f32", fn);
+  return FP8_OK;
+}
+
+int check_moe_sizes(const char* fn, int64_t tokens, int32_t topk) {
+  if (tokens < 0) return fail(FP8_ERR_SHAPE, "%s: negative token count", fn);
+  if (topk < 1 || topk > fp8lin::kMoeMaxTopk)
+    return fail(FP8_ERR_SHAPE, "%s: topk=%d outside [1, %d]", fn, topk, fp8lin::kMoeMaxTopk);
+  if (tokens >= ((int64_t)1 << 31) || tokens * topk >= ((int64_t)1 << 31))
+    return fail(FP8_ERR_UNSUPPORTED, "%s: 2^31 token-expert pairs or more", fn);
+  return FP8_OK;
+}
+
+int check_experts(const char* fn, int32_t experts) {
+  if (experts < 1 || experts > fp8lin::kMoeMaxExperts)
+    return fail(FP8_ERR_SHAPE, "%s: experts=%d outside [1, %d]", fn, experts,
+                fp8lin::kMoeMaxExperts);
+  return FP8_OK;
+}
+
+int moe_rows(const char* fn, int64_t tokens, int32_t topk, int32_t experts, int32_t multiple,
+             int64_t* rows) {
+  if (int e = check_moe_sizes(fn, tokens, topk)) return e;
+  if (int e = check_experts(fn, experts)) return e;
+  if (multiple < 1) return fail(FP8_ERR_SHAPE, "%s: multiple=%d", fn, multiple);
+  const int64_t pairs = tokens * topk;
+  const int64_t used = pairs < experts ? pairs : experts;
+  const int64_t r = (pairs + used * (multiple - 1)) / multiple * multiple;
+  if (r >= ((int64_t)1 << 31)) return fail(FP8_ERR_UNSUPPORTED, "%s: 2^31 sorted rows or more", fn);
+  *rows = r;
+  return FP8_OK;
+}
+
+// Sizes and index tensors of the row exchanges.
+int check_exchange(const char* fn, int64_t tokens, int32_t topk, int64_t rows, int64_t cols,
+                   int dtype, const int32_t* slot, const int32_t* source, bool need_source) {
+  if (int e = check_moe_sizes(fn, tokens, topk)) return e;
+  if (rows < 0 || cols < 0) return fail(FP8_ERR_SHAPE, "%s: negative size", fn);
+  if (int e = check_dtype(fn, dtype)) return e;
+  const int64_t limit = (int64_t)1 << 24;
+  if (rows >= ((int64_t)1 << 31) || cols >= ((int64_t)1 << 30) ||
+      (tokens + rows) * ((cols * elem_bytes(dtype) + 2047) / 2048) >= limit ||
+      tokens + rows >= limit)
+    return fail(FP8_ERR_UNSUPPORTED,
+                "%s: (tokens + rows) * ceil(row bytes / 2048) must be below 2^24", fn);
+  if (tokens > 0 && !slot) return fail(FP8_ERR_NULL, "%s: slot is NULL", fn);
+  if (need_source && rows > 0 && !source) return fail(FP8_ERR_NULL, "%s: source is NULL", fn);
+  if (!aligned_to(slot, 4) || !aligned_to(source, 4))
+    return fail(FP8_ERR_ALIGN, "%s: slot and source must be 4-byte aligned", fn);
+  return FP8_OK;
+}
+
+int check_out(const char* fn, const char* what, const void* p, int64_t n, int64_t align) {
+  if (n > 0 && !p) return fail(FP8_ERR_NULL, "%s: %s is NULL", fn, what);
+  if (!aligned_to(p, align))
+    return fail(FP8_ERR_ALIGN, "%s: %s is not aligned to its elements", fn, what);
+  return FP8_OK;
+}
+
+int check_workspace(const char* fn, const void* p, int64_t have, int64_t need) {
+  if (need == 0) return FP8_OK;
+  if (!p) return fail(FP8_ERR_NULL, "%s: workspace is NULL, needs %lld bytes", fn, (long long)need);
+  if (have < need)
+    return fail(FP8_ERR_SHAPE, "%s: workspace of %lld bytes, needs %lld", fn, (long long)have,
+                (long long)need);
+  if (!aligned_to(p, 4)) return fail(FP8_ERR_ALIGN, "%s: workspace must be 4-byte aligned", fn);
+  return FP8_OK;
+}
+
+}  // namespace
+
+int fp8_layernorm_fwd(const void* x, int64_t ldx, const void* gamma, const void* beta,
+                      int64_t rows, int64_t cols, int dtype, int param_dtype, float eps, void* y,
+                      float* mean, float* rstd, void* stream) {
+  const char* fn = "fp8_layernorm_fwd";
+  if (int e = check_layernorm(fn, rows, cols, dtype, param_dtype)) return e;
+  if (!(eps >= 0.f) || eps > 3.402823466e38f)
+    return fail(FP8_ERR_SHAPE, "%s: eps must be finite and not negative", fn);
+  if (int e = check_rows(fn, "x", x, ldx, rows, cols, dtype)) return e;
+  if (int e = check_out(fn, "y", y, rows, elem_bytes(dtype))) return e;
+  if (x && x == y) return fail(FP8_ERR_UNSUPPORTED, "%s: y must not be x", fn);
+  if (!aligned_to(gamma, elem_bytes(param_dtype)) || !aligned_to(beta, elem_bytes(param_dtype)) ||
+      !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return fail(FP8_ERR_ALIGN, "%s: a parameter or statistic is not aligned to its elements", fn);
+  if (rows == 0) return ok();
+  fp8lin::LayerNormArgs a{};
+  a.x = x, a.ldx = ldx, a.gamma = gamma, a.beta = beta, a.rows = rows, a.cols = cols;
+  a.dtype = dtype, a.param_dtype = param_dtype, a.eps = eps, a.y = y, a.mean = mean, a.rstd = rstd;
+  return hip_status(fp8lin::launch_layernorm(a, false, as_stream(stream)), fn);
+}
+
+int fp8_layernorm_bwd_workspace(int64_t rows, int64_t cols, int64_t* bytes) {
+  const char* fn = "fp8_layernorm_bwd_workspace";
+  if (!bytes) return fail(FP8_ERR_NULL, "%s: bytes is NULL", fn);
+  if (int e = check_layernorm(fn, rows, cols, FP8_DT_F32, FP8_DT_F32)) return e;
+  *bytes = fp8lin::layernorm_bwd_workspace(rows, cols);
+  return ok();
+}
+
+int fp8_layernorm_bwd(const void* dy, int64_t lddy, const void* x, int64_t ldx, const float* mean,
+                      const float* rstd, const void* gamma, int64_t rows, int64_t cols, int dtype,
+                      int param_dtype, void* dx, void* dgamma, void* dbeta, void* workspace,
+                      int64_t workspace_bytes, void* stream) {
+  const char* fn = "fp8_layernorm_bwd";
+  if (int e = check_layernorm(fn, rows, cols, dtype, param_dtype)) return e;
+  if (int e = check_rows(fn, "dy", dy, lddy, rows, cols, dtype)) return e;
+  if (int e = check_rows(fn, "x", x, ldx, rows, cols, dtype)) return e;
+  if (rows > 0 && (!mean || !rstd)) return fail(FP8_ERR_NULL, "%s: mean or rstd is NULL", fn);
+  if (!aligned_to(mean, 4) || !aligned_to(rstd, 4) || !aligned_to(dx, elem_bytes(dtype)) ||
+      !aligned_to(gamma, elem_bytes(param_dtype)) || !aligned_to(dgamma, elem_bytes(param_dtype)) ||
+      !aligned_to(dbeta, elem_bytes(param_dtype)))
+    return fail(FP8_ERR_ALIGN, "%s: a tensor is not aligned to its elements", fn);
+  if (dx && (dx == x || dx == dy))
+    return fail(FP8_ERR_UNSUPPORTED, "%s: dx must not be an input", fn);
+  if (!dx && !dgamma && !dbeta) return ok();
+  if (rows == 0 && !dgamma && !dbeta) return ok();
+  const int64_t need = (dgamma || dbeta) ? fp8lin::layernorm_bwd_workspace(rows, cols) : 0;
+  if (int e = check_workspace(fn, workspace, workspace_bytes, need)) return e;
+  fp8lin::LayerNormArgs a{};
+  a.x = x, a.ldx = ldx, a.dy = dy, a.lddy = lddy, a.gamma = gamma, a.rows = rows, a.cols = cols;
+  a.dtype = dtype, a.param_dtype = param_dtype, a.y = dx, a.dgamma = dgamma, a.dbeta = dbeta;
+  a.mean = const_cast<float*>(mean), a.rstd = const_cast<float*>(rstd);
+  a.workspace = need ? static_cast<float*>(workspace) : nullptr;
+  return hip_status(fp8lin::launch_layernorm(a, true, as_stream(stream)), fn);
+}
+
+int fp8_moe_rows(int64_t tokens, int32_t topk, int32_t experts, int32_t multiple, int64_t* rows) {
+  const char* fn = "fp8_moe_rows";
+  if (!rows) return fail(FP8_ERR_NULL, "%s: rows is NULL", fn);
+  if (int e = moe_rows(fn, tokens, topk, experts, multiple, rows)) return e;
+  return ok();
+}
+
+int fp8_moe_sort_workspace(int64_t tokens, int32_t topk, int32_t experts, int64_t* bytes) {
+  const char* fn = "fp8_moe_sort_workspace";
+  if (!bytes) return fail(FP8_ERR_NULL, "%s: bytes is NULL", fn);
+  if (int e = check_moe_sizes(fn, tokens, topk)) return e;
+  if (int e = check_experts(fn, experts)) return e;
+  *bytes = fp8lin::moe_sort_workspace(tokens * topk, experts);
+  return ok();
+}
+
+int fp8_moe_sort(const void* expert_idx, int idx_bytes, int64_t tokens, int32_t topk,
+                 int32_t experts, int32_t multiple, int32_t* slot, int32_t* source,
+                 int32_t* counts, int32_t* offsets, void* workspace, int64_t workspace_bytes,
+                 void* stream) {
+  const char* fn = "fp8_moe_sort";
+  int64_t rows = 0;
+  if (int e = moe_rows(fn, tokens, topk, experts, multiple, &rows)) return e;
+  if (idx_bytes != 4 && idx_bytes != 8)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: expert indices of %d bytes (4 or 8)", fn, idx_bytes);
+  const int64_t pairs = tokens * topk;
+  if (int e = check_out(fn, "expert_idx", expert_idx, pairs, idx_bytes)) return e;
+  if (int e = check_out(fn, "slot", slot, pairs, 4)) return e;
+  if (int e = check_out(fn, "source", source, rows, 4)) return e;
+  if (int e = check_out(fn, "counts", counts, experts, 4)) return e;
+  if (int e = check_out(fn, "offsets", offsets, experts + 1, 4)) return e;
+  const int64_t need = fp8lin::moe_sort_workspace(pairs, experts);
+  if (int e = check_workspace(fn, workspace, workspace_bytes, need)) return e;
+  fp8lin::MoeSortArgs a{};
+  a.idx = expert_idx, a.idx_bytes = idx_bytes, a.pairs = pairs, a.rows = rows;
+  a.experts = experts, a.multiple = multiple, a.slot = slot, a.source = source;
+  a.counts = counts, a.offsets = offsets, a.workspace = static_cast<int32_t*>(workspace);
+  return hip_status(fp8lin::launch_moe_sort(a, as_stream(stream)), fn);
+}
+
+int fp8_moe_dispatch(const void* x, int64_t ldx, const int32_t* slot, const int32_t* source,
+                     int64_t tokens, int32_t topk, int64_t rows, int64_t cols, int dtype, void* xs,
+                     void* stream) {
+  const char* fn = "fp8_moe_dispatch";
+  if (int e = check_exchange(fn, tokens, topk, rows, cols, dtype, slot, source, true)) return e;
+  if (int e = check_rows(fn, "x", x, ldx, tokens, cols, dtype)) return e;
+  if (int e = check_out(fn, "xs", xs, rows * cols, elem_bytes(dtype))) return e;
+  if (rows * cols == 0) return ok();
+  if (x == xs) return fail(FP8_ERR_UNSUPPORTED, "%s: xs must not be x", fn);
+  fp8lin::MoeArgs a{};
+  a.x = x, a.ldx = ldx, a.slot = slot, a.source = source, a.tokens = tokens, a.topk = topk;
+  a.rows = rows, a.cols = cols, a.dtype = dtype, a.out = xs;
+  return hip_status(fp8lin::launch_moe_dispatch(a, as_stream(stream)), fn);
+}
+
+namespace {
+
+int combine(const char* fn, const char* in, const char* out, const void* ys, int64_t ldys,
+            const int32_t* slot, const float* weights, int64_t tokens, int32_t topk, int64_t rows,
+            int64_t cols, int dtype, void* y, void* stream) {
+  if (int e = check_exchange(fn, tokens, topk, rows, cols, dtype, slot, nullptr, false)) return e;
+  if (int e = check_rows(fn, in, ys, ldys, rows, cols, dtype)) return e;
+  if (int e = check_out(fn, out, y, tokens * cols, elem_bytes(dtype))) return e;
+  if (tokens * cols == 0) return ok();
+  if (ys == y) return fail(FP8_ERR_UNSUPPORTED, "%s: %s must not be %s", fn, out, in);
+  fp8lin::MoeArgs a{};
+  a.ys = ys, a.ldys = ldys, a.slot = slot, a.weights = weights, a.tokens = tokens, a.topk = topk;
+  a.rows = rows, a.cols = cols, a.dtype = dtype, a.out = y;
+  return hip_status(fp8lin::launch_moe_combine(a, as_stream(stream)), fn);
+}
+
+}  // namespace
+
+int fp8_moe_dispatch_bwd(const void* dxs, int64_t lddxs, const int32_t* slot, int64_t tokens,
+                         int32_t topk, int64_t rows, int64_t cols, int dtype, void* dx,
+                         void* stream) {
+  return combine("fp8_moe_dispatch_bwd", "dxs", "dx", dxs, lddxs, slot, nullptr, tokens, topk,
+                 rows, cols, dtype, dx, stream);
+}
+
+int fp8_moe_combine(const void* ys, int64_t ldys, const int32_t* slot, const float* weights,
+                    int64_t tokens, int32_t topk, int64_t rows, int64_t cols, int dtype, void* y,
+                    void* stream) {
+  const char* fn = "fp8_moe_combine";
+  if (tokens > 0 && !weights) return fail(FP8_ERR_NULL, "%s: weights is NULL", fn);
+  if (!aligned_to(weights, 4)) return fail(FP8_ERR_ALIGN, "%s: weights must be 4-byte aligned", fn);
+  return combine(fn, "ys", "y", ys, ldys, slot, weights, tokens, topk, rows, cols, dtype, y, stream);
+}
+
+int fp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ldys,
+                        const int32_t* slot, const int32_t* source, const float* weights,
+                        int64_t tokens, int32_t topk, int64_t rows, int64_t cols, int dtype,
+                        void* dys, float* dw, void* stream) {
+  const char* fn = "fp8_moe_combine_bwd";
+  if (int e = check_exchange(fn, tokens, topk, rows, cols, dtype, slot, source, true)) return e;
+  if (tokens > 0 && !weights) return fail(FP8_ERR_NULL, "%s: weights is NULL", fn);
+  if (!aligned_to(weights, 4)) return fail(FP8_ERR_ALIGN, "%s: weights must be 4-byte aligned", fn);
+  if (int e = check_rows(fn, "dy", dy, lddy, tokens, cols, dtype)) return e;
+  if (int e = check_rows(fn, "ys", ys, ldys, rows, cols, dtype)) return e;
+  if (int e = check_out(fn, "dys", dys, rows * cols, elem_bytes(dtype))) return e;
+  if (int e = check_out(fn, "dw", dw, tokens * topk, 4)) return e;
+  if (tokens == 0 && rows * cols == 0) return ok();
+  if (dys && (dys == dy || dys == ys))
+    return fail(FP8_ERR_UNSUPPORTED, "%s: dys must not be an input", fn);
+  fp8lin::MoeArgs a{};
+  a.x = dy, a.ldx = lddy, a.ys = ys, a.ldys = ldys, a.slot = slot, a.source = source;
+  a.weights = weights, a.tokens = tokens, a.topk = topk, a.rows = rows, a.cols = cols;
+  a.dtype = dtype, a.out = dys, a.dw = dw;
+  return hip_status(fp8lin::launch_moe_combine_bwd(a, as_stream(stream)), fn);
+}
+
 }  // extern "C"

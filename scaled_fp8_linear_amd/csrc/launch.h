@@ -70,4 +70,47 @@ hipError_t launch_bias_rows(const uint16_t* bias, uint16_t* D, int64_t M, int64_
 hipError_t launch_bias_grad(const uint16_t* g, int64_t rows, int64_t cols, int64_t rows_valid,
                             uint16_t* db, hipStream_t s);
 
+// Layer norm over rows of `cols` elements (1 .. kLayerNormMaxCols); dtype and param_dtype
+// are rows.h's DType, param_dtype either dtype or float32. Forward: y, mean, rstd out (mean
+// and rstd may be null). Backward: y is dx (may be null), dgamma and dbeta out (each may be
+// null), workspace of layernorm_bwd_workspace() bytes (null if that is 0).
+constexpr int64_t kLayerNormMaxCols = 32768;
+struct LayerNormArgs {
+  const void *x, *dy, *gamma, *beta;
+  int64_t ldx, lddy, rows, cols;
+  int dtype, param_dtype;
+  float eps;
+  void *y, *dgamma, *dbeta;
+  float *mean, *rstd, *workspace;
+};
+int64_t layernorm_bwd_workspace(int64_t rows, int64_t cols);
+hipError_t launch_layernorm(const LayerNormArgs& a, bool backward, hipStream_t s);
+
+// Expert routing. kMoeMaxExperts: one counter per expert and wave in LDS.
+constexpr int32_t kMoeMaxExperts = 512, kMoeMaxTopk = 64;
+struct MoeSortArgs {
+  const void* idx;
+  int idx_bytes;                       // 4 or 8
+  int64_t pairs, rows;
+  int32_t experts, multiple;
+  int32_t *slot, *source, *counts, *offsets, *workspace;
+};
+int64_t moe_sort_workspace(int64_t pairs, int32_t experts);
+hipError_t launch_moe_sort(const MoeSortArgs& a, hipStream_t s);
+
+struct MoeArgs {
+  const void *x, *ys;                  // token rows [tokens, cols], sorted rows [rows, cols]
+  int64_t ldx, ldys;
+  const int32_t *slot, *source;
+  const float* weights;                // null: 1
+  int64_t tokens, rows, cols;
+  int32_t topk;
+  int dtype;
+  void* out;
+  float* dw;
+};
+hipError_t launch_moe_dispatch(const MoeArgs& a, hipStream_t s);      // x -> out [rows, cols]
+hipError_t launch_moe_combine(const MoeArgs& a, hipStream_t s);       // ys -> out [tokens, cols]
+hipError_t launch_moe_combine_bwd(const MoeArgs& a, hipStream_t s);   // x = dy -> out, dw
+
 }  // namespace fp8lin
