@@ -42,10 +42,32 @@ __device__ __forceinline__ void ld_params(const P* p, int c, int cols, float fil
   }
 }
 
-template <int LPR, int BLOCK> struct Group {
-  static constexpr int kRows = BLOCK / LPR;             // rows in flight per workgroup
-  static constexpr int kWaves = LPR > 64 ? LPR / 64 : 1;  // waves of a row
-};
+// Four partial sums; a workspace is aligned to its floats only.
+typedef float f32x4_t __attribute__((ext_vector_type(4)));
+typedef float sums_t __attribute__((ext_vector_type(4), aligned(4)));
+
+// The lane group (row of a turn) of this thread; the same for a whole wave where a row takes
+// one or more, so that row addresses are scalar.
+template <int LPR>
+__device__ __forceinline__ int row_group() {
+  const int g = threadIdx.x / LPR;
+  return LPR >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
+}
+
+// The row of a group in the turn that starts at r0. A group past the last row works on that
+// row and stores nothing, so that every group takes the same number of turns and the barriers
+// in a row's sums always meet.
+__device__ __forceinline__ int64_t turn_row(int64_t r0, int group, int64_t rows) {
+  return r0 + group < rows ? r0 + group : rows - 1;
+}
+
+// This lane's pieces of a row, not yet cut at its end.
+template <typename T, int LPR, int NV>
+__device__ __forceinline__ void ld_rows(const T* row, int lane, int cols, piece_t (&p)[NV]) {
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    p[v] = ld_raw<T, LPR == 16>(row, (v * LPR + lane) * Piece<T>::N, cols);
+}
 
 // Sum over the LPR lanes of a row. Rows of several waves meet in LDS (`part`, one float per
 // wave of the workgroup); the caller alternates buffers so that one barrier per sum is
@@ -55,19 +77,16 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   v = lanes_sum<(LPR < 64 ? LPR : 64)>(v);
   if constexpr (LPR > 64) {
     constexpr int W = LPR / 64;
-    const int wave = threadIdx.x / 64;
+    const int wave = row_group<64>();
     if (threadIdx.x % 64 == 0) part[wave] = v;
     __syncthreads();
-    const int w0 = wave / W * W;
-    v = 0.f;
-#pragma unroll
-    for (int i = 0; i < W; ++i) v += part[w0 + i];
+    v = lanes_sum<W>(part[wave / W * W + threadIdx.x % W]);
   }
   return v;
 }
 
 // LPR lanes own a row; lane l holds the pieces l, l + LPR, ... (EPT elements). A workgroup
-// walks the rows with the grid's stride.
+// walks the rows with the grid's stride and loads the next row while it works on this one.
 template <typename T, typename P, int LPR, int EPT, int BLOCK>
 __global__ void __launch_bounds__(BLOCK)
 layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__ gamma,
@@ -75,30 +94,39 @@ layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__
                      T* __restrict__ y, float* __restrict__ mean_out,
                      float* __restrict__ rstd_out) {
   constexpr int N = Piece<T>::N, NV = EPT / N, ROWS = BLOCK / LPR;
+  // gamma, beta and the next row stay in registers beside the row up to 16 elements a lane
+  constexpr bool kAhead = EPT <= 16;
   __shared__ float part[2][BLOCK / 64];
-  const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
-  const float inv_n = (float)cols;
-  float gm[NV][N], bt[NV][N];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
-    ld_params(beta, (v * LPR + lane) * N, cols, 0.f, bt[v]);
-  }
+  const int lane = threadIdx.x % LPR, group = row_group<LPR>();
+  const float fcols = (float)cols;
   const int64_t step = (int64_t)gridDim.x * ROWS;
-  // every group takes the same number of turns, so the barriers in row_sum always meet
+  piece_t cur[NV], next[NV];
+  if (kAhead)
+    ld_rows<T, LPR, NV>(x + turn_row((int64_t)blockIdx.x * ROWS, group, rows) * ldx, lane, cols,
+                        cur);
+  float gm[NV][N], bt[NV][N];
+  if constexpr (kAhead) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+      ld_params(beta, (v * LPR + lane) * N, cols, 0.f, bt[v]);
+    }
+  }
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < rows; r0 += step) {
+    if (!kAhead)
+      ld_rows<T, LPR, NV>(x + turn_row(r0, group, rows) * ldx, lane, cols, cur);
+    else if (r0 + step < rows)
+      ld_rows<T, LPR, NV>(x + turn_row(r0 + step, group, rows) * ldx, lane, cols, next);
     const int64_t r = r0 + group;
-    const bool live = r < rows;
     float f[NV][N];
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const piece_t p = live ? ld_row(x + r * ldx, (v * LPR + lane) * N, cols) : piece_t{0, 0, 0, 0};
-      unpack(p, f[v], T{});
+      unpack(cut<T>(cur[v], (v * LPR + lane) * N, cols), f[v], T{});
 #pragma unroll
       for (int i = 0; i < N; ++i) s += f[v][i];
     }
-    const float mean = row_sum<LPR>(s, part[0]) / inv_n;
+    const float mean = row_sum<LPR>(s, part[0]) / fcols;
     float q = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
@@ -106,16 +134,29 @@ layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         f[v][i] -= mean;
-        if (c + i < cols) q += f[v][i] * f[v][i];
+        const float d = c + i < cols ? f[v][i] : 0.f;
+        q = __builtin_fmaf(d, d, q);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<LPR>(q, part[1]) / inv_n + eps);
-    if (live) {
+    const float rstd = 1.0f / sqrtf(row_sum<LPR>(q, part[1]) / fcols + eps);
+    if (kAhead) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        arrived(next[v]);
+        cur[v] = next[v];
+      }
+    }
+    if (r < rows) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float o[N];
+        if constexpr (!kAhead) {
+          __builtin_amdgcn_sched_barrier(0);
+          ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+          ld_params(beta, (v * LPR + lane) * N, cols, 0.f, bt[v]);
+        }
 #pragma unroll
-        for (int i = 0; i < N; ++i) o[i] = f[v][i] * rstd * gm[v][i] + bt[v][i];
+        for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(f[v][i] * rstd, gm[v][i], bt[v][i]);
         st_row(y + r * cols, (v * LPR + lane) * N, cols, pack(o, T{}));
       }
       if (lane == 0) {
@@ -126,91 +167,156 @@ layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__
   }
 }
 
-// The gradient in one pass over dy and x. Lanes own columns as in the forward, so each also
-// sums dy xh and dy of its columns over the workgroup's rows, in registers; at the end the
-// workgroup's row groups are added in LDS in group order and written as one row of partial
-// sums, part[which][block][cols], which layernorm_bwd_params_kernel adds in block order. A
-// single workgroup writes dgamma and dbeta itself. Every order is fixed, so results repeat.
+// The gradient in one pass over dy and x, the next row loaded while this one is worked on.
+// Lanes own columns as in the forward, so each also sums dy xh and dy of its columns over the
+// workgroup's rows, in registers; at the end the workgroup's row groups are added in LDS in
+// group order and written as one row of partial sums, part[which][block][part_ld], which
+// layernorm_bwd_params_kernel adds in a fixed order. A single workgroup writes dgamma and
+// dbeta itself. Every order is fixed, so results repeat.
+//
+// A wave has 128 registers (16 waves a compute unit). What does not fit beside the two sums:
+// gamma (then in LDS), the next row (then not loaded ahead), and for the widest float32 rows
+// this row itself (then read again, from the cache, for dx).
+template <typename T, int EPT> struct BwdFit {
+  static constexpr int kRow = 2 * EPT * (int)sizeof(T) / 4, kSums = 2 * EPT;
+  static constexpr bool kHold = kRow + kSums < 96;
+  static constexpr bool kAhead = 2 * kRow + kSums <= 96;
+  static constexpr bool kGammaLds = (kAhead ? 2 : 1) * kRow + kSums + EPT > 96;
+};
+
 template <typename T, typename P, int LPR, int EPT, int BLOCK>
-__global__ void __launch_bounds__(BLOCK)
+__global__ void __launch_bounds__(BLOCK, 4)
 layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
                      const float* __restrict__ mean, const float* __restrict__ rstd,
                      const P* __restrict__ gamma, int64_t rows, int cols, T* __restrict__ dx,
-                     P* __restrict__ dgamma, P* __restrict__ dbeta, float* __restrict__ part) {
+                     P* __restrict__ dgamma, P* __restrict__ dbeta, float* __restrict__ part,
+                     int part_ld) {
+  using Fit = BwdFit<T, EPT>;
   constexpr int N = Piece<T>::N, NV = EPT / N, ROWS = BLOCK / LPR, WAVES = BLOCK / 64;
+  constexpr bool kGammaLds = Fit::kGammaLds, kHold = Fit::kHold, kAhead = Fit::kAhead;
   __shared__ float red[2][2][WAVES];
-  __shared__ float fold[ROWS > 1 ? BLOCK * EPT : 1];
-  const int lane = threadIdx.x % LPR, group = threadIdx.x / LPR;
+  constexpr int kFold = ROWS > 1 ? BLOCK * EPT : 1;
+  __shared__ __attribute__((aligned(16))) float fold[kGammaLds && kFold < LPR * EPT ? LPR * EPT : kFold];
+  const int lane = threadIdx.x % LPR, group = row_group<LPR>();
   const float fcols = (float)cols;
-  float gm[NV][N], ag[NV][N], ab[NV][N];
+  const int64_t step = (int64_t)gridDim.x * ROWS;
+  const bool ragged = cols % N != 0;
+  piece_t cx[NV], cd[NV], nx[NV], nd[NV];      // this row of x and dy, and the next
+  float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
+  if (kAhead && (int64_t)blockIdx.x * ROWS < rows) {
+    const int64_t r = turn_row((int64_t)blockIdx.x * ROWS, group, rows);
+    ld_rows<T, LPR, NV>(x + r * ldx, lane, cols, cx);
+    ld_rows<T, LPR, NV>(dy + r * lddy, lane, cols, cd);
+    mu = mean[r], rs = rstd[r];
+  }
+  float gm[kGammaLds ? 1 : NV][N], ag[NV][N], ab[NV][N];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+    if constexpr (kGammaLds) {
+      float g[N];
+      ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, g);
+      if (group == 0)
+#pragma unroll
+        for (int i = 0; i < N; ++i) fold[(v * LPR + lane) * N + i] = g[i];
+    } else {
+      ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) ag[v][i] = ab[v][i] = 0.f;
   }
-  const int64_t step = (int64_t)gridDim.x * ROWS;
+  if (kGammaLds && ROWS > 1) __syncthreads();     // one row group's lanes read their own
+  auto gamma_of = [&](int v, int i) {
+    if constexpr (kGammaLds) return fold[(v * LPR + lane) * N + i];
+    else return gm[v][i];
+  };
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < rows; r0 += step, turn ^= 1) {
     const int64_t r = r0 + group;
     const bool live = r < rows;
-    piece_t px[NV], pd[NV];
-    float mu = 0.f, rs = 0.f;
-    if (live) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        px[v] = ld_row(x + r * ldx, (v * LPR + lane) * N, cols);
-        pd[v] = ld_row(dy + r * lddy, (v * LPR + lane) * N, cols);
+    const int64_t q = turn_row(kAhead ? r0 + step : r0, group, rows);
+    if (!kAhead) {
+      if constexpr (kHold) {
+        ld_rows<T, LPR, NV>(x + q * ldx, lane, cols, cx);
+        ld_rows<T, LPR, NV>(dy + q * lddy, lane, cols, cd);
       }
-      mu = mean[r];
-      rs = rstd[r];
-    } else {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) px[v] = pd[v] = piece_t{0, 0, 0, 0};
+      mu = mean[q], rs = rstd[q];
+    } else if (r0 + step < rows) {
+      ld_rows<T, LPR, NV>(x + q * ldx, lane, cols, nx);
+      ld_rows<T, LPR, NV>(dy + q * lddy, lane, cols, nd);
+      nmu = mean[q], nrs = rstd[q];
     }
+    // a group past the last row takes its turn (the barriers must meet) with dy = 0
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      float fx[N], fd[N];
-      unpack(px[v], fx, T{});
-      unpack(pd[v], fd, T{});
       const int c = (v * LPR + lane) * N;
+      float fx[N], fd[N];
+      if constexpr (!kHold) {
+        cx[v] = ld_raw<T, false>(x + q * ldx, c, cols);
+        cd[v] = ld_raw<T, false>(dy + q * lddy, c, cols);
+      }
+      if (ragged) {
+        cx[v] = cut<T>(cx[v], c, cols);
+        cd[v] = cut<T>(cd[v], c, cols);
+      }
+      // past the row dy is 0 and x is some of the row's own values: nothing is added, and a
+      // NaN there is one that the row has anyway
+      if (!live || c >= cols) cd[v] = piece_t{0, 0, 0, 0};
+      unpack(cx[v], fx, T{});
+      unpack(cd[v], fd, T{});
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        // columns past the row hold dy = 0 and x = 0; an infinite mean must not reach them
-        const float xh = c + i < cols ? (fx[i] - mu) * rs : 0.f;
-        const float g = fd[i] * gm[v][i];
+        const float xh = (fx[i] - mu) * rs;
+        const float g = fd[i] * gamma_of(v, i);
         s1 += g;
-        s2 += g * xh;
-        ag[v][i] += fd[i] * xh;
-        ab[v][i] += fd[i];
+        s2 = __builtin_fmaf(g, xh, s2);
       }
+      if constexpr (!kHold || kGammaLds) __builtin_amdgcn_sched_barrier(0);
     }
     s1 = lanes_sum<(LPR < 64 ? LPR : 64)>(s1);
     s2 = lanes_sum<(LPR < 64 ? LPR : 64)>(s2);
     if constexpr (LPR > 64) {
       constexpr int W = LPR / 64;
-      const int wave = threadIdx.x / 64, w0 = wave / W * W;
+      const int wave = row_group<64>(), w = wave / W * W + threadIdx.x % W;
       if (threadIdx.x % 64 == 0) { red[turn][0][wave] = s1; red[turn][1][wave] = s2; }
       __syncthreads();
-      s1 = s2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < W; ++i) { s1 += red[turn][0][w0 + i]; s2 += red[turn][1][w0 + i]; }
+      s1 = lanes_sum<W>(red[turn][0][w]);
+      s2 = lanes_sum<W>(red[turn][1][w]);
     }
-    if (live && dx) {
-      const float m1 = s1 / fcols, m2 = s2 / fcols;
+    if (kAhead) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        float fx[N], fd[N], o[N];
-        unpack(px[v], fx, T{});
-        unpack(pd[v], fd, T{});
+      for (int v = 0; v < NV; ++v) { arrived(nx[v]); arrived(nd[v]); }
+    }
+    const float m1 = s1 / fcols, m2 = s2 / fcols;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const float xh = (fx[i] - mu) * rs;
-          o[i] = rs * (fd[i] * gm[v][i] - m1 - xh * m2);
-        }
-        st_row(dx + r * cols, (v * LPR + lane) * N, cols, pack(o, T{}));
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * LPR + lane) * N;
+      float fx[N], fd[N], o[N];
+      if constexpr (kHold) {
+        // from the 16 bytes again: the floats of the first sums would not fit
+        arrived(cx[v]);
+        arrived(cd[v]);
+      } else {
+        cx[v] = cut<T>(ld_raw<T, false>(x + q * ldx, c, cols), c, cols);
+        cd[v] = cut<T>(ld_raw<T, false>(dy + q * lddy, c, cols), c, cols);
+        if (!live) cd[v] = piece_t{0, 0, 0, 0};
       }
+      unpack(cx[v], fx, T{});
+      unpack(cd[v], fd, T{});
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float xh = (fx[i] - mu) * rs;
+        o[i] = rs * __builtin_fmaf(-xh, m2, __builtin_fmaf(fd[i], gamma_of(v, i), -m1));
+        ag[v][i] = __builtin_fmaf(fd[i], xh, ag[v][i]);
+        ab[v][i] += fd[i];
+      }
+      if (live && dx) st_row(dx + r * cols, c, cols, pack(o, T{}));
+      if constexpr (!kHold || kGammaLds) __builtin_amdgcn_sched_barrier(0);
+    }
+    if (kAhead) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v) cx[v] = nx[v], cd[v] = nd[v];
+      mu = nmu, rs = nrs;
     }
   }
   if (!dgamma && !dbeta) return;
@@ -219,67 +325,75 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
     P* out = which == 0 ? dgamma : dbeta;
     if (!out) continue;
     float (&acc)[NV][N] = which == 0 ? ag : ab;
+    float* dst = part ? part + ((int64_t)which * gridDim.x + blockIdx.x) * part_ld : nullptr;
     if constexpr (ROWS > 1) {
       __syncthreads();
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < N; ++i) fold[(group * NV + v) * (LPR * N) + i * LPR + lane] = acc[v][i];
+        for (int i = 0; i < N; i += 4)
+          *reinterpret_cast<f32x4_t*>(&fold[(group * NV * LPR + v * LPR + lane) * N + i]) =
+              f32x4_t{acc[v][i], acc[v][i + 1], acc[v][i + 2], acc[v][i + 3]};
       __syncthreads();
-      if (group == 0) {
+      for (int c = threadIdx.x; c < cols; c += BLOCK) {
+        float s = fold[c];
 #pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            float s = acc[v][i];
-            for (int k = 1; k < ROWS; ++k) s += fold[(k * NV + v) * (LPR * N) + i * LPR + lane];
-            acc[v][i] = s;
-          }
+        for (int k = 1; k < ROWS; ++k) s += fold[k * LPR * EPT + c];
+        if (dst) dst[c] = s;
+        else out[c] = from_f32<P>(s);
       }
-    }
-    if (group == 0) {
-      float* dst = part ? part + ((int64_t)which * gridDim.x + blockIdx.x) * cols : nullptr;
+    } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < N; i += 4) {
           const int c = (v * LPR + lane) * N + i;
-          if (c < cols) {
-            if (dst) dst[c] = acc[v][i];
-            else out[c] = from_f32<P>(acc[v][i]);
+          if (dst) {                       // part_ld is cols rounded up to 4
+            if (c < cols)
+              *reinterpret_cast<sums_t*>(dst + c) =
+                  sums_t{acc[v][i], acc[v][i + 1], acc[v][i + 2], acc[v][i + 3]};
+          } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (c + k < cols) out[c + k] = from_f32<P>(acc[v][i + k]);
           }
         }
     }
   }
 }
 
-// out[c] = sum over the blocks of part[which][block][c]: 64 columns a workgroup, 16 lanes of
-// rows per column, each adding its blocks in order; the 16 sums are then added in order.
+// out[c] = sum over the blocks of part[which][block][c]. 16 lanes take 64 columns, 64 such
+// lane groups the blocks k, k + 64, ...; their sums are then added in order.
+constexpr int kParamsRows = 64;
 template <typename P>
 __global__ void __launch_bounds__(1024)
-layernorm_bwd_params_kernel(const float* __restrict__ part, int blocks, int cols,
+layernorm_bwd_params_kernel(const float* __restrict__ part, int blocks, int cols, int part_ld,
                             P* __restrict__ dgamma, P* __restrict__ dbeta) {
-  __shared__ float s[16][64];
+  __shared__ f32x4_t s[kParamsRows][16];
   P* out = blockIdx.y == 0 ? dgamma : dbeta;
   if (!out) return;
-  const int cl = threadIdx.x % 64, rl = threadIdx.x / 64;
-  const int c = blockIdx.x * 64 + cl;
-  const float* p = part + (int64_t)blockIdx.y * blocks * cols;
-  float v = 0.f;
-  if (c < cols)
-    for (int b = rl; b < blocks; b += 16) v += p[(int64_t)b * cols + c];
-  s[rl][cl] = v;
+  const int cl = threadIdx.x % 16, rl = threadIdx.x / 16;
+  const int c = blockIdx.x * 64 + cl * 4;
+  const float* p = part + (int64_t)blockIdx.y * blocks * part_ld;
+  f32x4_t a = {0.f, 0.f, 0.f, 0.f};
+  if (c < cols) {
+#pragma unroll 4
+    for (int b = rl; b < blocks; b += kParamsRows)
+      a += *reinterpret_cast<const sums_t*>(p + (int64_t)b * part_ld + c);
+  }
+  s[rl][cl] = a;
   __syncthreads();
-  if (rl == 0 && c < cols) {
+  if (threadIdx.x < 64 && blockIdx.x * 64 + (int)threadIdx.x < cols) {
+    const float* col = reinterpret_cast<const float*>(s) + threadIdx.x;
     float t = 0.f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) t += s[i][cl];
-    out[c] = from_f32<P>(t);
+#pragma unroll 16
+    for (int i = 0; i < kParamsRows; ++i) t += col[i * 64];
+    out[blockIdx.x * 64 + threadIdx.x] = from_f32<P>(t);
   }
 }
 
 constexpr int kFwdBlock = 256, kBwdBlock = 512;
-constexpr int64_t kFwdGrid = 256 * 8, kBwdGrid = 512;
+constexpr int64_t kFwdGrid = 256 * 8, kBwdThreads = 256 * 1024;
 
 constexpr int block_of(int lpr, int block) { return lpr > block ? lpr : block; }
 
@@ -298,10 +412,10 @@ Shape row_shape(int64_t cols) {
 
 int64_t bwd_blocks(int64_t rows, int64_t cols) {
   const int lpr = row_shape(cols).lpr;
-  const int64_t per = block_of(lpr, kBwdBlock) / lpr;
-  const int64_t want = (rows + per - 1) / per;
+  const int block = block_of(lpr, kBwdBlock);
+  const int64_t per = block / lpr, want = (rows + per - 1) / per;
   if (want <= 4) return 1;
-  return std::min(want, kBwdGrid);
+  return std::min(want, kBwdThreads / block);
 }
 
 template <typename T, typename P, int LPR, int EPT>
@@ -320,16 +434,17 @@ hipError_t bwd(const LayerNormArgs& a, hipStream_t s) {
   constexpr int B = block_of(LPR, kBwdBlock);
   const int64_t blocks = bwd_blocks(a.rows, a.cols);
   float* part = blocks > 1 ? a.workspace : nullptr;
+  const int part_ld = (int)((a.cols + 3) / 4 * 4);
   hipLaunchKernelGGL((layernorm_bwd_kernel<T, P, LPR, EPT, B>), dim3((unsigned)blocks), dim3(B), 0,
                      s, static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx,
                      a.mean, a.rstd, static_cast<const P*>(a.gamma), a.rows, (int)a.cols,
                      static_cast<T*>(a.y), static_cast<P*>(a.dgamma), static_cast<P*>(a.dbeta),
-                     part);
+                     part, part_ld);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !part || (!a.dgamma && !a.dbeta)) return e;
   hipLaunchKernelGGL((layernorm_bwd_params_kernel<P>), dim3((unsigned)((a.cols + 63) / 64), 2),
-                     dim3(1024), 0, s, part, (int)blocks, (int)a.cols, static_cast<P*>(a.dgamma),
-                     static_cast<P*>(a.dbeta));
+                     dim3(1024), 0, s, part, (int)blocks, (int)a.cols, part_ld,
+                     static_cast<P*>(a.dgamma), static_cast<P*>(a.dbeta));
   return hipGetLastError();
 }
 
@@ -354,7 +469,7 @@ hipError_t by_shape(const LayerNormArgs& a, bool backward, hipStream_t s) {
 
 int64_t layernorm_bwd_workspace(int64_t rows, int64_t cols) {
   const int64_t b = bwd_blocks(rows, cols);
-  return b > 1 ? 2 * b * cols * (int64_t)sizeof(float) : 0;
+  return b > 1 ? 2 * b * ((cols + 3) / 4 * 4) * (int64_t)sizeof(float) : 0;
 }
 
 hipError_t launch_layernorm(const LayerNormArgs& a, bool backward, hipStream_t s) {

@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.h"
 
 namespace fp8lin {
@@ -19,11 +21,24 @@ struct F16 { uint16_t u; };
 typedef unsigned piece_t __attribute__((ext_vector_type(4)));
 typedef unsigned piece_any_t __attribute__((ext_vector_type(4), aligned(2)));
 
+typedef unsigned half_piece_any_t __attribute__((ext_vector_type(2), aligned(2)));
+typedef unsigned dword_any_t __attribute__((aligned(2)));
+
 __device__ __forceinline__ piece_t ld_piece(const void* p) {
   return *reinterpret_cast<const piece_any_t*>(p);
 }
 __device__ __forceinline__ void st_piece(void* p, piece_t v) {
   *reinterpret_cast<piece_any_t*>(p) = v;
+}
+
+// row + c for a column 0 <= c < 2^30. Where `row` is the same for a whole wave this is a
+// scalar base and a 32-bit lane offset, which the load and store instructions add up.
+template <typename T>
+__device__ __forceinline__ T* elem_at(T* row, int c) {
+  using Byte = std::conditional_t<std::is_const<T>::value, const char, char>;
+  uint32_t off = (uint32_t)c * (uint32_t)sizeof(T);
+  asm volatile("" : "+v"(off));      // else loops keep the offset widened to 64 bits
+  return reinterpret_cast<T*>(reinterpret_cast<Byte*>(row) + off);
 }
 
 typedef _Float16 fp8lin_f16x2 __attribute__((ext_vector_type(2)));
@@ -87,50 +102,98 @@ __device__ __forceinline__ piece_t pack(const float (&f)[4], float) {
   return v;
 }
 
-// The piece at column c of a row of `cols` elements: whole, cut off at the row's end (the
-// missing elements read as 0), or empty. Nothing past the row is touched.
-template <typename T>
-__device__ __forceinline__ piece_t ld_row(const T* row, int c, int cols) {
+// The piece at column c of a row of `cols` elements, in two steps, so that a kernel can have
+// several loads in flight: ld_raw issues one 16-byte load (of the row's last 16 bytes where
+// the piece is cut off by the row's end or lies past it), and cut moves a cut-off piece's
+// elements down and sets what is past the row to 0. Nothing outside the row is touched; rows
+// shorter than a piece (kShort: they may be) are read element by element.
+template <typename T, bool kShort = true>
+__device__ __forceinline__ piece_t ld_raw(const T* row, int c, int cols) {
   constexpr int N = Piece<T>::N;
-  if (c + N <= cols) return ld_piece(row + c);
+  if (!kShort || cols >= N) return ld_piece(elem_at(row, c + N <= cols ? c : cols - N));
   piece_t v = {0u, 0u, 0u, 0u};
-  if (c < cols) {
+  if (c == 0) {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (c + i < cols) v[i] = __builtin_bit_cast(uint32_t, row[c + i]);
+        if (i < cols) v[i] = __builtin_bit_cast(uint32_t, row[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i)
-        if (c + i < cols) v[i / 2] |= (uint32_t)row[c + i].u << (16 * (i & 1));
+        if (i < cols) v[i / 2] |= (uint32_t)row[i].u << (16 * (i & 1));
     }
   }
   return v;
 }
 template <typename T>
+__device__ __forceinline__ piece_t cut(piece_t v, int c, int cols) {
+  constexpr int N = Piece<T>::N;
+  if (c + N <= cols || cols < N) return v;
+  const int past = (c + N - cols) * (int)sizeof(T);        // bytes past the row's end
+  if (past >= 16) return piece_t{0u, 0u, 0u, 0u};
+  if (past & 8) v = piece_t{v[2], v[3], 0u, 0u};
+  if (past & 4) v = piece_t{v[1], v[2], v[3], 0u};
+  if constexpr (sizeof(T) == 2) {
+    if (past & 2)
+      v = piece_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16,
+                  v[3] >> 16};
+  }
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ piece_t ld_row(const T* row, int c, int cols) {
+  return cut<T>(ld_raw(row, c, cols), c, cols);
+}
+template <typename T>
 __device__ __forceinline__ void st_row(T* row, int c, int cols, piece_t v) {
   constexpr int N = Piece<T>::N;
+  T* p = elem_at(row, c);
   if (c + N <= cols) {
-    st_piece(row + c, v);
-  } else if (c < cols) {
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (c + i < cols) reinterpret_cast<uint32_t*>(row)[c + i] = v[i];
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (c + i < cols) row[c + i].u = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    st_piece(p, v);
+  } else if (c < cols) {                     // 8, 4 and 2 bytes of what is left
+    const int left = (cols - c) * (int)sizeof(T);
+    if (left & 8) {
+      *reinterpret_cast<half_piece_any_t*>(p) = half_piece_any_t{v[0], v[1]};
+      v[0] = v[2], v[1] = v[3];
+      p = elem_at(p, 8 / (int)sizeof(T));
     }
+    if (left & 4) {
+      *reinterpret_cast<dword_any_t*>(p) = v[0];
+      v[0] = v[1];
+      p = elem_at(p, 4 / (int)sizeof(T));
+    }
+    if constexpr (sizeof(T) == 2)
+      if (left & 2) *reinterpret_cast<uint16_t*>(p) = (uint16_t)v[0];
   }
 }
 
+// Loads into v have arrived here. Placed before a row's stores, it keeps the wait for a
+// prefetched row from also waiting for those stores (both count down one counter).
+__device__ __forceinline__ void arrived(piece_t& v) { asm volatile("" : "+v"(v)); }
+
 // Sum over groups of LANES consecutive lanes (a power of two, at most 64): every lane gets
-// the same value, added in the same order on every run.
+// the same value, added in the same order on every run. Lanes are paired by DPP within 16 and
+// by the row swaps beyond, which need neither LDS nor index registers.
+template <int CTRL> __device__ __forceinline__ float dpp(float v) {
+  return __int_as_float(
+      __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
-#pragma unroll
-  for (int off = LANES / 2; off > 0; off >>= 1) v += __shfl_xor(v, off, 64);
+  if constexpr (LANES >= 2) v += dpp<0xB1>(v);        // quad_perm 1,0,3,2
+  if constexpr (LANES >= 4) v += dpp<0x4E>(v);        // quad_perm 2,3,0,1
+  if constexpr (LANES >= 8) v += dpp<0x141>(v);       // mirror of each 8 lanes
+  if constexpr (LANES >= 16) v += dpp<0x140>(v);      // mirror of each 16 lanes
+  if constexpr (LANES >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  if constexpr (LANES >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false,
+                                                    false);
+    v = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
   return v;
 }
 
