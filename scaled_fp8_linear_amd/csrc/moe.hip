@@ -26,9 +26,14 @@ namespace {
 
 // ------------------------------------------------------------------------------ sort
 
+// A workgroup ranks up to kSortBlock * S pairs, S to a lane, in registers. Up to kSortOne
+// pairs one workgroup does it all in one launch; above, chunks of kSortChunk pairs are counted
+// first, and every workgroup adds up the counts of all; above kSortDirect of those, chunks of
+// kSortLong, whose counts a launch between turns into starts.
 constexpr int kSortBlock = 1024, kSortWaves = kSortBlock / 64;
-constexpr int64_t kSortChunk = 16384;     // pairs per workgroup, up to kSortGrid workgroups
-constexpr int64_t kSortGrid = 256;
+constexpr int64_t kSortOne = 16 * kSortBlock, kSortChunk = 4 * kSortBlock;
+constexpr int64_t kSortLong = 16 * kSortBlock, kSortDirect = 64;
+constexpr int kSortShares = 16;
 
 __device__ __forceinline__ int expert_of(int32_t v, int experts) {
   return v >= 0 && v < experts ? v : -1;
@@ -37,69 +42,143 @@ __device__ __forceinline__ int expert_of(int64_t v, int experts) {
   return v >= 0 && v < experts ? (int)v : -1;
 }
 
-// Pairs [p0, p1) of workgroup b; wave w of it walks [w0, w1), 64 pairs a step.
-struct Span { int64_t p0, p1; };
-__device__ __forceinline__ Span wave_span(int64_t pairs, int64_t chunk) {
-  const int64_t per = chunk / kSortWaves;                 // chunk is a multiple of 64 * waves
-  const int64_t a = (int64_t)blockIdx.x * chunk + (int64_t)(threadIdx.x / 64) * per;
-  const int64_t b = a + per;
-  return {a < pairs ? a : pairs, b < pairs ? b : pairs};
+__device__ __forceinline__ int wave_index() {
+  return __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
 }
 
-// Count this wave's pairs by expert into cnt[experts] (LDS, this wave's own).
-template <typename I>
-__device__ __forceinline__ void count_span(const I* idx, Span sp, int experts, int* cnt) {
+// The experts of this lane's S pairs (-1: none): wave w of the workgroup has the 64 S pairs
+// from first_pair on, 64 a step.
+template <int S>
+__device__ __forceinline__ int64_t first_pair() {
+  return ((int64_t)blockIdx.x * kSortWaves + wave_index()) * (64 * S);
+}
+template <int S, typename I>
+__device__ __forceinline__ void ld_experts(const I* idx, int64_t p0, int64_t pairs, int experts,
+                                           int (&e)[S]) {
   const int lane = threadIdx.x % 64;
-  for (int64_t p = sp.p0 + lane; p < sp.p1; p += 64) {
-    const int e = expert_of(idx[p], experts);
-    if (e >= 0) atomicAdd(&cnt[e], 1);
+  I v[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) v[s] = p0 + s * 64 + lane < pairs ? idx[p0 + s * 64 + lane] : (I)-1;
+#pragma unroll
+  for (int s = 0; s < S; ++s) e[s] = expert_of(v[s], experts);
+}
+
+// counts[block][expert] of the workgroup's pairs.
+template <int S, typename I>
+__global__ void __launch_bounds__(kSortBlock)
+moe_count_kernel(const I* __restrict__ idx, int64_t pairs, int experts,
+                 int32_t* __restrict__ block_counts) {
+  __shared__ int cnt[kMoeMaxExperts];
+  int e[S];
+  ld_experts<S>(idx, first_pair<S>(), pairs, experts, e);
+  for (int i = threadIdx.x; i < experts; i += kSortBlock) cnt[i] = 0;
+  __syncthreads();
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+    if (e[s] >= 0) atomicAdd(&cnt[e[s]], 1);
+  __syncthreads();
+  for (int i = threadIdx.x; i < experts; i += kSortBlock)
+    block_counts[(int64_t)blockIdx.x * experts + i] = cnt[i];
+}
+
+// counts[block][expert] become the counts of the blocks before; totals[expert] their sum. A
+// lane has an expert, a wave a share of the blocks.
+__global__ void __launch_bounds__(kSortBlock)
+moe_scan_kernel(int32_t* __restrict__ block_counts, int64_t blocks, int experts,
+                int32_t* __restrict__ totals) {
+  __shared__ int sum[kSortWaves][64];
+  const int lane = threadIdx.x % 64, wave = wave_index(), e = blockIdx.x * 64 + lane;
+  const int64_t per = (blocks + kSortWaves - 1) / kSortWaves;
+  const int64_t b0 = wave * per < blocks ? wave * per : blocks;
+  const int64_t b1 = b0 + per < blocks ? b0 + per : blocks;
+  int n = 0;
+  if (e < experts)
+#pragma unroll 8
+    for (int64_t b = b0; b < b1; ++b) n += block_counts[b * experts + e];
+  sum[wave][lane] = n;
+  __syncthreads();
+  int at = 0;
+  for (int w = 0; w < wave; ++w) at += sum[w][lane];
+  if (e >= experts) return;
+  if (wave == kSortWaves - 1) totals[e] = at + n;
+  for (int64_t b = b0; b < b1; ++b) {
+    const int c = block_counts[b * experts + e];
+    block_counts[b * experts + e] = at;
+    at += c;
   }
 }
 
-// Per-workgroup counts by expert, for a sort over several workgroups.
-template <typename I>
+// The sort. A pair's row is its expert's start, plus the expert's pairs in earlier workgroups,
+// in earlier waves of this workgroup, in earlier steps of this wave, and in lower lanes of its
+// step. The last comes from one ballot per bit of the expert index: the lanes that agree in
+// every bit are the same expert's. Counts are integers added in a fixed order.
+// block_counts: null for a single workgroup; else the counts of the blocks, or with totals
+// those of the blocks before each.
+template <int S, typename I>
 __global__ void __launch_bounds__(kSortBlock)
-moe_count_kernel(const I* __restrict__ idx, int64_t pairs, int64_t chunk, int experts,
-                 int32_t* __restrict__ block_counts) {
-  __shared__ int cnt[kMoeMaxExperts];
-  for (int e = threadIdx.x; e < experts; e += kSortBlock) cnt[e] = 0;
-  __syncthreads();
-  count_span(idx, wave_span(pairs, chunk), experts, cnt);
-  __syncthreads();
-  for (int e = threadIdx.x; e < experts; e += kSortBlock)
-    block_counts[(int64_t)blockIdx.x * experts + e] = cnt[e];
-}
-
-// The sort. A stable rank is: pairs of the same expert in earlier workgroups, in earlier
-// waves of this workgroup, in earlier steps of this wave, and in lower lanes of this step.
-// The last comes from one ballot per bit of the expert index: the lanes that agree in every
-// bit are the same expert's. Counts are integers, so nothing depends on the atomics' order.
-template <typename I>
-__global__ void __launch_bounds__(kSortBlock)
-moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int64_t chunk, int experts, int bits,
-                int multiple, int64_t rows, const int32_t* __restrict__ block_counts,
-                int32_t* __restrict__ slot, int32_t* __restrict__ source,
-                int32_t* __restrict__ counts, int32_t* __restrict__ offsets) {
-  extern __shared__ int lds[];                 // next[waves][experts], then total[experts]
+moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int experts, int bits, int multiple,
+                int64_t rows, const int32_t* __restrict__ block_counts,
+                const int32_t* __restrict__ totals, int32_t* __restrict__ slot,
+                int32_t* __restrict__ source, int32_t* __restrict__ counts,
+                int32_t* __restrict__ offsets) {
+  extern __shared__ int lds[];                 // next[waves][experts], then the share sums
   __shared__ int wave_sum[kSortWaves];
+  __shared__ int end;
   int* next = lds;
-  int* total = lds + kSortWaves * experts;     // the expert's pairs, then its padded end
-  const int t = threadIdx.x, lane = t % 64, wave = t / 64;
+  int2* share = reinterpret_cast<int2*>(lds + kSortWaves * experts);
+  const int t = threadIdx.x, lane = t % 64, wave = wave_index();
+  const int64_t p0 = first_pair<S>();
+  int e[S], row[S];
+  ld_experts<S>(idx, p0, pairs, experts, e);
+  // block counts: lane groups of 2^bits lanes take every `shares`-th block
+  const int shares = min(kSortBlock >> bits, kSortShares);
+  const int se = t & ((1 << bits) - 1), sg = t >> bits;
+  int2 n = {0, 0};                             // all blocks, blocks before this
+  if (block_counts && !totals && se < experts && sg < shares) {
+#pragma unroll 4
+    for (int b = sg; b < (int)gridDim.x; b += shares) {
+      const int c = block_counts[(int64_t)b * experts + se];
+      n.x += c;
+      if (b < (int)blockIdx.x) n.y += c;
+    }
+  }
   for (int i = t; i < kSortWaves * experts; i += kSortBlock) next[i] = 0;
+  share[t] = n;
   __syncthreads();
-  const Span sp = wave_span(pairs, chunk);
-  count_span(idx, sp, experts, next + wave * experts);
+  // ranks among the wave's own pairs
+  volatile int* mine = next + wave * experts;
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    uint64_t same = __ballot(e[s] >= 0);
+    row[s] = -1;
+    if (!same) continue;
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t m = __ballot((e[s] >> b) & 1);
+      same &= ((e[s] >> b) & 1) ? m : ~m;
+    }
+    if (e[s] >= 0) {
+      const int rank = __popcll(same & ((1ull << lane) - 1)), had = mine[e[s]];
+      row[s] = had + rank;
+      // the wave runs in step: every lane has read the counter before the lowest adds to it
+      __builtin_amdgcn_wave_barrier();
+      if (rank == 0) mine[e[s]] = had + __popcll(same);
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
   __syncthreads();
   // thread e: expert e's pairs over all workgroups and before this one
   int tot = 0, before = 0;
   if (t < experts) {
-    if (gridDim.x == 1) {
+    if (!block_counts) {
       for (int w = 0; w < kSortWaves; ++w) tot += next[w * experts + t];
+    } else if (totals) {
+      tot = totals[t];
+      before = block_counts[(int64_t)blockIdx.x * experts + t];
     } else {
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int c = block_counts[(int64_t)b * experts + t];
-        tot += c;
-        if (b < (int)blockIdx.x) before += c;
+      for (int g = 0; g < shares; ++g) {
+        const int2 c = share[(g << bits) + t];
+        tot += c.x;
+        before += c.y;
       }
     }
   }
@@ -122,7 +201,7 @@ moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int64_t chunk, int exp
       next[w * experts + t] = at;
       at += c;
     }
-    total[t] = pre;
+    if (t == experts - 1) end = pre;
     if (blockIdx.x == 0) {
       counts[t] = tot;
       offsets[t + 1] = pre;
@@ -133,65 +212,43 @@ moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int64_t chunk, int exp
       for (int r = start + tot; r < pre; ++r) source[r] = -1;
   }
   __syncthreads();
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const int64_t p = p0 + s * 64 + lane;
+    if (p >= pairs) break;
+    if (e[s] >= 0) {
+      row[s] += next[wave * experts + e[s]];
+      source[row[s]] = (int32_t)p;
+    }
+    slot[p] = row[s];
+  }
   // rows past the last expert's
-  for (int64_t r = total[experts - 1] + (int64_t)blockIdx.x * kSortBlock + t; r < rows;
+  for (int64_t r = end + (int64_t)blockIdx.x * kSortBlock + t; r < rows;
        r += (int64_t)gridDim.x * kSortBlock)
     source[r] = -1;
-  volatile int* mine = next + wave * experts;
-  for (int64_t p0 = sp.p0; p0 < sp.p1; p0 += 64) {
-    const int64_t p = p0 + lane;
-    const bool in = p < sp.p1;
-    const int e = in ? expert_of(idx[p], experts) : -1;
-    uint64_t same = __ballot(e >= 0);
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t m = __ballot((e >> b) & 1);
-      same &= ((e >> b) & 1) ? m : ~m;
-    }
-    int row = -1;
-    if (e >= 0) {
-      const int rank = __popcll(same & ((1ull << lane) - 1));
-      row = mine[e] + rank;
-      // the wave runs in step: every lane has read the counter before the lowest adds to it
-      __builtin_amdgcn_wave_barrier();
-      if (rank == 0) mine[e] = row + __popcll(same);
-      source[row] = (int32_t)p;
-    }
-    __builtin_amdgcn_wave_barrier();
-    if (in) slot[p] = row;
-  }
 }
 
 // -------------------------------------------------------------------------- exchanges
 
-constexpr int kMoveBlock = 256, kMovePieces = 4;           // 4 KiB of a row per wave
-constexpr int kMoveBytes = 64 * 16 * kMovePieces;
+constexpr int kMoveBlock = 256, kMoveWaves = kMoveBlock / 64;
+constexpr int kMovePieces = 4, kSumPieces = 2;             // 16-byte pieces of a row per lane
 constexpr int kZeroRows = 8;                               // rows checked by a wave
 
-// 16 bytes of a row of `bytes` bytes (a multiple of 2) at byte b; the row's last piece may be
-// cut off at its end.
-__device__ __forceinline__ piece_t ld_bytes(const uint8_t* row, int64_t b, int64_t bytes) {
-  if (b + 16 <= bytes) return ld_piece(row + b);
-  piece_t v = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (b + 2 * i < bytes)
-      v[i / 2] |= (uint32_t)*reinterpret_cast<const uint16_t*>(row + b + 2 * i) << (16 * (i & 1));
-  return v;
-}
-__device__ __forceinline__ void st_bytes(uint8_t* row, int64_t b, int64_t bytes, piece_t v) {
-  if (b + 16 <= bytes) {
-    st_piece(row + b, v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (b + 2 * i < bytes)
-      *reinterpret_cast<uint16_t*>(row + b + 2 * i) = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+// Waves of the grid, the same for all lanes (addresses of rows are scalar).
+__device__ __forceinline__ uint32_t grid_wave() {
+  return blockIdx.x * (uint32_t)kMoveWaves + (uint32_t)wave_index();
 }
 
-// Zero the padding rows among rows [r0, r0 + kZeroRows), bytes [b0, b0 + kMoveBytes).
+// The row of a pair, -1 where there is none in the buffer.
+__device__ __forceinline__ int row_of(const int32_t* slot, int64_t pair, int64_t rows) {
+  const int r = slot[pair];
+  return r >= 0 && r < rows ? r : -1;
+}
+
+// Zero the padding rows among rows [r0, r0 + kZeroRows), kMovePieces pieces a lane from c0 on.
+template <typename T>
 __device__ __forceinline__ void zero_padding(const int32_t* source, int64_t r0, int64_t rows,
-                                             int64_t b0, int64_t bytes, uint8_t* out) {
+                                             int c0, int cols, T* out) {
   const int lane = threadIdx.x % 64;
   const int64_t r = r0 + lane;
   const bool pad = lane < kZeroRows && r < rows && source[r] < 0;
@@ -199,57 +256,60 @@ __device__ __forceinline__ void zero_padding(const int32_t* source, int64_t r0, 
   while (m) {
     const int i = __ffsll((unsigned long long)m) - 1;
     m &= m - 1;
-    uint8_t* row = out + (r0 + i) * bytes;
+    T* row = out + (r0 + i) * cols;
 #pragma unroll
     for (int v = 0; v < kMovePieces; ++v)
-      st_bytes(row, b0 + (v * 64 + lane) * 16, bytes, piece_t{0, 0, 0, 0});
+      st_row(row, c0 + (v * 64 + lane) * Piece<T>::N, cols, piece_t{0, 0, 0, 0});
   }
 }
 
-// One wave per (token, 4 KiB of the row): loaded once, stored to each of the token's rows.
-// The waves after those zero the padding rows.
+// One wave per (token, kMovePieces pieces a lane of the row): loaded once, stored to each of
+// the token's rows. The waves after those zero the padding rows.
+template <typename T>
 __global__ void __launch_bounds__(kMoveBlock)
-moe_dispatch_kernel(const uint8_t* __restrict__ x, int64_t ld_bytes_x,
-                    const int32_t* __restrict__ slot, const int32_t* __restrict__ source,
-                    int64_t tokens, int topk, int64_t rows, int64_t bytes, int64_t chunks,
-                    uint8_t* __restrict__ xs) {
+moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slot,
+                    const int32_t* __restrict__ source, int64_t tokens, int topk, int64_t rows,
+                    int cols, uint32_t chunks, T* __restrict__ xs) {
+  constexpr int N = Piece<T>::N, kCols = 64 * N * kMovePieces;
   const int lane = threadIdx.x % 64;
-  int64_t u = (int64_t)blockIdx.x * (kMoveBlock / 64) + threadIdx.x / 64;
-  if (u >= tokens * chunks) {
-    u -= tokens * chunks;
-    const int64_t r0 = u / chunks * kZeroRows;
-    if (r0 < rows) zero_padding(source, r0, rows, u % chunks * kMoveBytes, bytes, xs);
+  uint32_t u = grid_wave();
+  const uint32_t moves = (uint32_t)tokens * chunks;
+  if (u >= moves) {
+    u -= moves;
+    const int64_t r0 = (int64_t)(u / chunks) * kZeroRows;
+    if (r0 < rows) zero_padding(source, r0, rows, (int)(u % chunks) * kCols, cols, xs);
     return;
   }
-  const int64_t t = u / chunks, b0 = u % chunks * kMoveBytes;
+  const int64_t t = u / chunks;
+  const int c0 = (int)(u % chunks) * kCols + lane * N;
+  const T* src = x + t * ldx;
   piece_t v[kMovePieces];
 #pragma unroll
-  for (int i = 0; i < kMovePieces; ++i)
-    v[i] = ld_bytes(x + t * ld_bytes_x, b0 + (i * 64 + lane) * 16, bytes);
-  for (int j = 0; j < topk; ++j) {
-    const int r = slot[t * topk + j];
-    if (r < 0 || r >= rows) continue;
+  for (int i = 0; i < kMovePieces; ++i) v[i] = ld_raw(src, c0 + i * 64 * N, cols);
 #pragma unroll
-    for (int i = 0; i < kMovePieces; ++i)
-      st_bytes(xs + r * bytes, b0 + (i * 64 + lane) * 16, bytes, v[i]);
+  for (int i = 0; i < kMovePieces; ++i) v[i] = cut<T>(v[i], c0 + i * 64 * N, cols);
+  for (int j = 0; j < topk; ++j) {
+    const int r = row_of(slot, t * topk + j, rows);
+    if (r < 0) continue;
+    T* dst = xs + (int64_t)r * cols;
+#pragma unroll
+    for (int i = 0; i < kMovePieces; ++i) st_row(dst, c0 + i * 64 * N, cols, v[i]);
   }
 }
 
-constexpr int kSumPieces = 2;                              // 16-byte pieces of a row per lane
-
-// One wave per (token, 2 KiB of the row): the token's rows, four in flight, summed in the
-// order of the choices in float32 and rounded once.
-template <typename T>
+// One wave per (token, kSumPieces pieces a lane of the row): the token's rows, U in flight,
+// summed in the order of the choices in float32 and rounded once.
+template <typename T, int U>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict__ slot,
                    const float* __restrict__ weights, int64_t tokens, int topk, int64_t rows,
-                   int cols, int chunks, T* __restrict__ y) {
-  constexpr int N = Piece<T>::N, U = 4;
+                   int cols, uint32_t chunks, T* __restrict__ y) {
+  constexpr int N = Piece<T>::N, kCols = 64 * N * kSumPieces;
   const int lane = threadIdx.x % 64;
-  const int64_t u = (int64_t)blockIdx.x * (kMoveBlock / 64) + threadIdx.x / 64;
-  if (u >= tokens * chunks) return;
+  const uint32_t u = grid_wave();
   const int64_t t = u / chunks;
-  const int c0 = ((int)(u % chunks) * kSumPieces * 64 + lane) * N;
+  if (t >= tokens) return;
+  const int c0 = (int)(u % chunks) * kCols + lane * N;
   float acc[kSumPieces][N];
 #pragma unroll
   for (int i = 0; i < kSumPieces; ++i)
@@ -258,26 +318,29 @@ moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __rest
   for (int j0 = 0; j0 < topk; j0 += U) {
     piece_t v[U][kSumPieces];
     float w[U];
-    bool live[U];
+    int r[U];
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      const int j = j0 + q;
-      const int r = j < topk ? slot[t * topk + j] : -1;
-      live[q] = r >= 0 && r < rows;
-      w[q] = live[q] && weights ? weights[t * topk + j] : 1.f;
-#pragma unroll
-      for (int i = 0; i < kSumPieces; ++i)
-        v[q][i] = live[q] ? ld_row(ys + r * ldys, c0 + i * 64 * N, cols) : piece_t{0, 0, 0, 0};
+      const int64_t pair = t * topk + j0 + q;
+      r[q] = j0 + q < topk ? row_of(slot, pair, rows) : -1;
+      w[q] = r[q] >= 0 && weights ? weights[pair] : 1.f;
     }
 #pragma unroll
     for (int q = 0; q < U; ++q) {
-      if (!live[q]) continue;
+      if (r[q] < 0) continue;
+#pragma unroll
+      for (int i = 0; i < kSumPieces; ++i)
+        v[q][i] = ld_raw(ys + r[q] * ldys, c0 + i * 64 * N, cols);
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+      if (r[q] < 0) continue;
 #pragma unroll
       for (int i = 0; i < kSumPieces; ++i) {
         float f[N];
-        unpack(v[q][i], f, T{});
+        unpack(cut<T>(v[q][i], c0 + i * 64 * N, cols), f, T{});
 #pragma unroll
-        for (int n = 0; n < N; ++n) acc[i][n] += w[q] * f[n];
+        for (int n = 0; n < N; ++n) acc[i][n] = __builtin_fmaf(w[q], f[n], acc[i][n]);
       }
     }
   }
@@ -286,134 +349,191 @@ moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __rest
     st_row(y + t * cols, c0 + i * 64 * N, cols, pack(acc[i], T{}));
 }
 
-constexpr int kDotChoices = 8;                             // choices per walk over the row
-
-// One workgroup per token: it reads dy[t] once per 8 choices, writes w dy to their rows and
-// sums dy ys of each (lanes, then waves, in a fixed order). The workgroups after the tokens'
-// zero the padding rows.
-template <typename T>
+// W waves per token read dy[t] once per J choices, write w dy to their rows and sum dy ys of
+// each (lanes, then waves, in a fixed order). The workgroups after the tokens' zero the
+// padding rows.
+template <typename T, int W, int J>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ ys,
                        int64_t ldys, const int32_t* __restrict__ slot,
                        const int32_t* __restrict__ source, const float* __restrict__ weights,
-                       int64_t tokens, int topk, int64_t rows, int cols, int chunks,
-                       T* __restrict__ dys, float* __restrict__ dw) {
-  constexpr int N = Piece<T>::N, J = kDotChoices, WAVES = kMoveBlock / 64;
-  __shared__ float part[WAVES][J];
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int64_t t = blockIdx.x;
-  if (t >= tokens) {
-    const int64_t u = (t - tokens) * WAVES + wave;
-    const int64_t r0 = u / chunks * kZeroRows;
+                       int64_t tokens, uint32_t token_blocks, int topk, int64_t rows, int cols,
+                       uint32_t chunks, T* __restrict__ dys, float* __restrict__ dw) {
+  constexpr int N = Piece<T>::N, PER = kMoveWaves / W;
+  __shared__ float part[W][J];
+  const int lane = threadIdx.x % 64, wave = wave_index();
+  if (blockIdx.x >= token_blocks) {
+    const uint32_t u = grid_wave() - token_blocks * kMoveWaves;
+    const int64_t r0 = (int64_t)(u / chunks) * kZeroRows;
     if (r0 < rows)
-      zero_padding(source, r0, rows, u % chunks * kMoveBytes, (int64_t)cols * sizeof(T),
-                   reinterpret_cast<uint8_t*>(dys));
+      zero_padding(source, r0, rows, (int)(u % chunks) * (64 * N * kMovePieces), cols, dys);
     return;
   }
+  const int64_t t = (int64_t)blockIdx.x * PER + (W == 1 ? wave : 0);
+  if (t >= tokens) return;                       // a whole token's waves
+  const int lt = W == 1 ? lane : (int)threadIdx.x;
   const T* g = dy + t * lddy;
   for (int j0 = 0; j0 < topk; j0 += J) {
     int r[J];
     float w[J], dot[J];
 #pragma unroll
     for (int q = 0; q < J; ++q) {
-      const int j = j0 + q;
-      r[q] = j < topk ? slot[t * topk + j] : -1;
-      if (r[q] >= rows) r[q] = -1;
-      w[q] = r[q] >= 0 ? weights[t * topk + j] : 0.f;
+      const int64_t pair = t * topk + j0 + q;
+      r[q] = j0 + q < topk ? row_of(slot, pair, rows) : -1;
+      w[q] = r[q] >= 0 ? weights[pair] : 0.f;
       dot[q] = 0.f;
     }
-    for (int c = threadIdx.x * N; c < cols; c += kMoveBlock * N) {
+    for (int c = lt * N; c < cols; c += W * 64 * N) {
+      piece_t pg = ld_raw(g, c, cols), py[J];
+#pragma unroll
+      for (int q = 0; q < J; ++q)
+        if (r[q] >= 0) py[q] = ld_raw(ys + r[q] * ldys, c, cols);
       float fg[N];
-      unpack(ld_row(g, c, cols), fg, T{});
+      unpack(cut<T>(pg, c, cols), fg, T{});
 #pragma unroll
       for (int q = 0; q < J; ++q) {
         if (r[q] < 0) continue;
         float fy[N], o[N];
-        unpack(ld_row(ys + r[q] * ldys, c, cols), fy, T{});
+        unpack(cut<T>(py[q], c, cols), fy, T{});
 #pragma unroll
         for (int n = 0; n < N; ++n) {
-          dot[q] += fg[n] * fy[n];
+          dot[q] = __builtin_fmaf(fg[n], fy[n], dot[q]);
           o[n] = w[q] * fg[n];
         }
         st_row(dys + (int64_t)r[q] * cols, c, cols, pack(o, T{}));
       }
     }
-    __syncthreads();
+    if constexpr (W == 1) {
 #pragma unroll
-    for (int q = 0; q < J; ++q) {
-      const float d = lanes_sum<64>(dot[q]);
-      if (lane == 0) part[wave][q] = d;
-    }
-    __syncthreads();
-    if (threadIdx.x < J && j0 + (int)threadIdx.x < topk) {
-      float d = 0.f;
+      for (int q = 0; q < J; ++q) {
+        const float d = lanes_sum<64>(dot[q]);
+        if (lane == 0 && j0 + q < topk) dw[t * topk + j0 + q] = d;
+      }
+    } else {
+      __syncthreads();
 #pragma unroll
-      for (int k = 0; k < WAVES; ++k) d += part[k][threadIdx.x];
-      dw[t * topk + j0 + threadIdx.x] = d;
+      for (int q = 0; q < J; ++q) {
+        const float d = lanes_sum<64>(dot[q]);
+        if (lane == 0) part[wave][q] = d;
+      }
+      __syncthreads();
+      if (threadIdx.x < J && j0 + (int)threadIdx.x < topk) {
+        float d = 0.f;
+#pragma unroll
+        for (int k = 0; k < W; ++k) d += part[k][threadIdx.x];
+        dw[t * topk + j0 + threadIdx.x] = d;
+      }
     }
   }
 }
 
-int64_t sort_chunk(int64_t pairs) {
-  // whole steps of every wave; more than kSortGrid chunks of kSortChunk become longer chunks
-  int64_t c = kSortChunk;
-  if (pairs > c * kSortGrid) c = (pairs + kSortGrid - 1) / kSortGrid;
-  return (c + kSortBlock - 1) / kSortBlock * kSortBlock;
+struct SortPlan { int64_t chunk, blocks; bool scan; };
+SortPlan sort_plan(int64_t pairs) {
+  if (pairs <= kSortOne) return {kSortOne, 1, false};
+  const int64_t b = (pairs + kSortChunk - 1) / kSortChunk;
+  if (b <= kSortDirect) return {kSortChunk, b, false};
+  return {kSortLong, (pairs + kSortLong - 1) / kSortLong, true};
 }
 
-template <typename I>
-hipError_t sort_launch(const MoeSortArgs& a, hipStream_t s) {
-  const int64_t chunk = sort_chunk(a.pairs);
-  const unsigned blocks = (unsigned)std::max<int64_t>(1, (a.pairs + chunk - 1) / chunk);
+template <int S, typename I>
+hipError_t sort_steps(const MoeSortArgs& a, const SortPlan& plan, hipStream_t s) {
   int bits = 0;
   while ((1 << bits) < a.experts) ++bits;
   const I* idx = static_cast<const I*>(a.idx);
-  if (blocks > 1) {
-    hipLaunchKernelGGL((moe_count_kernel<I>), dim3(blocks), dim3(kSortBlock), 0, s, idx, a.pairs,
-                       chunk, a.experts, a.workspace);
+  const unsigned blocks = (unsigned)plan.blocks;
+  int32_t* block_counts = blocks > 1 ? a.workspace : nullptr;
+  int32_t* totals = plan.scan ? a.workspace + plan.blocks * a.experts : nullptr;
+  if (block_counts) {
+    hipLaunchKernelGGL((moe_count_kernel<S, I>), dim3(blocks), dim3(kSortBlock), 0, s, idx,
+                       a.pairs, a.experts, block_counts);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  const unsigned lds = (kSortWaves + 1) * (unsigned)a.experts * sizeof(int);
-  hipLaunchKernelGGL((moe_sort_kernel<I>), dim3(blocks), dim3(kSortBlock), lds, s, idx, a.pairs,
-                     chunk, a.experts, bits, a.multiple, a.rows, a.workspace, a.slot, a.source,
+  if (totals) {
+    hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)(a.experts + 63) / 64), dim3(kSortBlock), 0,
+                       s, block_counts, plan.blocks, a.experts, totals);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const unsigned lds = (kSortWaves * (unsigned)a.experts + 2 * kSortBlock) * sizeof(int);
+  hipLaunchKernelGGL((moe_sort_kernel<S, I>), dim3(blocks), dim3(kSortBlock), lds, s, idx, a.pairs,
+                     a.experts, bits, a.multiple, a.rows, block_counts, totals, a.slot, a.source,
                      a.counts, a.offsets);
   return hipGetLastError();
 }
 
-int64_t zero_units(int64_t rows, int64_t chunks) {
+template <typename I>
+hipError_t sort_launch(const MoeSortArgs& a, hipStream_t s) {
+  const SortPlan plan = sort_plan(a.pairs);
+  if (a.pairs <= kSortBlock) return sort_steps<1, I>(a, plan, s);
+  if (a.pairs <= 4 * kSortBlock || plan.chunk == kSortChunk) return sort_steps<4, I>(a, plan, s);
+  return sort_steps<16, I>(a, plan, s);
+}
+
+// Chunks of a row of `pieces` pieces a lane, and the waves that zero its padding rows.
+template <typename T> uint32_t row_chunks(int64_t cols, int pieces) {
+  const int per = 64 * Piece<T>::N * pieces;
+  return (uint32_t)((cols + per - 1) / per);
+}
+int64_t zero_waves(int64_t rows, int64_t chunks) {
   return (rows + kZeroRows - 1) / kZeroRows * chunks;
 }
+unsigned move_blocks(int64_t waves) { return (unsigned)((waves + kMoveWaves - 1) / kMoveWaves); }
 
 template <typename T>
-hipError_t combine(const MoeArgs& a, hipStream_t s) {
-  const int per = kSumPieces * 64 * Piece<T>::N;
-  const int chunks = (int)((a.cols + per - 1) / per);
-  const int64_t blocks = (a.tokens * chunks + kMoveBlock / 64 - 1) / (kMoveBlock / 64);
-  hipLaunchKernelGGL((moe_combine_kernel<T>), dim3((unsigned)blocks), dim3(kMoveBlock), 0, s,
-                     static_cast<const T*>(a.ys), a.ldys, a.slot, a.weights, a.tokens, a.topk,
-                     a.rows, (int)a.cols, chunks, static_cast<T*>(a.out));
+hipError_t dispatch(const MoeArgs& a, hipStream_t s) {
+  const uint32_t chunks = row_chunks<T>(a.cols, kMovePieces);
+  const unsigned blocks = move_blocks(a.tokens * chunks + zero_waves(a.rows, chunks));
+  hipLaunchKernelGGL((moe_dispatch_kernel<T>), dim3(blocks), dim3(kMoveBlock), 0, s,
+                     static_cast<const T*>(a.x), a.ldx, a.slot, a.source, a.tokens, a.topk, a.rows,
+                     (int)a.cols, chunks, static_cast<T*>(a.out));
   return hipGetLastError();
 }
 
+template <typename T, int U>
+hipError_t combine_rows(const MoeArgs& a, hipStream_t s) {
+  const uint32_t chunks = row_chunks<T>(a.cols, kSumPieces);
+  hipLaunchKernelGGL((moe_combine_kernel<T, U>), dim3(move_blocks(a.tokens * chunks)),
+                     dim3(kMoveBlock), 0, s, static_cast<const T*>(a.ys), a.ldys, a.slot,
+                     a.weights, a.tokens, a.topk, a.rows, (int)a.cols, chunks,
+                     static_cast<T*>(a.out));
+  return hipGetLastError();
+}
+template <typename T>
+hipError_t combine(const MoeArgs& a, hipStream_t s) {
+  return a.topk <= 4 ? combine_rows<T, 4>(a, s) : combine_rows<T, 8>(a, s);
+}
+
+template <typename T, int W, int J>
+hipError_t combine_bwd_rows(const MoeArgs& a, hipStream_t s) {
+  const uint32_t chunks = row_chunks<T>(a.cols, kMovePieces);
+  const int64_t per = kMoveWaves / W;
+  const uint32_t token_blocks = (uint32_t)((a.tokens + per - 1) / per);
+  const unsigned blocks = token_blocks + move_blocks(zero_waves(a.rows, chunks));
+  hipLaunchKernelGGL((moe_combine_bwd_kernel<T, W, J>), dim3(blocks), dim3(kMoveBlock), 0, s,
+                     static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.ys), a.ldys,
+                     a.slot, a.source, a.weights, a.tokens, token_blocks, a.topk, a.rows,
+                     (int)a.cols, chunks, static_cast<T*>(a.out), a.dw);
+  return hipGetLastError();
+}
+template <typename T, int W>
+hipError_t combine_bwd_waves(const MoeArgs& a, hipStream_t s) {
+  if (a.topk <= 2) return combine_bwd_rows<T, W, 2>(a, s);
+  return a.topk <= 4 ? combine_bwd_rows<T, W, 4>(a, s) : combine_bwd_rows<T, W, 8>(a, s);
+}
 template <typename T>
 hipError_t combine_bwd(const MoeArgs& a, hipStream_t s) {
-  const int64_t bytes = a.cols * (int64_t)sizeof(T);
-  const int chunks = (int)((bytes + kMoveBytes - 1) / kMoveBytes);
-  const int waves = kMoveBlock / 64;
-  const int64_t blocks = a.tokens + (zero_units(a.rows, chunks) + waves - 1) / waves;
-  hipLaunchKernelGGL((moe_combine_bwd_kernel<T>), dim3((unsigned)blocks), dim3(kMoveBlock), 0, s,
-                     static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.ys), a.ldys,
-                     a.slot, a.source, a.weights, a.tokens, a.topk, a.rows, (int)a.cols, chunks,
-                     static_cast<T*>(a.out), a.dw);
-  return hipGetLastError();
+  // rows of up to two pieces a lane take one wave: four would leave most lanes idle
+  return a.cols <= 2 * 64 * Piece<T>::N ? combine_bwd_waves<T, 1>(a, s)
+                                        : combine_bwd_waves<T, kMoveWaves>(a, s);
 }
 
 }  // namespace
 
 int64_t moe_sort_workspace(int64_t pairs, int32_t experts) {
-  const int64_t chunk = sort_chunk(pairs), blocks = (pairs + chunk - 1) / chunk;
-  return blocks > 1 ? blocks * experts * (int64_t)sizeof(int32_t) : 0;
+  const SortPlan plan = sort_plan(pairs);
+  if (plan.blocks == 1) return 0;
+  return (plan.blocks + (plan.scan ? 1 : 0)) * experts * (int64_t)sizeof(int32_t);
 }
 
 hipError_t launch_moe_sort(const MoeSortArgs& a, hipStream_t s) {
@@ -421,14 +541,8 @@ hipError_t launch_moe_sort(const MoeSortArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_moe_dispatch(const MoeArgs& a, hipStream_t s) {
-  const int64_t es = a.dtype == kF32 ? 4 : 2, bytes = a.cols * es;
-  const int64_t chunks = (bytes + kMoveBytes - 1) / kMoveBytes;
-  const int waves = kMoveBlock / 64;
-  const int64_t blocks = (a.tokens * chunks + zero_units(a.rows, chunks) + waves - 1) / waves;
-  hipLaunchKernelGGL(moe_dispatch_kernel, dim3((unsigned)blocks), dim3(kMoveBlock), 0, s,
-                     static_cast<const uint8_t*>(a.x), a.ldx * es, a.slot, a.source, a.tokens,
-                     a.topk, a.rows, bytes, chunks, static_cast<uint8_t*>(a.out));
-  return hipGetLastError();
+  // only moved, so 2-byte elements of either type are the same
+  return a.dtype == kF32 ? dispatch<float>(a, s) : dispatch<BF16>(a, s);
 }
 
 hipError_t launch_moe_combine(const MoeArgs& a, hipStream_t s) {
