@@ -20,26 +20,30 @@ namespace fp8lin {
 
 namespace {
 
-// EPT consecutive-piece elements of a parameter row as floats (`fill` without a tensor).
-template <typename P, int N>
-__device__ __forceinline__ void ld_params(const P* p, int c, int cols, float fill, float (&f)[N]) {
+// The N elements at column c of a parameter row as floats (`fill` without a tensor). Read once
+// a workgroup, so the parameters' type (the rows' or float32) is a value, not another kernel.
+template <typename T, int N>
+__device__ __forceinline__ void ld_params(const void* p, bool f32, int c, int cols, float fill,
+                                          float (&f)[N]) {
   if (!p) {
 #pragma unroll
     for (int i = 0; i < N; ++i) f[i] = fill;
-    return;
-  }
-  constexpr int PN = Piece<P>::N;
-  if constexpr (PN <= N) {
+  } else if (f32) {
 #pragma unroll
-    for (int h = 0; h < N / PN; ++h) {
-      float t[PN];
-      unpack(ld_row(p, c + h * PN, cols), t, P{});
+    for (int h = 0; h < N; h += 4) {
+      float t[4];
+      unpack(ld_row(static_cast<const float*>(p), c + h, cols), t, float{});
 #pragma unroll
-      for (int i = 0; i < PN; ++i) f[h * PN + i] = t[i];
+      for (int i = 0; i < 4; ++i) f[h + i] = t[i];
     }
   } else {
-    static_assert(PN <= N, "a parameter piece is at most a data piece");
+    unpack(ld_row(static_cast<const T*>(p), c, cols), f, T{});
   }
+}
+template <typename T>
+__device__ __forceinline__ void st_param(void* p, bool f32, int c, float v) {
+  if (f32) static_cast<float*>(p)[c] = v;
+  else static_cast<T*>(p)[c] = from_f32<T>(v);
 }
 
 // Four partial sums; a workspace is aligned to its floats only.
@@ -62,11 +66,11 @@ __device__ __forceinline__ int64_t turn_row(int64_t r0, int group, int64_t rows)
 }
 
 // This lane's pieces of a row, not yet cut at its end.
-template <typename T, int LPR, int NV>
+template <Cache C, int LPR, typename T, int NV>
 __device__ __forceinline__ void ld_rows(const T* row, int lane, int cols, piece_t (&p)[NV]) {
 #pragma unroll
   for (int v = 0; v < NV; ++v)
-    p[v] = ld_raw<T, LPR == 16>(row, (v * LPR + lane) * Piece<T>::N, cols);
+    p[v] = ld_raw<C, LPR == 16>(row, (v * LPR + lane) * Piece<T>::N, cols);
 }
 
 // Sum over the LPR lanes of a row. Rows of several waves meet in LDS (`part`, one float per
@@ -85,12 +89,22 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
   return v;
 }
 
+// The forward's workgroups are short (eight to a compute unit), the backward's hold one unit
+// each: 16 waves of 128 registers, and as few rows of partial sums as that allows. Backward of
+// 8192x4096 bf16: 45.0 us so, 45.3 us with twice as many workgroups of 512, 48.1 us with four
+// times as many of 256; of 1021x5003 f16 21.4, 22.5 and 22.6 us, and with half the workgroups
+// 24.6 us. The forward of 8192x4096 does not depend on its grid (23.0 to 23.7 us).
+constexpr int kFwdBlock = 256, kBwdBlock = 1024;
+constexpr int64_t kFwdGrid = 256 * 8, kBwdGrid = 256;
+
+constexpr int fwd_block(int lpr) { return lpr > kFwdBlock ? lpr : kFwdBlock; }
+
 // LPR lanes own a row; lane l holds the pieces l, l + LPR, ... (EPT elements). A workgroup
 // walks the rows with the grid's stride and loads the next row while it works on this one.
-template <typename T, typename P, int LPR, int EPT, int BLOCK>
+template <typename T, int LPR, int EPT, int BLOCK, Cache LOAD>
 __global__ void __launch_bounds__(BLOCK)
-layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__ gamma,
-                     const P* __restrict__ beta, int64_t rows, int cols, float eps,
+layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const void* __restrict__ gamma,
+                     const void* __restrict__ beta, bool params_f32, int64_t rows, int cols, float eps,
                      T* __restrict__ y, float* __restrict__ mean_out,
                      float* __restrict__ rstd_out) {
   constexpr int N = Piece<T>::N, NV = EPT / N, ROWS = BLOCK / LPR;
@@ -102,21 +116,21 @@ layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__
   const int64_t step = (int64_t)gridDim.x * ROWS;
   piece_t cur[NV], next[NV];
   if (kAhead)
-    ld_rows<T, LPR, NV>(x + turn_row((int64_t)blockIdx.x * ROWS, group, rows) * ldx, lane, cols,
+    ld_rows<LOAD, LPR>(x + turn_row((int64_t)blockIdx.x * ROWS, group, rows) * ldx, lane, cols,
                         cur);
   float gm[NV][N], bt[NV][N];
   if constexpr (kAhead) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
-      ld_params(beta, (v * LPR + lane) * N, cols, 0.f, bt[v]);
+      ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+      ld_params<T>(beta, params_f32, (v * LPR + lane) * N, cols, 0.f, bt[v]);
     }
   }
   for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < rows; r0 += step) {
     if (!kAhead)
-      ld_rows<T, LPR, NV>(x + turn_row(r0, group, rows) * ldx, lane, cols, cur);
+      ld_rows<LOAD, LPR>(x + turn_row(r0, group, rows) * ldx, lane, cols, cur);
     else if (r0 + step < rows)
-      ld_rows<T, LPR, NV>(x + turn_row(r0 + step, group, rows) * ldx, lane, cols, next);
+      ld_rows<LOAD, LPR>(x + turn_row(r0 + step, group, rows) * ldx, lane, cols, next);
     const int64_t r = r0 + group;
     float f[NV][N];
     float s = 0.f;
@@ -152,12 +166,12 @@ layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const P* __restrict__
         float o[N];
         if constexpr (!kAhead) {
           __builtin_amdgcn_sched_barrier(0);
-          ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
-          ld_params(beta, (v * LPR + lane) * N, cols, 0.f, bt[v]);
+          ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+          ld_params<T>(beta, params_f32, (v * LPR + lane) * N, cols, 0.f, bt[v]);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(f[v][i] * rstd, gm[v][i], bt[v][i]);
-        st_row(y + r * cols, (v * LPR + lane) * N, cols, pack(o, T{}));
+        st_row<kStream>(y + r * cols, (v * LPR + lane) * N, cols, pack(o, T{}));
       }
       if (lane == 0) {
         if (mean_out) mean_out[r] = mean;
@@ -184,15 +198,16 @@ template <typename T, int EPT> struct BwdFit {
   static constexpr bool kGammaLds = (kAhead ? 2 : 1) * kRow + kSums + EPT > 96;
 };
 
-template <typename T, typename P, int LPR, int EPT, int BLOCK>
-__global__ void __launch_bounds__(BLOCK, 4)
+template <typename T, int LPR, int EPT, Cache LOAD, Cache STORE>
+__global__ void __launch_bounds__(kBwdBlock)
 layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
                      const float* __restrict__ mean, const float* __restrict__ rstd,
-                     const P* __restrict__ gamma, int64_t rows, int cols, T* __restrict__ dx,
-                     P* __restrict__ dgamma, P* __restrict__ dbeta, float* __restrict__ part,
-                     int part_ld) {
+                     const void* __restrict__ gamma, bool params_f32, int64_t rows, int cols,
+                     T* __restrict__ dx, void* __restrict__ dgamma, void* __restrict__ dbeta,
+                     float* __restrict__ part, int part_ld) {
   using Fit = BwdFit<T, EPT>;
-  constexpr int N = Piece<T>::N, NV = EPT / N, ROWS = BLOCK / LPR, WAVES = BLOCK / 64;
+  constexpr int BLOCK = kBwdBlock, WAVES = BLOCK / 64;
+  constexpr int N = Piece<T>::N, NV = EPT / N, ROWS = BLOCK / LPR;
   constexpr bool kGammaLds = Fit::kGammaLds, kHold = Fit::kHold, kAhead = Fit::kAhead;
   __shared__ float red[2][2][WAVES];
   constexpr int kFold = ROWS > 1 ? BLOCK * EPT : 1;
@@ -205,8 +220,8 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
   float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
   if (kAhead && (int64_t)blockIdx.x * ROWS < rows) {
     const int64_t r = turn_row((int64_t)blockIdx.x * ROWS, group, rows);
-    ld_rows<T, LPR, NV>(x + r * ldx, lane, cols, cx);
-    ld_rows<T, LPR, NV>(dy + r * lddy, lane, cols, cd);
+    ld_rows<LOAD, LPR>(x + r * ldx, lane, cols, cx);
+    ld_rows<LOAD, LPR>(dy + r * lddy, lane, cols, cd);
     mu = mean[r], rs = rstd[r];
   }
   float gm[kGammaLds ? 1 : NV][N], ag[NV][N], ab[NV][N];
@@ -214,12 +229,12 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
   for (int v = 0; v < NV; ++v) {
     if constexpr (kGammaLds) {
       float g[N];
-      ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, g);
+      ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, g);
       if (group == 0)
 #pragma unroll
         for (int i = 0; i < N; ++i) fold[(v * LPR + lane) * N + i] = g[i];
     } else {
-      ld_params(gamma, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+      ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, gm[v]);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) ag[v][i] = ab[v][i] = 0.f;
@@ -236,13 +251,13 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
     const int64_t q = turn_row(kAhead ? r0 + step : r0, group, rows);
     if (!kAhead) {
       if constexpr (kHold) {
-        ld_rows<T, LPR, NV>(x + q * ldx, lane, cols, cx);
-        ld_rows<T, LPR, NV>(dy + q * lddy, lane, cols, cd);
+        ld_rows<LOAD, LPR>(x + q * ldx, lane, cols, cx);
+        ld_rows<LOAD, LPR>(dy + q * lddy, lane, cols, cd);
       }
       mu = mean[q], rs = rstd[q];
     } else if (r0 + step < rows) {
-      ld_rows<T, LPR, NV>(x + q * ldx, lane, cols, nx);
-      ld_rows<T, LPR, NV>(dy + q * lddy, lane, cols, nd);
+      ld_rows<LOAD, LPR>(x + q * ldx, lane, cols, nx);
+      ld_rows<LOAD, LPR>(dy + q * lddy, lane, cols, nd);
       nmu = mean[q], nrs = rstd[q];
     }
     // a group past the last row takes its turn (the barriers must meet) with dy = 0
@@ -252,8 +267,8 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
       const int c = (v * LPR + lane) * N;
       float fx[N], fd[N];
       if constexpr (!kHold) {
-        cx[v] = ld_raw<T, false>(x + q * ldx, c, cols);
-        cd[v] = ld_raw<T, false>(dy + q * lddy, c, cols);
+        cx[v] = ld_raw<LOAD, false>(x + q * ldx, c, cols);
+        cd[v] = ld_raw<LOAD, false>(dy + q * lddy, c, cols);
       }
       if (ragged) {
         cx[v] = cut<T>(cx[v], c, cols);
@@ -297,8 +312,8 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
         arrived(cx[v]);
         arrived(cd[v]);
       } else {
-        cx[v] = cut<T>(ld_raw<T, false>(x + q * ldx, c, cols), c, cols);
-        cd[v] = cut<T>(ld_raw<T, false>(dy + q * lddy, c, cols), c, cols);
+        cx[v] = cut<T>(ld_raw<LOAD, false>(x + q * ldx, c, cols), c, cols);
+        cd[v] = cut<T>(ld_raw<LOAD, false>(dy + q * lddy, c, cols), c, cols);
         if (!live) cd[v] = piece_t{0, 0, 0, 0};
       }
       unpack(cx[v], fx, T{});
@@ -310,7 +325,7 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
         ag[v][i] = __builtin_fmaf(fd[i], xh, ag[v][i]);
         ab[v][i] += fd[i];
       }
-      if (live && dx) st_row(dx + r * cols, c, cols, pack(o, T{}));
+      if (live && dx) st_row<STORE>(dx + r * cols, c, cols, pack(o, T{}));
       if constexpr (!kHold || kGammaLds) __builtin_amdgcn_sched_barrier(0);
     }
     if (kAhead) {
@@ -322,7 +337,7 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
   if (!dgamma && !dbeta) return;
 #pragma unroll
   for (int which = 0; which < 2; ++which) {
-    P* out = which == 0 ? dgamma : dbeta;
+    void* out = which == 0 ? dgamma : dbeta;
     if (!out) continue;
     float (&acc)[NV][N] = which == 0 ? ag : ab;
     float* dst = part ? part + ((int64_t)which * gridDim.x + blockIdx.x) * part_ld : nullptr;
@@ -340,7 +355,7 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
 #pragma unroll
         for (int k = 1; k < ROWS; ++k) s += fold[k * LPR * EPT + c];
         if (dst) dst[c] = s;
-        else out[c] = from_f32<P>(s);
+        else st_param<T>(out, params_f32, c, s);
       }
     } else {
 #pragma unroll
@@ -355,7 +370,7 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
           } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (c + k < cols) out[c + k] = from_f32<P>(acc[v][i + k]);
+              if (c + k < cols) st_param<T>(out, params_f32, c + k, acc[v][i + k]);
           }
         }
     }
@@ -392,11 +407,6 @@ layernorm_bwd_params_kernel(const float* __restrict__ part, int blocks, int cols
   }
 }
 
-constexpr int kFwdBlock = 256, kBwdBlock = 512;
-constexpr int64_t kFwdGrid = 256 * 8, kBwdThreads = 256 * 1024;
-
-constexpr int block_of(int lpr, int block) { return lpr > block ? lpr : block; }
-
 // Lanes and elements per lane of a row of `cols` elements.
 struct Shape { int lpr, ept; };
 Shape row_shape(int64_t cols) {
@@ -411,48 +421,70 @@ Shape row_shape(int64_t cols) {
 }
 
 int64_t bwd_blocks(int64_t rows, int64_t cols) {
-  const int lpr = row_shape(cols).lpr;
-  const int block = block_of(lpr, kBwdBlock);
-  const int64_t per = block / lpr, want = (rows + per - 1) / per;
-  if (want <= 4) return 1;
-  return std::min(want, kBwdThreads / block);
+  const int64_t per = kBwdBlock / row_shape(cols).lpr, want = (rows + per - 1) / per;
+  return want <= 4 ? 1 : std::min(want, kBwdGrid);     // 4 turns cost less than another launch
 }
 
-template <typename T, typename P, int LPR, int EPT>
+template <typename T, int LPR, int EPT, Cache LOAD>
 hipError_t fwd(const LayerNormArgs& a, hipStream_t s) {
-  constexpr int B = block_of(LPR, kFwdBlock);
+  constexpr int B = fwd_block(LPR);
   const int64_t blocks = std::min<int64_t>((a.rows + B / LPR - 1) / (B / LPR), kFwdGrid);
-  hipLaunchKernelGGL((layernorm_fwd_kernel<T, P, LPR, EPT, B>), dim3((unsigned)blocks), dim3(B), 0,
-                     s, static_cast<const T*>(a.x), a.ldx, static_cast<const P*>(a.gamma),
-                     static_cast<const P*>(a.beta), a.rows, (int)a.cols, a.eps,
-                     static_cast<T*>(a.y), a.mean, a.rstd);
+  hipLaunchKernelGGL((layernorm_fwd_kernel<T, LPR, EPT, B, LOAD>), dim3((unsigned)blocks), dim3(B),
+                     0, s, static_cast<const T*>(a.x), a.ldx, a.gamma, a.beta,
+                     a.param_dtype == kF32, a.rows, (int)a.cols, a.eps, static_cast<T*>(a.y),
+                     a.mean, a.rstd);
   return hipGetLastError();
 }
 
-template <typename T, typename P, int LPR, int EPT>
+template <typename T, int LPR, int EPT, Cache LOAD, Cache STORE>
 hipError_t bwd(const LayerNormArgs& a, hipStream_t s) {
-  constexpr int B = block_of(LPR, kBwdBlock);
   const int64_t blocks = bwd_blocks(a.rows, a.cols);
   float* part = blocks > 1 ? a.workspace : nullptr;
   const int part_ld = (int)((a.cols + 3) / 4 * 4);
-  hipLaunchKernelGGL((layernorm_bwd_kernel<T, P, LPR, EPT, B>), dim3((unsigned)blocks), dim3(B), 0,
-                     s, static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx,
-                     a.mean, a.rstd, static_cast<const P*>(a.gamma), a.rows, (int)a.cols,
-                     static_cast<T*>(a.y), static_cast<P*>(a.dgamma), static_cast<P*>(a.dbeta),
-                     part, part_ld);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess || !part || (!a.dgamma && !a.dbeta)) return e;
-  hipLaunchKernelGGL((layernorm_bwd_params_kernel<P>), dim3((unsigned)((a.cols + 63) / 64), 2),
-                     dim3(1024), 0, s, part, (int)blocks, (int)a.cols, part_ld,
-                     static_cast<P*>(a.dgamma), static_cast<P*>(a.dbeta));
+  hipLaunchKernelGGL((layernorm_bwd_kernel<T, LPR, EPT, LOAD, STORE>), dim3((unsigned)blocks),
+                     dim3(kBwdBlock), 0, s, static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x),
+                     a.ldx, a.mean, a.rstd, a.gamma, a.param_dtype == kF32, a.rows, (int)a.cols,
+                     static_cast<T*>(a.y), a.dgamma, a.dbeta, part, part_ld);
   return hipGetLastError();
 }
 
-template <typename T, typename P>
+template <typename P>
+hipError_t bwd_params(const LayerNormArgs& a, hipStream_t s) {
+  const int part_ld = (int)((a.cols + 3) / 4 * 4);
+  hipLaunchKernelGGL((layernorm_bwd_params_kernel<P>), dim3((unsigned)((a.cols + 63) / 64), 2),
+                     dim3(1024), 0, s, a.workspace, (int)bwd_blocks(a.rows, a.cols), (int)a.cols,
+                     part_ld, static_cast<P*>(a.dgamma), static_cast<P*>(a.dbeta));
+  return hipGetLastError();
+}
+
+// What streams, by the bytes of one tensor of rows (the caches by the memory hold 256 MiB).
+// Measured over three sets of tensors in turn, so that small ones are found in the caches.
+//   Forward, x kept up to kKeepRows: 8192x4096 bf16 24.2 us (streamed 30.7), above 2048x14336
+//   f32 63.4 us streamed (kept 65.7), 32768x4096 f32 191 us (201). y streams: 24.2 us against
+//   30.7 with 8192x4096 bf16, 9.8 against 10.8 with 2048x4096, 53.3 against 54.0 with 8192x4096
+//   f32. The quantize pass that reads y next then runs longer: addition, norm and quantize
+//   together take 82.5 us at 8192x4096 with y streamed and 79.5 us with y kept, 29.4 and 29.8
+//   us at 2048x4096.
+//   Backward, dy and x kept up to kKeepGrad: 2048x4096 bf16 19.8 us (streamed 22.7), 8192x4096
+//   49.0 us (43.9). dx kept up to kKeepRows: 8192x4096 bf16 43.9 us (streamed 47.8), above
+//   16384x4096 bf16 77.7 us streamed (kept 80.6), 32768x4096 f32 293 us (312).
+constexpr int64_t kKeepGrad = 24 << 20, kKeepRows = 96 << 20;
+
+template <typename T, int LPR, int EPT>
+hipError_t by_size(const LayerNormArgs& a, bool backward, hipStream_t s) {
+  const int64_t bytes = a.rows * a.cols * (int64_t)sizeof(T);
+  if (!backward)
+    return bytes <= kKeepRows ? fwd<T, LPR, EPT, kKeep>(a, s) : fwd<T, LPR, EPT, kStream>(a, s);
+  if (bytes <= kKeepGrad) return bwd<T, LPR, EPT, kKeep, kKeep>(a, s);
+  return bytes <= kKeepRows ? bwd<T, LPR, EPT, kStream, kKeep>(a, s)
+                          : bwd<T, LPR, EPT, kStream, kStream>(a, s);
+}
+
+template <typename T>
 hipError_t by_shape(const LayerNormArgs& a, bool backward, hipStream_t s) {
   const Shape k = row_shape(a.cols);
 #define FP8LIN_LN(L, E) \
-  if (k.lpr == L && k.ept == E) return backward ? bwd<T, P, L, E>(a, s) : fwd<T, P, L, E>(a, s);
+  if (k.lpr == L && k.ept == E) return by_size<T, L, E>(a, backward, s);
   FP8LIN_LN(16, 8)
   FP8LIN_LN(64, 8)
   FP8LIN_LN(64, 16)
@@ -473,12 +505,12 @@ int64_t layernorm_bwd_workspace(int64_t rows, int64_t cols) {
 }
 
 hipError_t launch_layernorm(const LayerNormArgs& a, bool backward, hipStream_t s) {
-  const bool same = a.param_dtype == a.dtype;
-  if (a.dtype == kBF16)
-    return same ? by_shape<BF16, BF16>(a, backward, s) : by_shape<BF16, float>(a, backward, s);
-  if (a.dtype == kF16)
-    return same ? by_shape<F16, F16>(a, backward, s) : by_shape<F16, float>(a, backward, s);
-  return by_shape<float, float>(a, backward, s);
+  const hipError_t e = a.dtype == kBF16  ? by_shape<BF16>(a, backward, s)
+                       : a.dtype == kF16 ? by_shape<F16>(a, backward, s)
+                                         : by_shape<float>(a, backward, s);
+  if (e != hipSuccess || !backward || !a.workspace) return e;
+  if (a.param_dtype == kBF16) return bwd_params<BF16>(a, s);
+  return a.param_dtype == kF16 ? bwd_params<F16>(a, s) : bwd_params<float>(a, s);
 }
 
 }  // namespace fp8lin

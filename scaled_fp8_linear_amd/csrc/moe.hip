@@ -259,7 +259,7 @@ __device__ __forceinline__ void zero_padding(const int32_t* source, int64_t r0, 
     T* row = out + (r0 + i) * cols;
 #pragma unroll
     for (int v = 0; v < kMovePieces; ++v)
-      st_row(row, c0 + (v * 64 + lane) * Piece<T>::N, cols, piece_t{0, 0, 0, 0});
+      st_row<kStream>(row, c0 + (v * 64 + lane) * Piece<T>::N, cols, piece_t{0, 0, 0, 0});
   }
 }
 
@@ -285,7 +285,7 @@ moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restr
   const T* src = x + t * ldx;
   piece_t v[kMovePieces];
 #pragma unroll
-  for (int i = 0; i < kMovePieces; ++i) v[i] = ld_raw(src, c0 + i * 64 * N, cols);
+  for (int i = 0; i < kMovePieces; ++i) v[i] = ld_raw<kKeep>(src, c0 + i * 64 * N, cols);
 #pragma unroll
   for (int i = 0; i < kMovePieces; ++i) v[i] = cut<T>(v[i], c0 + i * 64 * N, cols);
   for (int j = 0; j < topk; ++j) {
@@ -293,7 +293,7 @@ moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restr
     if (r < 0) continue;
     T* dst = xs + (int64_t)r * cols;
 #pragma unroll
-    for (int i = 0; i < kMovePieces; ++i) st_row(dst, c0 + i * 64 * N, cols, v[i]);
+    for (int i = 0; i < kMovePieces; ++i) st_row<kStream>(dst, c0 + i * 64 * N, cols, v[i]);
   }
 }
 
@@ -330,7 +330,7 @@ moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __rest
       if (r[q] < 0) continue;
 #pragma unroll
       for (int i = 0; i < kSumPieces; ++i)
-        v[q][i] = ld_raw(ys + r[q] * ldys, c0 + i * 64 * N, cols);
+        v[q][i] = ld_raw<kStream>(ys + r[q] * ldys, c0 + i * 64 * N, cols);
     }
 #pragma unroll
     for (int q = 0; q < U; ++q) {
@@ -346,7 +346,7 @@ moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __rest
   }
 #pragma unroll
   for (int i = 0; i < kSumPieces; ++i)
-    st_row(y + t * cols, c0 + i * 64 * N, cols, pack(acc[i], T{}));
+    st_row<kStream>(y + t * cols, c0 + i * 64 * N, cols, pack(acc[i], T{}));
 }
 
 // W waves per token read dy[t] once per J choices, write w dy to their rows and sum dy ys of
@@ -384,10 +384,10 @@ moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restri
       dot[q] = 0.f;
     }
     for (int c = lt * N; c < cols; c += W * 64 * N) {
-      piece_t pg = ld_raw(g, c, cols), py[J];
+      piece_t pg = ld_raw<kStream>(g, c, cols), py[J];
 #pragma unroll
       for (int q = 0; q < J; ++q)
-        if (r[q] >= 0) py[q] = ld_raw(ys + r[q] * ldys, c, cols);
+        if (r[q] >= 0) py[q] = ld_raw<kStream>(ys + r[q] * ldys, c, cols);
       float fg[N];
       unpack(cut<T>(pg, c, cols), fg, T{});
 #pragma unroll
@@ -400,7 +400,7 @@ moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restri
           dot[q] = __builtin_fmaf(fg[n], fy[n], dot[q]);
           o[n] = w[q] * fg[n];
         }
-        st_row(dys + (int64_t)r[q] * cols, c, cols, pack(o, T{}));
+        st_row<kStream>(dys + (int64_t)r[q] * cols, c, cols, pack(o, T{}));
       }
     }
     if constexpr (W == 1) {
@@ -501,7 +501,7 @@ hipError_t combine_rows(const MoeArgs& a, hipStream_t s) {
 }
 template <typename T>
 hipError_t combine(const MoeArgs& a, hipStream_t s) {
-  return a.topk <= 4 ? combine_rows<T, 4>(a, s) : combine_rows<T, 8>(a, s);
+  return combine_rows<T, 4>(a, s);
 }
 
 template <typename T, int W, int J>

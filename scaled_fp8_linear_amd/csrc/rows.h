@@ -24,11 +24,22 @@ typedef unsigned piece_any_t __attribute__((ext_vector_type(4), aligned(2)));
 typedef unsigned half_piece_any_t __attribute__((ext_vector_type(2), aligned(2)));
 typedef unsigned dword_any_t __attribute__((aligned(2)));
 
+// Cached pieces, or streaming ones (non-temporal: passed through the caches rather than kept
+// there). Which is faster for a tensor that is read or written once depends on the mix of reads
+// and writes around it, so each kernel states what it uses and what it measured.
+enum Cache { kKeep = 0, kStream = 1 };
+
+template <Cache C>
 __device__ __forceinline__ piece_t ld_piece(const void* p) {
-  return *reinterpret_cast<const piece_any_t*>(p);
+  const piece_any_t* q = reinterpret_cast<const piece_any_t*>(p);
+  if constexpr (C == kStream) return __builtin_nontemporal_load(q);
+  else return *q;
 }
+template <Cache C>
 __device__ __forceinline__ void st_piece(void* p, piece_t v) {
-  *reinterpret_cast<piece_any_t*>(p) = v;
+  piece_any_t* q = reinterpret_cast<piece_any_t*>(p);
+  if constexpr (C == kStream) __builtin_nontemporal_store((piece_any_t)v, q);
+  else *q = v;
 }
 
 // row + c for a column 0 <= c < 2^30. Where `row` is the same for a whole wave this is a
@@ -107,10 +118,10 @@ __device__ __forceinline__ piece_t pack(const float (&f)[4], float) {
 // the piece is cut off by the row's end or lies past it), and cut moves a cut-off piece's
 // elements down and sets what is past the row to 0. Nothing outside the row is touched; rows
 // shorter than a piece (kShort: they may be) are read element by element.
-template <typename T, bool kShort = true>
+template <Cache C, bool kShort = true, typename T>
 __device__ __forceinline__ piece_t ld_raw(const T* row, int c, int cols) {
   constexpr int N = Piece<T>::N;
-  if (!kShort || cols >= N) return ld_piece(elem_at(row, c + N <= cols ? c : cols - N));
+  if (!kShort || cols >= N) return ld_piece<C>(elem_at(row, c + N <= cols ? c : cols - N));
   piece_t v = {0u, 0u, 0u, 0u};
   if (c == 0) {
     if constexpr (sizeof(T) == 4) {
@@ -142,14 +153,14 @@ __device__ __forceinline__ piece_t cut(piece_t v, int c, int cols) {
 }
 template <typename T>
 __device__ __forceinline__ piece_t ld_row(const T* row, int c, int cols) {
-  return cut<T>(ld_raw(row, c, cols), c, cols);
+  return cut<T>(ld_raw<kKeep>(row, c, cols), c, cols);
 }
-template <typename T>
+template <Cache C, typename T>
 __device__ __forceinline__ void st_row(T* row, int c, int cols, piece_t v) {
   constexpr int N = Piece<T>::N;
   T* p = elem_at(row, c);
   if (c + N <= cols) {
-    st_piece(p, v);
+    st_piece<C>(p, v);
   } else if (c < cols) {                     // 8, 4 and 2 bytes of what is left
     const int left = (cols - c) * (int)sizeof(T);
     if (left & 8) {
