@@ -44,6 +44,7 @@ class Fp8Error(RuntimeError):
 
 
 _lib = None
+_binding = None                 # the native checks and calls of the row operators (binding.cpp)
 
 _i64, _i32, _int, _vp = ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_void_p
 
@@ -93,7 +94,24 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8_version.restype = ctypes.c_char_p
     lib.fp8_version.argtypes = []
     _lib = lib
+    if _binding is not None:
+        _bind(lib)
     return lib
+
+
+def _bind(lib) -> None:
+    """Give the native binding the library's entry points and this module's helpers."""
+    global _binding
+    if _binding is None:
+        try:
+            from . import _binding as native
+        except ImportError as e:
+            raise RuntimeError("_binding.so is missing or does not load: build it with `python -m "
+                               f"scaled_fp8_linear_amd.build` ({e})") from e
+        _binding = native
+    at = {n: ctypes.cast(getattr(lib, n), _vp).value for n in EXPORTS}
+    _binding.bind(at, _new, _check, _cur_device or torch.cuda.current_device,
+                  _raw_stream or (lambda d: torch.cuda.current_stream(d).cuda_stream))
 
 
 def _check(fn: str, status: int) -> None:
@@ -549,78 +567,23 @@ def fp8_unpad_varlen(x_pad, cu_seqlens, cu_seqlens_pad, x=None, stream=None):
 
 
 # ------------------------------------------------------- layer norm, expert dispatch
-_DT = {torch.bfloat16: FP8_DT_BF16, torch.float16: FP8_DT_F16, torch.float32: FP8_DT_F32}
-_I32 = (torch.int32,)
-_F32 = (torch.float32,)
-
-
-def _rows2d(t, name, dev=None, dtype=None, cols=None, rows=None):
-    """Check a [rows, cols] input whose rows may be a cut out of a wider tensor; returns its
-    row stride in elements (at least the width; 0- and 1-row tensors may have any)."""
-    if t.dtype not in _DT:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected bfloat16, float16 or float32")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must be 2-D [rows, cols], got shape {tuple(t.shape)}")
-    r, c = t.shape
-    if (cols is not None and c != cols) or (rows is not None and r != rows):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         f"({'any' if rows is None else rows}, {'any' if cols is None else cols})")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the operands on {dev}")
-    ld, inner = t.stride()
-    if c > 1 and inner != 1:
-        raise ValueError(f"{name}: the columns of a row must be contiguous, stride {inner}")
-    if r <= 1:
-        return max(ld, c)
-    if ld < c:
-        raise ValueError(f"{name}: rows overlap (stride {ld}, {c} columns)")
-    return ld
-
-
-def _dptr(t):
-    """Address of a device tensor whose layout was checked (any row stride)."""
-    if t is None:
-        return None
-    if not t.is_cuda:
-        raise ValueError("fp8lin takes device tensors")
-    return t.data_ptr()
-
-
-def _launch_on(x, stream):
-    """Checks before the call's own allocations: a device tensor, on the current device
-    (kernels go to the current device's stream)."""
-    if not x.is_cuda:
-        raise ValueError("fp8lin takes device tensors")
-    cur = _cur_device() if _cur_device is not None else torch.cuda.current_device()
-    if x.device.index != cur:
-        raise ValueError(f"the operands are on {x.device}, the current device is cuda:{cur}")
-    if stream is not None and stream.device.index != cur:
-        raise ValueError(f"the stream is on {stream.device}, the current device is cuda:{cur}")
+# The checks and calls of these operators are native (csrc/binding.cpp): for a few tokens their
+# time in Python was more than the kernels'.
+_NAMED = {"BFloat16": torch.bfloat16, "Half": torch.float16, "Float": torch.float32,
+          "Int": torch.int32, "Byte": torch.uint8}
 
 
 def _new(shape, dtype, dev, stream):
     """An output or workspace in the memory pool of the stream that will write it, so that a
     call on a stream other than the current one never reuses memory in use on the latter."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=_NAMED[dtype], device=dev)
 
 
-def _params(dtype, cols, dev, *named):
-    """The common dtype of the given parameter tensors [cols]: the rows' dtype or float32."""
-    pdt = None
-    for t, name in named:
-        if t is None:
-            continue
-        if pdt is None:
-            if t.dtype != dtype and t.dtype != torch.float32:
-                raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype} or float32")
-            pdt = t.dtype
-        _need(t, name, (cols,), (pdt,), dev)
-    return pdt
+def _native():
+    if _binding is None or _lib is None:
+        _bind(load())
+    return _binding
 
 
 def fp8_layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, y=None, mean=None, rstd=None,
@@ -628,25 +591,7 @@ def fp8_layernorm_fwd(x, gamma=None, beta=None, eps=1e-5, y=None, mean=None, rst
     """Layer norm of each row of x [rows, cols] (bf16, f16 or f32; rows may be strided).
     gamma, beta [cols] in x's dtype or float32, or None. Returns (y, mean, rstd): y in x's
     dtype, the statistics float32 [rows] (None without ``want_stats`` unless passed)."""
-    ldx = _rows2d(x, "x")
-    rows, cols = x.shape
-    dev = x.device
-    pdt = _params(x.dtype, cols, dev, (gamma, "gamma"), (beta, "beta")) or x.dtype
-    _need(y, "y", (rows, cols), (x.dtype,), dev)
-    _need(mean, "mean", (rows,), _F32, dev)
-    _need(rstd, "rstd", (rows,), _F32, dev)
-    _launch_on(x, stream)
-    if y is None:
-        y = _new((rows, cols), x.dtype, dev, stream)
-    if want_stats:
-        if mean is None:
-            mean = _new((rows,), torch.float32, dev, stream)
-        if rstd is None:
-            rstd = _new((rows,), torch.float32, dev, stream)
-    _check("fp8_layernorm_fwd", load().fp8_layernorm_fwd(
-        x.data_ptr(), ldx, _dptr(gamma), _dptr(beta), rows, cols, _DT[x.dtype], _DT[pdt],
-        float(eps), y.data_ptr(), _dptr(mean), _dptr(rstd), _stream(stream)))
-    return y, mean, rstd
+    return _native().layernorm_fwd(x, gamma, beta, eps, y, mean, rstd, want_stats, stream)
 
 
 def fp8_layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, dgamma=None, dbeta=None,
@@ -656,46 +601,11 @@ def fp8_layernorm_bwd(dy, x, mean, rstd, gamma=None, dx=None, dgamma=None, dbeta
     (dx, dgamma, dbeta), None for those not wanted and not passed. dgamma and dbeta have
     gamma's dtype (``param_dtype``, else x's dtype, without gamma). ``workspace``: a uint8
     tensor of at least fp8_layernorm_bwd_workspace(rows, cols) bytes, else allocated."""
-    ldx = _rows2d(x, "x")
-    rows, cols = x.shape
-    dev = x.device
-    lddy = _rows2d(dy, "dy", dev, x.dtype, cols, rows)
-    _need(mean, "mean", (rows,), _F32, dev)
-    _need(rstd, "rstd", (rows,), _F32, dev)
-    if mean is None or rstd is None:
-        raise ValueError("mean and rstd of the forward are needed")
-    pdt = _params(x.dtype, cols, dev, (gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta"))
-    if pdt is None:
-        pdt = x.dtype if param_dtype is None else param_dtype
-        if pdt not in (x.dtype, torch.float32):
-            raise ValueError(f"param_dtype {pdt}, expected {x.dtype} or float32")
-    _need(dx, "dx", (rows, cols), (x.dtype,), dev)
-    _launch_on(x, stream)
-    if want_dx and dx is None:
-        dx = _new((rows, cols), x.dtype, dev, stream)
-    if want_dgamma and dgamma is None:
-        dgamma = _new((cols,), pdt, dev, stream)
-    if want_dbeta and dbeta is None:
-        dbeta = _new((cols,), pdt, dev, stream)
-    need = 0
-    if dgamma is not None or dbeta is not None:
-        need = fp8_layernorm_bwd_workspace(rows, cols)
-        workspace = _workspace(workspace, need, dev, stream)
-    _check("fp8_layernorm_bwd", load().fp8_layernorm_bwd(
-        dy.data_ptr(), lddy, x.data_ptr(), ldx, mean.data_ptr(), rstd.data_ptr(), _dptr(gamma),
-        rows, cols, _DT[x.dtype], _DT[pdt], _dptr(dx), _dptr(dgamma), _dptr(dbeta),
-        _dptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)))
-    return dx, dgamma, dbeta
-
-
-def _workspace(t, need, dev, stream):
-    if t is None:
-        return _new((need,), torch.uint8, dev, stream) if need else None
-    if t.dtype != torch.uint8 or not t.is_contiguous() or t.device != dev:
-        raise ValueError(f"workspace must be a contiguous uint8 tensor on {dev}")
-    if t.numel() < need:
-        raise ValueError(f"workspace holds {t.numel()} bytes, needs {need}")
-    return t
+    if param_dtype is not None and param_dtype not in (x.dtype, torch.float32):
+        raise ValueError(f"param_dtype {param_dtype}, expected {x.dtype} or float32")
+    return _native().layernorm_bwd(dy, x, mean, rstd, gamma, dx, dgamma, dbeta, want_dx,
+                                   want_dgamma, want_dbeta, param_dtype is torch.float32,
+                                   workspace, stream)
 
 
 def fp8_layernorm_bwd_workspace(rows, cols):
@@ -729,118 +639,32 @@ def fp8_moe_sort(expert_idx, experts, multiple=16, slot=None, source=None, count
     outside [0, experts) drops its pair) by expert, stably, every expert's rows padded to a
     multiple of ``multiple``. Returns int32 (slot [tokens, topk], source [rows], counts
     [experts], offsets [experts + 1]); see fp8lin.h. Nothing reaches the host."""
-    if expert_idx.dim() != 2:
-        raise ValueError(f"expert_idx must be 2-D [tokens, topk], got {tuple(expert_idx.shape)}")
-    tokens, topk = expert_idx.shape
-    dev = expert_idx.device
-    _need(expert_idx, "expert_idx", (tokens, topk), (torch.int32, torch.int64))
-    rows = fp8_moe_rows(tokens, topk, experts, multiple)
-    _need(slot, "slot", (tokens, topk), _I32, dev)
-    _need(source, "source", (rows,), _I32, dev)
-    _need(counts, "counts", (experts,), _I32, dev)
-    _need(offsets, "offsets", (experts + 1,), _I32, dev)
-    _launch_on(expert_idx, stream)
-    if slot is None:
-        slot = _new((tokens, topk), torch.int32, dev, stream)
-    if source is None:
-        source = _new((rows,), torch.int32, dev, stream)
-    if counts is None:
-        counts = _new((experts,), torch.int32, dev, stream)
-    if offsets is None:
-        offsets = _new((experts + 1,), torch.int32, dev, stream)
-    workspace = _workspace(workspace, fp8_moe_sort_workspace(tokens, topk, experts), dev, stream)
-    _check("fp8_moe_sort", load().fp8_moe_sort(
-        expert_idx.data_ptr(), expert_idx.element_size(), tokens, topk, int(experts),
-        int(multiple), slot.data_ptr(), source.data_ptr(), counts.data_ptr(), offsets.data_ptr(),
-        _dptr(workspace), 0 if workspace is None else workspace.numel(), _stream(stream)))
-    return slot, source, counts, offsets
-
-
-def _plan(slot, source, dev):
-    """(tokens, topk, rows) of a sort's index tensors."""
-    if slot.dim() != 2:
-        raise ValueError(f"slot must be 2-D [tokens, topk], got {tuple(slot.shape)}")
-    _need(slot, "slot", slot.shape, _I32, dev)
-    if source is not None:
-        if source.dim() != 1:
-            raise ValueError(f"source must be 1-D [rows], got {tuple(source.shape)}")
-        _need(source, "source", source.shape, _I32, dev)
-    return slot.shape[0], slot.shape[1], 0 if source is None else source.shape[0]
+    return _native().moe_sort(expert_idx, experts, multiple, slot, source, counts, offsets,
+                              workspace, stream)
 
 
 def fp8_moe_dispatch(x, slot, source, xs=None, stream=None):
     """xs [rows, cols]: the tokens' rows of x [tokens, cols] (rows may be strided) in the order
     of the sort, 0 in the padding rows."""
-    ldx = _rows2d(x, "x")
-    dev, cols = x.device, x.shape[1]
-    tokens, topk, rows = _plan(slot, source, dev)
-    if x.shape[0] != tokens:
-        raise ValueError(f"x has {x.shape[0]} rows, slot is for {tokens} tokens")
-    _need(xs, "xs", (rows, cols), (x.dtype,), dev)
-    _launch_on(x, stream)
-    if xs is None:
-        xs = _new((rows, cols), x.dtype, dev, stream)
-    _check("fp8_moe_dispatch", load().fp8_moe_dispatch(
-        x.data_ptr(), ldx, slot.data_ptr(), source.data_ptr(), tokens, topk, rows, cols,
-        _DT[x.dtype], xs.data_ptr(), _stream(stream)))
-    return xs
+    return _native().moe_dispatch(x, slot, source, xs, stream)
 
 
 def fp8_moe_dispatch_bwd(dxs, slot, dx=None, stream=None):
     """dx [tokens, cols]: the dispatch's gradient, each token's rows of dxs [rows, cols] (may be
     strided) added up."""
-    ld = _rows2d(dxs, "dxs")
-    dev, (rows, cols) = dxs.device, dxs.shape
-    tokens, topk, _ = _plan(slot, None, dev)
-    _need(dx, "dx", (tokens, cols), (dxs.dtype,), dev)
-    _launch_on(dxs, stream)
-    if dx is None:
-        dx = _new((tokens, cols), dxs.dtype, dev, stream)
-    _check("fp8_moe_dispatch_bwd", load().fp8_moe_dispatch_bwd(
-        dxs.data_ptr(), ld, slot.data_ptr(), tokens, topk, rows, cols, _DT[dxs.dtype],
-        dx.data_ptr(), _stream(stream)))
-    return dx
+    return _native().moe_dispatch_bwd(dxs, slot, dx, stream)
 
 
 def fp8_moe_combine(ys, slot, weights, y=None, stream=None):
     """y [tokens, cols]: each token's rows of ys [rows, cols] (may be strided) added with the
     router's weights, float32 [tokens, topk]; dropped pairs add nothing."""
-    ld = _rows2d(ys, "ys")
-    dev, (rows, cols) = ys.device, ys.shape
-    tokens, topk, _ = _plan(slot, None, dev)
-    _need(weights, "weights", (tokens, topk), _F32, dev)
-    _need(y, "y", (tokens, cols), (ys.dtype,), dev)
-    _launch_on(ys, stream)
-    if y is None:
-        y = _new((tokens, cols), ys.dtype, dev, stream)
-    _check("fp8_moe_combine", load().fp8_moe_combine(
-        ys.data_ptr(), ld, slot.data_ptr(), weights.data_ptr(), tokens, topk, rows, cols,
-        _DT[ys.dtype], y.data_ptr(), _stream(stream)))
-    return y
+    return _native().moe_combine(ys, slot, weights, y, stream)
 
 
 def fp8_moe_combine_bwd(dy, ys, slot, source, weights, dys=None, dw=None, stream=None):
     """The combine's gradients (dys [rows, cols], dw float32 [tokens, topk]) from dy
     [tokens, cols] and ys; padding rows of dys and dropped pairs of dw are 0."""
-    ldys = _rows2d(ys, "ys")
-    dev, cols = ys.device, ys.shape[1]
-    tokens, topk, rows = _plan(slot, source, dev)
-    if ys.shape[0] != rows:
-        raise ValueError(f"ys has {ys.shape[0]} rows, source {rows}")
-    lddy = _rows2d(dy, "dy", dev, ys.dtype, cols, tokens)
-    _need(weights, "weights", (tokens, topk), _F32, dev)
-    _need(dys, "dys", (rows, cols), (ys.dtype,), dev)
-    _need(dw, "dw", (tokens, topk), _F32, dev)
-    _launch_on(ys, stream)
-    if dys is None:
-        dys = _new((rows, cols), ys.dtype, dev, stream)
-    if dw is None:
-        dw = _new((tokens, topk), torch.float32, dev, stream)
-    _check("fp8_moe_combine_bwd", load().fp8_moe_combine_bwd(
-        dy.data_ptr(), lddy, ys.data_ptr(), ldys, slot.data_ptr(), source.data_ptr(),
-        weights.data_ptr(), tokens, topk, rows, cols, _DT[ys.dtype], dys.data_ptr(),
-        dw.data_ptr(), _stream(stream)))
-    return dys, dw
+    return _native().moe_combine_bwd(dy, ys, slot, source, weights, dys, dw, stream)
 
 
 def fp8_last_error() -> str:

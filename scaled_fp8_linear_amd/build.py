@@ -1,4 +1,5 @@
-"""Build ``libfp8lin.so`` (the gfx950 kernels and the C ABI) in-tree with hipcc.
+"""Build ``libfp8lin.so`` (the gfx950 kernels and the C ABI) in-tree with hipcc, and
+``_binding.so`` (the CPython side of the row operators) with g++ against torch's headers.
 
 Usage: ``python -m scaled_fp8_linear_amd.build`` (or ``__graft_entry__.build()``).
 Every call recompiles; object files go to ``scaled_fp8_linear_amd/_build/``.
@@ -15,6 +16,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libfp8lin.so")
+BINDING = os.path.join(PKG, "_binding.so")
 ROOT = os.path.dirname(PKG)
 
 SOURCES = ["abi.cpp", "quantize_amax.hip", "quantize_block.hip", "scale_update.hip",
@@ -50,10 +52,31 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _compile_binding() -> None:
+    import sysconfig
+
+    import torch
+    home = os.path.dirname(torch.__file__)
+    lib = os.path.join(home, "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-fPIC", "-shared", "-std=c++17", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-isystem", os.path.join(home, "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{lib}", f"-Wl,-rpath,{lib}",
+           "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with ThreadPoolExecutor(min(8, len(SOURCES))) as ex:
+    with ThreadPoolExecutor(min(8, len(SOURCES) + 1)) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
@@ -61,7 +84,7 @@ def build(verbose: bool = False) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     if verbose:
-        print(f"built {LIB}")
+        print(f"built {LIB}\nbuilt {BINDING}")
     return LIB
 
 

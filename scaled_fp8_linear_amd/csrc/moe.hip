@@ -264,7 +264,10 @@ __device__ __forceinline__ void zero_padding(const int32_t* source, int64_t r0, 
 }
 
 // One wave per (token, kMovePieces pieces a lane of the row): loaded once, stored to each of
-// the token's rows. The waves after those zero the padding rows.
+// the token's rows. The waves after those zero the padding rows. Bound by the writes of the
+// sorted rows: 8192 tokens to 8 of 64 experts, width 4096 bf16 in 109.6 us, 5.6 TB/s. They
+// stream (117.8 us kept, and no size was found where that cost); the tokens' rows are kept, 122
+// us with the sort against 136 us streamed.
 template <typename T>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slot,
@@ -297,14 +300,19 @@ moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restr
   }
 }
 
-// One wave per (token, kSumPieces pieces a lane of the row): the token's rows, U in flight,
-// summed in the order of the choices in float32 and rounded once.
-template <typename T, int U>
+// One wave per (token, kSumPieces pieces a lane of the row): the token's rows, two in flight,
+// summed in the order of the choices in float32 and rounded once. Bound by the reads of the
+// sorted rows: 8192 tokens, 8 of 64 experts, width 4096 bf16 in 99.5 us, 5.9 TB/s. More rows in
+// flight leave fewer waves on a unit: four take as long there and 30.8 us where two take 25.1
+// (4096 tokens, 8 of 64, width 1024 f32), one takes 12.8 us where two take 11.4 (1024 tokens,
+// width 2048 bf16).
+constexpr int kSumRows = 2;
+template <typename T, Cache C>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict__ slot,
                    const float* __restrict__ weights, int64_t tokens, int topk, int64_t rows,
                    int cols, uint32_t chunks, T* __restrict__ y) {
-  constexpr int N = Piece<T>::N, kCols = 64 * N * kSumPieces;
+  constexpr int N = Piece<T>::N, kCols = 64 * N * kSumPieces, U = kSumRows;
   const int lane = threadIdx.x % 64;
   const uint32_t u = grid_wave();
   const int64_t t = u / chunks;
@@ -330,7 +338,7 @@ moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __rest
       if (r[q] < 0) continue;
 #pragma unroll
       for (int i = 0; i < kSumPieces; ++i)
-        v[q][i] = ld_raw<kStream>(ys + r[q] * ldys, c0 + i * 64 * N, cols);
+        v[q][i] = ld_raw<C>(ys + r[q] * ldys, c0 + i * 64 * N, cols);
     }
 #pragma unroll
     for (int q = 0; q < U; ++q) {
@@ -346,13 +354,13 @@ moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __rest
   }
 #pragma unroll
   for (int i = 0; i < kSumPieces; ++i)
-    st_row<kStream>(y + t * cols, c0 + i * 64 * N, cols, pack(acc[i], T{}));
+    st_row<C>(y + t * cols, c0 + i * 64 * N, cols, pack(acc[i], T{}));
 }
 
 // W waves per token read dy[t] once per J choices, write w dy to their rows and sum dy ys of
 // each (lanes, then waves, in a fixed order). The workgroups after the tokens' zero the
 // padding rows.
-template <typename T, int W, int J>
+template <typename T, int W, int J, Cache C>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ ys,
                        int64_t ldys, const int32_t* __restrict__ slot,
@@ -384,10 +392,10 @@ moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restri
       dot[q] = 0.f;
     }
     for (int c = lt * N; c < cols; c += W * 64 * N) {
-      piece_t pg = ld_raw<kStream>(g, c, cols), py[J];
+      piece_t pg = ld_raw<C>(g, c, cols), py[J];
 #pragma unroll
       for (int q = 0; q < J; ++q)
-        if (r[q] >= 0) py[q] = ld_raw<kStream>(ys + r[q] * ldys, c, cols);
+        if (r[q] >= 0) py[q] = ld_raw<C>(ys + r[q] * ldys, c, cols);
       float fg[N];
       unpack(cut<T>(pg, c, cols), fg, T{});
 #pragma unroll
@@ -400,7 +408,7 @@ moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restri
           dot[q] = __builtin_fmaf(fg[n], fy[n], dot[q]);
           o[n] = w[q] * fg[n];
         }
-        st_row<kStream>(dys + (int64_t)r[q] * cols, c, cols, pack(o, T{}));
+        st_row<C>(dys + (int64_t)r[q] * cols, c, cols, pack(o, T{}));
       }
     }
     if constexpr (W == 1) {
@@ -443,17 +451,19 @@ hipError_t sort_steps(const MoeSortArgs& a, const SortPlan& plan, hipStream_t s)
   const unsigned blocks = (unsigned)plan.blocks;
   int32_t* block_counts = blocks > 1 ? a.workspace : nullptr;
   int32_t* totals = plan.scan ? a.workspace + plan.blocks * a.experts : nullptr;
-  if (block_counts) {
-    hipLaunchKernelGGL((moe_count_kernel<S, I>), dim3(blocks), dim3(kSortBlock), 0, s, idx,
-                       a.pairs, a.experts, block_counts);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (totals) {
-    hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)(a.experts + 63) / 64), dim3(kSortBlock), 0,
-                       s, block_counts, plan.blocks, a.experts, totals);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  if constexpr (S > 1) {                       // S = 1 is for one workgroup
+    if (block_counts) {
+      hipLaunchKernelGGL((moe_count_kernel<S, I>), dim3(blocks), dim3(kSortBlock), 0, s, idx,
+                         a.pairs, a.experts, block_counts);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (totals) {
+      hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)(a.experts + 63) / 64), dim3(kSortBlock),
+                         0, s, block_counts, plan.blocks, a.experts, totals);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
   }
   const unsigned lds = (kSortWaves * (unsigned)a.experts + 2 * kSortBlock) * sizeof(int);
   hipLaunchKernelGGL((moe_sort_kernel<S, I>), dim3(blocks), dim3(kSortBlock), lds, s, idx, a.pairs,
@@ -490,10 +500,20 @@ hipError_t dispatch(const MoeArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename T, int U>
+// Tensors of rows up to 96 MiB together are kept in the caches, larger ones stream. Measured over
+// three sets of tensors in turn: the combine of 4096 tokens, 8 of 64, width 1024 bf16 (72 MiB)
+// takes 13.6 us kept and 15.1 us streamed, with 2 of 8 and width 4096 (97 MiB) 21.5 and 18.8 us;
+// the combine's gradient of 2000 tokens, 2 of 8, width 4096 (78 MiB) 14.9 and 16.9 us, of 4096
+// tokens (160 MiB) 35.1 and 31.7 us.
+constexpr int64_t kKeepBytes = 96 << 20;
+bool keeps(const MoeArgs& a, int64_t rows) {
+  return rows * a.cols * (a.dtype == kF32 ? 4 : 2) <= kKeepBytes;
+}
+
+template <typename T, Cache C>
 hipError_t combine_rows(const MoeArgs& a, hipStream_t s) {
   const uint32_t chunks = row_chunks<T>(a.cols, kSumPieces);
-  hipLaunchKernelGGL((moe_combine_kernel<T, U>), dim3(move_blocks(a.tokens * chunks)),
+  hipLaunchKernelGGL((moe_combine_kernel<T, C>), dim3(move_blocks(a.tokens * chunks)),
                      dim3(kMoveBlock), 0, s, static_cast<const T*>(a.ys), a.ldys, a.slot,
                      a.weights, a.tokens, a.topk, a.rows, (int)a.cols, chunks,
                      static_cast<T*>(a.out));
@@ -501,31 +521,37 @@ hipError_t combine_rows(const MoeArgs& a, hipStream_t s) {
 }
 template <typename T>
 hipError_t combine(const MoeArgs& a, hipStream_t s) {
-  return combine_rows<T, 4>(a, s);
+  return keeps(a, a.rows + a.tokens) ? combine_rows<T, kKeep>(a, s)
+                                     : combine_rows<T, kStream>(a, s);
 }
 
-template <typename T, int W, int J>
+template <typename T, int W, int J, Cache C>
 hipError_t combine_bwd_rows(const MoeArgs& a, hipStream_t s) {
   const uint32_t chunks = row_chunks<T>(a.cols, kMovePieces);
   const int64_t per = kMoveWaves / W;
   const uint32_t token_blocks = (uint32_t)((a.tokens + per - 1) / per);
   const unsigned blocks = token_blocks + move_blocks(zero_waves(a.rows, chunks));
-  hipLaunchKernelGGL((moe_combine_bwd_kernel<T, W, J>), dim3(blocks), dim3(kMoveBlock), 0, s,
+  hipLaunchKernelGGL((moe_combine_bwd_kernel<T, W, J, C>), dim3(blocks), dim3(kMoveBlock), 0, s,
                      static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.ys), a.ldys,
                      a.slot, a.source, a.weights, a.tokens, token_blocks, a.topk, a.rows,
                      (int)a.cols, chunks, static_cast<T*>(a.out), a.dw);
   return hipGetLastError();
 }
-template <typename T, int W>
+template <typename T, int W, Cache C>
+hipError_t combine_bwd_choices(const MoeArgs& a, hipStream_t s) {
+  if (a.topk <= 2) return combine_bwd_rows<T, W, 2, C>(a, s);
+  return a.topk <= 4 ? combine_bwd_rows<T, W, 4, C>(a, s) : combine_bwd_rows<T, W, 8, C>(a, s);
+}
+template <typename T, Cache C>
 hipError_t combine_bwd_waves(const MoeArgs& a, hipStream_t s) {
-  if (a.topk <= 2) return combine_bwd_rows<T, W, 2>(a, s);
-  return a.topk <= 4 ? combine_bwd_rows<T, W, 4>(a, s) : combine_bwd_rows<T, W, 8>(a, s);
+  // rows of up to two pieces a lane take one wave: four would leave most lanes idle
+  return a.cols <= 2 * 64 * Piece<T>::N ? combine_bwd_choices<T, 1, C>(a, s)
+                                        : combine_bwd_choices<T, kMoveWaves, C>(a, s);
 }
 template <typename T>
 hipError_t combine_bwd(const MoeArgs& a, hipStream_t s) {
-  // rows of up to two pieces a lane take one wave: four would leave most lanes idle
-  return a.cols <= 2 * 64 * Piece<T>::N ? combine_bwd_waves<T, 1>(a, s)
-                                        : combine_bwd_waves<T, kMoveWaves>(a, s);
+  return keeps(a, 2 * a.rows + a.tokens) ? combine_bwd_waves<T, kKeep>(a, s)
+                                         : combine_bwd_waves<T, kStream>(a, s);
 }
 
 }  // namespace
