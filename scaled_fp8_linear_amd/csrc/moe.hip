@@ -26,14 +26,14 @@ namespace {
 
 // ------------------------------------------------------------------------------ sort
 
-// A workgroup ranks up to kSortBlock * S pairs, S to a lane, in registers. Up to kSortOne
-// pairs one workgroup does it all in one launch; above, chunks of kSortChunk pairs are counted
-// first, and every workgroup adds up the counts of all; above kSortDirect of those, chunks of
-// kSortLong, whose counts a launch between turns into starts.
+// A workgroup ranks up to kSortBlock * S pairs, S to a lane, in registers; what it costs is the
+// instructions of the ranking, about 0.8 us a step on one compute unit. So up to kSortOne pairs
+// one workgroup does it all in one launch (4000 pairs 6.1 us); above, chunks of kSortBlock are
+// counted first, and every workgroup adds up the counts of all; above kSortDirect of those,
+// chunks of kSortLong, whose counts a launch between turns into starts.
 constexpr int kSortBlock = 1024, kSortWaves = kSortBlock / 64;
-constexpr int64_t kSortOne = 16 * kSortBlock, kSortChunk = 4 * kSortBlock;
-constexpr int64_t kSortLong = 16 * kSortBlock, kSortDirect = 64;
-constexpr int kSortShares = 16;
+constexpr int kSortSteps = 4, kSortShares = 16;
+constexpr int64_t kSortOne = kSortSteps * kSortBlock, kSortLong = kSortOne, kSortDirect = 128;
 
 __device__ __forceinline__ int expert_of(int32_t v, int experts) {
   return v >= 0 && v < experts ? v : -1;
@@ -44,6 +44,12 @@ __device__ __forceinline__ int expert_of(int64_t v, int experts) {
 
 __device__ __forceinline__ int wave_index() {
   return __builtin_amdgcn_readfirstlane((int)threadIdx.x / 64);
+}
+
+// Bits of `mask` below this lane's.
+__device__ __forceinline__ int lanes_below(uint64_t mask) {
+  return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                        __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
 }
 
 // The experts of this lane's S pairs (-1: none): wave w of the workgroup has the 64 S pairs
@@ -111,7 +117,12 @@ moe_scan_kernel(int32_t* __restrict__ block_counts, int64_t blocks, int experts,
 // The sort. A pair's row is its expert's start, plus the expert's pairs in earlier workgroups,
 // in earlier waves of this workgroup, in earlier steps of this wave, and in lower lanes of its
 // step. The last comes from one ballot per bit of the expert index: the lanes that agree in
-// every bit are the same expert's. Counts are integers added in a fixed order.
+// every bit are the same expert's. A wave's LDS operations run in order, so a step's counters
+// hold the steps before it; nothing depends on the order of the waves.
+//
+// The pairs of one step go to as many experts, so writing source from there costs a line a
+// pair. With more than one step (4000 pairs: 6.9 us) the workgroup's pairs are brought into their
+// order in LDS first and written along the rows (6.1 us).
 // block_counts: null for a single workgroup; else the counts of the blocks, or with totals
 // those of the blocks before each.
 template <int S, typename I>
@@ -121,11 +132,13 @@ moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int experts, int bits,
                 const int32_t* __restrict__ totals, int32_t* __restrict__ slot,
                 int32_t* __restrict__ source, int32_t* __restrict__ counts,
                 int32_t* __restrict__ offsets) {
-  extern __shared__ int lds[];                 // next[waves][experts], then the share sums
-  __shared__ int wave_sum[kSortWaves];
-  __shared__ int end;
-  int* next = lds;
-  int2* share = reinterpret_cast<int2*>(lds + kSortWaves * experts);
+  constexpr bool kOrder = S > 1;
+  __shared__ int next[kSortWaves * kMoeMaxExperts];        // [waves][experts]
+  __shared__ int2 share[kOrder ? 1 : kSortBlock];          // only chunks of one step are added
+  __shared__ int2 wave_sum[kSortWaves], pad[kMoeMaxExperts];
+  __shared__ int shift[kOrder ? kMoeMaxExperts : 1], end, placed;
+  __shared__ uint16_t order_pair[kOrder ? S * kSortBlock : 1];
+  __shared__ uint16_t order_expert[kOrder ? S * kSortBlock : 1];
   const int t = threadIdx.x, lane = t % 64, wave = wave_index();
   const int64_t p0 = first_pair<S>();
   int e[S], row[S];
@@ -143,84 +156,122 @@ moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int experts, int bits,
     }
   }
   for (int i = t; i < kSortWaves * experts; i += kSortBlock) next[i] = 0;
-  share[t] = n;
+  if constexpr (!kOrder) share[t] = n;
   __syncthreads();
-  // ranks among the wave's own pairs
-  volatile int* mine = next + wave * experts;
+  // ranks among the wave's own pairs: the lanes of a step that hold the same expert, then the
+  // lowest of them adds their number to the wave's counter, steps in order
+  uint64_t same[S];
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    uint64_t same = __ballot(e[s] >= 0);
-    row[s] = -1;
-    if (!same) continue;
-    for (int b = 0; b < bits; ++b) {
-      const uint64_t m = __ballot((e[s] >> b) & 1);
-      same &= ((e[s] >> b) & 1) ? m : ~m;
+  for (int k = 0; k < S; ++k) same[k] = __ballot(e[k] >= 0);
+  for (int b = 0; b < bits; ++b) {
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      const int bit = (e[k] >> b) & 1;
+      const uint64_t m = __ballot(bit);
+      same[k] &= bit ? m : ~m;
     }
-    if (e[s] >= 0) {
-      const int rank = __popcll(same & ((1ull << lane) - 1)), had = mine[e[s]];
-      row[s] = had + rank;
-      // the wave runs in step: every lane has read the counter before the lowest adds to it
-      __builtin_amdgcn_wave_barrier();
-      if (rank == 0) mine[e[s]] = had + __popcll(same);
-    }
-    __builtin_amdgcn_wave_barrier();
+  }
+  int* mine = next + wave * experts;
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    row[k] = 0;
+    if (e[k] >= 0 && lanes_below(same[k]) == 0)
+      row[k] = atomicAdd(&mine[e[k]], __popcll(same[k]));
+  }
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    const int first = e[k] >= 0 ? __ffsll((unsigned long long)same[k]) - 1 : lane;
+    row[k] = __shfl(row[k], first, 64) + lanes_below(same[k]);
   }
   __syncthreads();
-  // thread e: expert e's pairs over all workgroups and before this one
-  int tot = 0, before = 0;
-  if (t < experts) {
-    if (!block_counts) {
-      for (int w = 0; w < kSortWaves; ++w) tot += next[w * experts + t];
-    } else if (totals) {
-      tot = totals[t];
-      before = block_counts[(int64_t)blockIdx.x * experts + t];
-    } else {
-      for (int g = 0; g < shares; ++g) {
-        const int2 c = share[(g << bits) + t];
-        tot += c.x;
-        before += c.y;
+  // thread e: expert e's pairs over all workgroups, before this one, and of this one
+  int c[kSortWaves], tot = 0, before = 0, own = 0;
+  int2 pre = {0, 0};                           // inclusive prefix of the padded and own counts
+  int padded = 0;
+  if (wave * 64 < experts) {
+    if (t < experts) {
+#pragma unroll
+      for (int w = 0; w < kSortWaves; ++w) {
+        c[w] = next[w * experts + t];
+        own += c[w];
+      }
+      if (!block_counts) {
+        tot = own;
+      } else if (totals) {
+        tot = totals[t];
+        before = block_counts[(int64_t)blockIdx.x * experts + t];
+      } else if constexpr (!kOrder) {
+#pragma unroll 8
+        for (int g = 0; g < shares; ++g) {
+          const int2 k = share[(g << bits) + t];
+          tot += k.x;
+          before += k.y;
+        }
       }
     }
-  }
-  const int padded = (tot + multiple - 1) / multiple * multiple;
-  // inclusive prefix of the padded counts over the threads
-  int pre = padded;
+    padded = (tot + multiple - 1) / multiple * multiple;
+    pre = int2{padded, own};
 #pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int o = __shfl_up(pre, off, 64);
-    if (lane >= off) pre += o;
-  }
-  if (lane == 63) wave_sum[wave] = pre;
-  __syncthreads();
-  for (int w = 0; w < wave; ++w) pre += wave_sum[w];
-  const int start = pre - padded;
-  if (t < experts) {
-    int at = start + before;
-    for (int w = 0; w < kSortWaves; ++w) {
-      const int c = next[w * experts + t];
-      next[w * experts + t] = at;
-      at += c;
+    for (int off = 1; off < 64; off <<= 1) {
+      const int x = __shfl_up(pre.x, off, 64), y = kOrder ? __shfl_up(pre.y, off, 64) : 0;
+      if (lane >= off) pre.x += x, pre.y += y;
     }
-    if (t == experts - 1) end = pre;
+  }
+  if (experts > 64) {
+    if (lane == 63) wave_sum[wave] = pre;
+    __syncthreads();
+    if (wave * 64 < experts)
+      for (int w = 0; w < wave; ++w) pre.x += wave_sum[w].x, pre.y += wave_sum[w].y;
+  }
+  if (t < experts) {
+    const int start = pre.x - padded, first = start + before;
+    int at = kOrder ? pre.y - own : first;
+    if constexpr (kOrder) shift[t] = first - at;
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      next[w * experts + t] = at;
+      at += c[w];
+    }
+    pad[t] = int2{start + tot, pre.x};
+    if (t == experts - 1) {
+      end = pre.x;
+      placed = pre.y;
+    }
     if (blockIdx.x == 0) {
       counts[t] = tot;
-      offsets[t + 1] = pre;
+      offsets[t + 1] = pre.x;
       if (t == 0) offsets[0] = 0;
     }
-    // this expert's padding rows, by one workgroup
-    if (t % (int)gridDim.x == (int)blockIdx.x)
-      for (int r = start + tot; r < pre; ++r) source[r] = -1;
   }
   __syncthreads();
+  const int64_t block_p0 = (int64_t)blockIdx.x * (kSortBlock * S);
 #pragma unroll
-  for (int s = 0; s < S; ++s) {
-    const int64_t p = p0 + s * 64 + lane;
+  for (int k = 0; k < S; ++k) {
+    const int64_t p = p0 + k * 64 + lane;
     if (p >= pairs) break;
-    if (e[s] >= 0) {
-      row[s] += next[wave * experts + e[s]];
-      source[row[s]] = (int32_t)p;
+    int r = -1;
+    if (e[k] >= 0) {
+      r = row[k] + next[wave * experts + e[k]];
+      if constexpr (kOrder) {
+        order_pair[r] = (uint16_t)(p - block_p0);
+        order_expert[r] = (uint16_t)e[k];
+        r += shift[e[k]];
+      } else {
+        source[r] = (int32_t)p;
+      }
     }
-    slot[p] = row[s];
+    slot[p] = r;
+  }
+  // padding rows, 16 lanes an expert, every expert's by one workgroup
+  for (int i = t;; i += kSortBlock) {
+    const int x = (int)blockIdx.x + (int)gridDim.x * (i / 16);
+    if (x >= experts) break;
+    for (int r = pad[x].x + i % 16; r < pad[x].y; r += 16) source[r] = -1;
+  }
+  if constexpr (kOrder) {
+    __syncthreads();
+    for (int i = t; i < placed; i += kSortBlock)
+      source[i + shift[order_expert[i]]] = (int32_t)(block_p0 + order_pair[i]);
   }
   // rows past the last expert's
   for (int64_t r = end + (int64_t)blockIdx.x * kSortBlock + t; r < rows;
@@ -391,24 +442,33 @@ moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restri
       w[q] = r[q] >= 0 ? weights[pair] : 0.f;
       dot[q] = 0.f;
     }
-    for (int c = lt * N; c < cols; c += W * 64 * N) {
-      piece_t pg = ld_raw<C>(g, c, cols), py[J];
+    constexpr int STEPS = J <= 4 ? 2 : 1, kStep = W * 64 * N;
+    for (int c0 = lt * N; c0 < cols; c0 += STEPS * kStep) {
+      piece_t pg[STEPS], py[STEPS][J];
 #pragma unroll
-      for (int q = 0; q < J; ++q)
-        if (r[q] >= 0) py[q] = ld_raw<C>(ys + r[q] * ldys, c, cols);
-      float fg[N];
-      unpack(cut<T>(pg, c, cols), fg, T{});
+      for (int k = 0; k < STEPS; ++k) {
+        pg[k] = ld_raw<C>(g, c0 + k * kStep, cols);
 #pragma unroll
-      for (int q = 0; q < J; ++q) {
-        if (r[q] < 0) continue;
-        float fy[N], o[N];
-        unpack(cut<T>(py[q], c, cols), fy, T{});
+        for (int q = 0; q < J; ++q)
+          if (r[q] >= 0) py[k][q] = ld_raw<C>(ys + r[q] * ldys, c0 + k * kStep, cols);
+      }
 #pragma unroll
-        for (int n = 0; n < N; ++n) {
-          dot[q] = __builtin_fmaf(fg[n], fy[n], dot[q]);
-          o[n] = w[q] * fg[n];
+      for (int k = 0; k < STEPS; ++k) {
+        const int c = c0 + k * kStep;
+        float fg[N];
+        unpack(cut<T>(pg[k], c, cols), fg, T{});
+#pragma unroll
+        for (int q = 0; q < J; ++q) {
+          if (r[q] < 0) continue;
+          float fy[N], o[N];
+          unpack(cut<T>(py[k][q], c, cols), fy, T{});
+#pragma unroll
+          for (int n = 0; n < N; ++n) {
+            dot[q] = __builtin_fmaf(fg[n], fy[n], dot[q]);
+            o[n] = w[q] * fg[n];
+          }
+          st_row<C>(dys + (int64_t)r[q] * cols, c, cols, pack(o, T{}));
         }
-        st_row<C>(dys + (int64_t)r[q] * cols, c, cols, pack(o, T{}));
       }
     }
     if constexpr (W == 1) {
@@ -435,12 +495,13 @@ moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restri
   }
 }
 
-struct SortPlan { int64_t chunk, blocks; bool scan; };
+struct SortPlan { int64_t steps, blocks; bool scan; };
 SortPlan sort_plan(int64_t pairs) {
-  if (pairs <= kSortOne) return {kSortOne, 1, false};
-  const int64_t b = (pairs + kSortChunk - 1) / kSortChunk;
-  if (b <= kSortDirect) return {kSortChunk, b, false};
-  return {kSortLong, (pairs + kSortLong - 1) / kSortLong, true};
+  const int64_t b = (pairs + kSortBlock - 1) / kSortBlock;
+  if (b <= 1) return {1, 1, false};
+  if (pairs <= kSortOne) return {kSortSteps, 1, false};
+  if (b <= kSortDirect) return {1, b, false};
+  return {kSortSteps, (pairs + kSortLong - 1) / kSortLong, true};
 }
 
 template <int S, typename I>
@@ -451,22 +512,19 @@ hipError_t sort_steps(const MoeSortArgs& a, const SortPlan& plan, hipStream_t s)
   const unsigned blocks = (unsigned)plan.blocks;
   int32_t* block_counts = blocks > 1 ? a.workspace : nullptr;
   int32_t* totals = plan.scan ? a.workspace + plan.blocks * a.experts : nullptr;
-  if constexpr (S > 1) {                       // S = 1 is for one workgroup
-    if (block_counts) {
-      hipLaunchKernelGGL((moe_count_kernel<S, I>), dim3(blocks), dim3(kSortBlock), 0, s, idx,
-                         a.pairs, a.experts, block_counts);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
-    if (totals) {
-      hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)(a.experts + 63) / 64), dim3(kSortBlock),
-                         0, s, block_counts, plan.blocks, a.experts, totals);
-      const hipError_t e = hipGetLastError();
-      if (e != hipSuccess) return e;
-    }
+  if (block_counts) {
+    hipLaunchKernelGGL((moe_count_kernel<S, I>), dim3(blocks), dim3(kSortBlock), 0, s, idx,
+                       a.pairs, a.experts, block_counts);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
   }
-  const unsigned lds = (kSortWaves * (unsigned)a.experts + 2 * kSortBlock) * sizeof(int);
-  hipLaunchKernelGGL((moe_sort_kernel<S, I>), dim3(blocks), dim3(kSortBlock), lds, s, idx, a.pairs,
+  if (totals) {
+    hipLaunchKernelGGL(moe_scan_kernel, dim3((unsigned)(a.experts + 63) / 64), dim3(kSortBlock), 0,
+                       s, block_counts, plan.blocks, a.experts, totals);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((moe_sort_kernel<S, I>), dim3(blocks), dim3(kSortBlock), 0, s, idx, a.pairs,
                      a.experts, bits, a.multiple, a.rows, block_counts, totals, a.slot, a.source,
                      a.counts, a.offsets);
   return hipGetLastError();
@@ -475,9 +533,7 @@ hipError_t sort_steps(const MoeSortArgs& a, const SortPlan& plan, hipStream_t s)
 template <typename I>
 hipError_t sort_launch(const MoeSortArgs& a, hipStream_t s) {
   const SortPlan plan = sort_plan(a.pairs);
-  if (a.pairs <= kSortBlock) return sort_steps<1, I>(a, plan, s);
-  if (a.pairs <= 4 * kSortBlock || plan.chunk == kSortChunk) return sort_steps<4, I>(a, plan, s);
-  return sort_steps<16, I>(a, plan, s);
+  return plan.steps == 1 ? sort_steps<1, I>(a, plan, s) : sort_steps<kSortSteps, I>(a, plan, s);
 }
 
 // Chunks of a row of `pieces` pieces a lane, and the waves that zero its padding rows.
