@@ -282,164 +282,175 @@ moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int experts, int bits,
 // -------------------------------------------------------------------------- exchanges
 
 constexpr int kMoveBlock = 256, kMoveWaves = kMoveBlock / 64;
-constexpr int kMovePieces = 4, kSumPieces = 2;             // 16-byte pieces of a row per lane
-constexpr int kZeroRows = 8;                               // rows checked by a wave
 
 // Waves of the grid, the same for all lanes (addresses of rows are scalar).
 __device__ __forceinline__ uint32_t grid_wave() {
   return blockIdx.x * (uint32_t)kMoveWaves + (uint32_t)wave_index();
 }
 
-// The row of a pair, -1 where there is none in the buffer.
-__device__ __forceinline__ int row_of(const int32_t* slot, int64_t pair, int64_t rows) {
-  const int r = slot[pair];
-  return r >= 0 && r < rows ? r : -1;
-}
-
-// Zero the padding rows among rows [r0, r0 + kZeroRows), kMovePieces pieces a lane from c0 on.
-template <typename T>
-__device__ __forceinline__ void zero_padding(const int32_t* source, int64_t r0, int64_t rows,
-                                             int c0, int cols, T* out) {
-  const int lane = threadIdx.x % 64;
-  const int64_t r = r0 + lane;
-  const bool pad = lane < kZeroRows && r < rows && source[r] < 0;
-  uint64_t m = __ballot(pad);
-  while (m) {
-    const int i = __ffsll((unsigned long long)m) - 1;
-    m &= m - 1;
-    T* row = out + (r0 + i) * cols;
-#pragma unroll
-    for (int v = 0; v < kMovePieces; ++v)
-      st_row<kStream>(row, c0 + (v * 64 + lane) * Piece<T>::N, cols, piece_t{0, 0, 0, 0});
+// A token's choices, one to a lane (topk is at most 64): the row of choice j in lane j, -1 where
+// there is none in the buffer. One load for all; a choice's row comes out as a scalar.
+static_assert(kMoeMaxTopk <= 64, "a lane holds a choice");
+struct Choices {
+  int row;
+  float weight;
+  __device__ __forceinline__ Choices(const int32_t* slot, const float* weights, int64_t token,
+                                     int topk, int64_t rows) {
+    const int lane = threadIdx.x % 64;
+    const int64_t pair = token * topk + lane;
+    const int r = lane < topk ? slot[pair] : -1;
+    weight = lane < topk && weights ? weights[pair] : 1.f;
+    row = r < rows ? r : -1;
   }
-}
+  __device__ __forceinline__ int row_of(int j) const {
+    return __builtin_amdgcn_readlane(row, j);
+  }
+  __device__ __forceinline__ float weight_of(int j) const {
+    return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(weight), j));
+  }
+};
 
-// One wave per (token, kMovePieces pieces a lane of the row): loaded once, stored to each of
-// the token's rows. The waves after those zero the padding rows. Bound by the writes of the
+// Zeroing the padding rows: a wave checks kRows rows and zeroes those without a pair, PIECES
+// 16-byte pieces a lane, one row after the other. More rows a wave are fewer waves that find
+// nothing but longer ones that do: dispatch of 300 tokens, 6 of 64, width 512 bf16 3.1 us with 8
+// rows a wave and 5.5 us with 64, of 8192 tokens, 8 of 64, width 64 7.4 and 8.3 us.
+template <typename T, int PIECES> struct Zero {
+  static constexpr int kRows = 8, kCols = 64 * Piece<T>::N * PIECES;
+  static int64_t waves(int64_t rows, int64_t cols) {
+    return (rows + kRows - 1) / kRows * ((cols + kCols - 1) / kCols);
+  }
+  static __device__ __forceinline__ void run(uint32_t wave, const int32_t* source, int64_t rows,
+                                             int cols, T* out) {
+    const uint32_t chunks = (uint32_t)(cols + kCols - 1) / kCols;
+    const int lane = threadIdx.x % 64, c0 = (int)(wave % chunks) * kCols;
+    const int64_t r0 = (int64_t)(wave / chunks) * kRows, r = r0 + lane;
+    uint64_t m = __ballot(lane < kRows && r < rows && source[r] < 0);
+    while (m) {
+      const int i = __ffsll((unsigned long long)m) - 1;
+      m &= m - 1;
+#pragma unroll
+      for (int v = 0; v < PIECES; ++v)
+        st_row<kStream>(out + (r0 + i) * cols, c0 + (v * 64 + lane) * Piece<T>::N, cols,
+                        piece_t{0, 0, 0, 0});
+    }
+  }
+};
+
+// One wave per (token, PIECES pieces a lane of the row): loaded once, stored to each of
+// the token's rows. The first waves zero the padding rows. Bound by the writes of the
 // sorted rows: 8192 tokens to 8 of 64 experts, width 4096 bf16 in 109.6 us, 5.6 TB/s. They
 // stream (117.8 us kept, and no size was found where that cost); the tokens' rows are kept, 122
 // us with the sort against 136 us streamed.
-template <typename T>
+template <typename T, int PIECES>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slot,
                     const int32_t* __restrict__ source, int64_t tokens, int topk, int64_t rows,
-                    int cols, uint32_t chunks, T* __restrict__ xs) {
-  constexpr int N = Piece<T>::N, kCols = 64 * N * kMovePieces;
+                    int cols, uint32_t chunks, uint32_t zeros, T* __restrict__ xs) {
+  constexpr int N = Piece<T>::N, kCols = 64 * N * PIECES;
   const int lane = threadIdx.x % 64;
   uint32_t u = grid_wave();
-  const uint32_t moves = (uint32_t)tokens * chunks;
-  if (u >= moves) {
-    u -= moves;
-    const int64_t r0 = (int64_t)(u / chunks) * kZeroRows;
-    if (r0 < rows) zero_padding(source, r0, rows, (int)(u % chunks) * kCols, cols, xs);
+  if (u < zeros) {
+    Zero<T, PIECES>::run(u, source, rows, cols, xs);
     return;
   }
+  u -= zeros;
   const int64_t t = u / chunks;
+  if (t >= tokens) return;
   const int c0 = (int)(u % chunks) * kCols + lane * N;
   const T* src = x + t * ldx;
-  piece_t v[kMovePieces];
+  const Choices choices(slot, nullptr, t, topk, rows);
+  piece_t v[PIECES];
 #pragma unroll
-  for (int i = 0; i < kMovePieces; ++i) v[i] = ld_raw<kKeep>(src, c0 + i * 64 * N, cols);
+  for (int i = 0; i < PIECES; ++i) v[i] = ld_raw<kKeep>(src, c0 + i * 64 * N, cols);
 #pragma unroll
-  for (int i = 0; i < kMovePieces; ++i) v[i] = cut<T>(v[i], c0 + i * 64 * N, cols);
+  for (int i = 0; i < PIECES; ++i) v[i] = cut<T>(v[i], c0 + i * 64 * N, cols);
   for (int j = 0; j < topk; ++j) {
-    const int r = row_of(slot, t * topk + j, rows);
+    const int r = choices.row_of(j);
     if (r < 0) continue;
     T* dst = xs + (int64_t)r * cols;
 #pragma unroll
-    for (int i = 0; i < kMovePieces; ++i) st_row<kStream>(dst, c0 + i * 64 * N, cols, v[i]);
+    for (int i = 0; i < PIECES; ++i) st_row<kStream>(dst, c0 + i * 64 * N, cols, v[i]);
   }
 }
 
-// One wave per (token, kSumPieces pieces a lane of the row): the token's rows, two in flight,
+// One wave per (token, PIECES pieces a lane of the row): the token's rows, U in flight,
 // summed in the order of the choices in float32 and rounded once. Bound by the reads of the
-// sorted rows: 8192 tokens, 8 of 64 experts, width 4096 bf16 in 99.5 us, 5.9 TB/s. More rows in
-// flight leave fewer waves on a unit: four take as long there and 30.8 us where two take 25.1
-// (4096 tokens, 8 of 64, width 1024 f32), one takes 12.8 us where two take 11.4 (1024 tokens,
-// width 2048 bf16).
-constexpr int kSumRows = 2;
-template <typename T, Cache C>
+// sorted rows: 8192 tokens, 8 of 64 experts, width 4096 bf16 in 99.5 us, 5.9 TB/s.
+template <typename T, int PIECES, int U, Cache C>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_combine_kernel(const T* __restrict__ ys, int64_t ldys, const int32_t* __restrict__ slot,
                    const float* __restrict__ weights, int64_t tokens, int topk, int64_t rows,
                    int cols, uint32_t chunks, T* __restrict__ y) {
-  constexpr int N = Piece<T>::N, kCols = 64 * N * kSumPieces, U = kSumRows;
+  constexpr int N = Piece<T>::N, kCols = 64 * N * PIECES;
   const int lane = threadIdx.x % 64;
   const uint32_t u = grid_wave();
   const int64_t t = u / chunks;
   if (t >= tokens) return;
   const int c0 = (int)(u % chunks) * kCols + lane * N;
-  float acc[kSumPieces][N];
+  const Choices choices(slot, weights, t, topk, rows);
+  float acc[PIECES][N];
 #pragma unroll
-  for (int i = 0; i < kSumPieces; ++i)
+  for (int i = 0; i < PIECES; ++i)
 #pragma unroll
     for (int n = 0; n < N; ++n) acc[i][n] = 0.f;
   for (int j0 = 0; j0 < topk; j0 += U) {
-    piece_t v[U][kSumPieces];
-    float w[U];
+    piece_t v[U][PIECES];
     int r[U];
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
-      const int64_t pair = t * topk + j0 + q;
-      r[q] = j0 + q < topk ? row_of(slot, pair, rows) : -1;
-      w[q] = r[q] >= 0 && weights ? weights[pair] : 1.f;
-    }
+    for (int q = 0; q < U; ++q) r[q] = j0 + q < topk ? choices.row_of(j0 + q) : -1;
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       if (r[q] < 0) continue;
 #pragma unroll
-      for (int i = 0; i < kSumPieces; ++i)
+      for (int i = 0; i < PIECES; ++i)
         v[q][i] = ld_raw<C>(ys + r[q] * ldys, c0 + i * 64 * N, cols);
     }
 #pragma unroll
     for (int q = 0; q < U; ++q) {
       if (r[q] < 0) continue;
+      const float w = choices.weight_of(j0 + q);
 #pragma unroll
-      for (int i = 0; i < kSumPieces; ++i) {
+      for (int i = 0; i < PIECES; ++i) {
         float f[N];
         unpack(cut<T>(v[q][i], c0 + i * 64 * N, cols), f, T{});
 #pragma unroll
-        for (int n = 0; n < N; ++n) acc[i][n] = __builtin_fmaf(w[q], f[n], acc[i][n]);
+        for (int n = 0; n < N; ++n) acc[i][n] = __builtin_fmaf(w, f[n], acc[i][n]);
       }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kSumPieces; ++i)
+  for (int i = 0; i < PIECES; ++i)
     st_row<C>(y + t * cols, c0 + i * 64 * N, cols, pack(acc[i], T{}));
 }
 
 // W waves per token read dy[t] once per J choices, write w dy to their rows and sum dy ys of
-// each (lanes, then waves, in a fixed order). The workgroups after the tokens' zero the
-// padding rows.
+// each (lanes, then waves, in a fixed order). The first workgroups zero the padding rows.
 template <typename T, int W, int J, Cache C>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_combine_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ ys,
                        int64_t ldys, const int32_t* __restrict__ slot,
                        const int32_t* __restrict__ source, const float* __restrict__ weights,
-                       int64_t tokens, uint32_t token_blocks, int topk, int64_t rows, int cols,
-                       uint32_t chunks, T* __restrict__ dys, float* __restrict__ dw) {
+                       int64_t tokens, uint32_t zero_blocks, int topk, int64_t rows, int cols,
+                       T* __restrict__ dys, float* __restrict__ dw) {
   constexpr int N = Piece<T>::N, PER = kMoveWaves / W;
   __shared__ float part[W][J];
   const int lane = threadIdx.x % 64, wave = wave_index();
-  if (blockIdx.x >= token_blocks) {
-    const uint32_t u = grid_wave() - token_blocks * kMoveWaves;
-    const int64_t r0 = (int64_t)(u / chunks) * kZeroRows;
-    if (r0 < rows)
-      zero_padding(source, r0, rows, (int)(u % chunks) * (64 * N * kMovePieces), cols, dys);
+  if (blockIdx.x < zero_blocks) {
+    Zero<T, W>::run(grid_wave(), source, rows, cols, dys);
     return;
   }
-  const int64_t t = (int64_t)blockIdx.x * PER + (W == 1 ? wave : 0);
+  const int64_t t = (int64_t)(blockIdx.x - zero_blocks) * PER + (W == 1 ? wave : 0);
   if (t >= tokens) return;                       // a whole token's waves
   const int lt = W == 1 ? lane : (int)threadIdx.x;
   const T* g = dy + t * lddy;
+  const Choices choices(slot, weights, t, topk, rows);
   for (int j0 = 0; j0 < topk; j0 += J) {
     int r[J];
     float w[J], dot[J];
 #pragma unroll
     for (int q = 0; q < J; ++q) {
-      const int64_t pair = t * topk + j0 + q;
-      r[q] = j0 + q < topk ? row_of(slot, pair, rows) : -1;
-      w[q] = r[q] >= 0 ? weights[pair] : 0.f;
+      r[q] = j0 + q < topk ? choices.row_of(j0 + q) : -1;
+      w[q] = r[q] >= 0 ? choices.weight_of(j0 + q) : 0.f;
       dot[q] = 0.f;
     }
     constexpr int STEPS = J <= 4 ? 2 : 1, kStep = W * 64 * N;
@@ -536,24 +547,34 @@ hipError_t sort_launch(const MoeSortArgs& a, hipStream_t s) {
   return plan.steps == 1 ? sort_steps<1, I>(a, plan, s) : sort_steps<kSortSteps, I>(a, plan, s);
 }
 
-// Chunks of a row of `pieces` pieces a lane, and the waves that zero its padding rows.
+// Chunks of a row of `pieces` pieces a lane.
 template <typename T> uint32_t row_chunks(int64_t cols, int pieces) {
   const int per = 64 * Piece<T>::N * pieces;
   return (uint32_t)((cols + per - 1) / per);
 }
-int64_t zero_waves(int64_t rows, int64_t chunks) {
-  return (rows + kZeroRows - 1) / kZeroRows * chunks;
-}
 unsigned move_blocks(int64_t waves) { return (unsigned)((waves + kMoveWaves - 1) / kMoveWaves); }
 
+// Waves that are on the card at once. A launch of no more is bound by a wave's own waits.
+constexpr int64_t kResidentWaves = 256 * 32;
+
+template <typename T, int PIECES>
+hipError_t dispatch_rows(const MoeArgs& a, hipStream_t s) {
+  const uint32_t chunks = row_chunks<T>(a.cols, PIECES);
+  const int64_t zeros = Zero<T, PIECES>::waves(a.rows, a.cols);
+  const unsigned blocks = move_blocks(a.tokens * chunks + zeros);
+  hipLaunchKernelGGL((moe_dispatch_kernel<T, PIECES>), dim3(blocks), dim3(kMoveBlock), 0, s,
+                     static_cast<const T*>(a.x), a.ldx, a.slot, a.source, a.tokens, a.topk, a.rows,
+                     (int)a.cols, chunks, (uint32_t)zeros, static_cast<T*>(a.out));
+  return hipGetLastError();
+}
+// One piece a lane where that fits the row or the card (8192 tokens, 8 of 64, width 64 bf16:
+// 7.4 us, with four pieces 10.4 us; one token, width 4096 2.9 and 3.8 us); else four, 2 % faster
+// for 8192 tokens of width 4096.
 template <typename T>
 hipError_t dispatch(const MoeArgs& a, hipStream_t s) {
-  const uint32_t chunks = row_chunks<T>(a.cols, kMovePieces);
-  const unsigned blocks = move_blocks(a.tokens * chunks + zero_waves(a.rows, chunks));
-  hipLaunchKernelGGL((moe_dispatch_kernel<T>), dim3(blocks), dim3(kMoveBlock), 0, s,
-                     static_cast<const T*>(a.x), a.ldx, a.slot, a.source, a.tokens, a.topk, a.rows,
-                     (int)a.cols, chunks, static_cast<T*>(a.out));
-  return hipGetLastError();
+  const int64_t chunks = row_chunks<T>(a.cols, 1);
+  return chunks <= 1 || a.tokens * chunks <= kResidentWaves ? dispatch_rows<T, 1>(a, s)
+                                                            : dispatch_rows<T, 4>(a, s);
 }
 
 // Tensors of rows up to 96 MiB together are kept in the caches, larger ones stream. Measured over
@@ -566,31 +587,34 @@ bool keeps(const MoeArgs& a, int64_t rows) {
   return rows * a.cols * (a.dtype == kF32 ? 4 : 2) <= kKeepBytes;
 }
 
-template <typename T, Cache C>
+template <typename T, int PIECES, int U, Cache C>
 hipError_t combine_rows(const MoeArgs& a, hipStream_t s) {
-  const uint32_t chunks = row_chunks<T>(a.cols, kSumPieces);
-  hipLaunchKernelGGL((moe_combine_kernel<T, C>), dim3(move_blocks(a.tokens * chunks)),
+  const uint32_t chunks = row_chunks<T>(a.cols, PIECES);
+  hipLaunchKernelGGL((moe_combine_kernel<T, PIECES, U, C>), dim3(move_blocks(a.tokens * chunks)),
                      dim3(kMoveBlock), 0, s, static_cast<const T*>(a.ys), a.ldys, a.slot,
                      a.weights, a.tokens, a.topk, a.rows, (int)a.cols, chunks,
                      static_cast<T*>(a.out));
   return hipGetLastError();
 }
+// Where the waves do not all fit on the card at once, two pieces of two rows in flight: more
+// leave fewer waves on a unit (4096 tokens, 8 of 64, width 1024 f32: two rows 25.1 us, four 30.8
+// us, one 25.5 us). Where they do, a wave's own waits count: one piece of eight rows.
 template <typename T>
 hipError_t combine(const MoeArgs& a, hipStream_t s) {
-  return keeps(a, a.rows + a.tokens) ? combine_rows<T, kKeep>(a, s)
-                                     : combine_rows<T, kStream>(a, s);
+  if (!keeps(a, a.rows + a.tokens)) return combine_rows<T, 2, 2, kStream>(a, s);
+  const bool resident = a.tokens * row_chunks<T>(a.cols, 1) <= kResidentWaves;
+  return resident ? combine_rows<T, 1, 8, kKeep>(a, s) : combine_rows<T, 2, 2, kKeep>(a, s);
 }
 
 template <typename T, int W, int J, Cache C>
 hipError_t combine_bwd_rows(const MoeArgs& a, hipStream_t s) {
-  const uint32_t chunks = row_chunks<T>(a.cols, kMovePieces);
   const int64_t per = kMoveWaves / W;
-  const uint32_t token_blocks = (uint32_t)((a.tokens + per - 1) / per);
-  const unsigned blocks = token_blocks + move_blocks(zero_waves(a.rows, chunks));
+  const uint32_t zero_blocks = move_blocks(Zero<T, W>::waves(a.rows, a.cols));
+  const unsigned blocks = zero_blocks + (unsigned)((a.tokens + per - 1) / per);
   hipLaunchKernelGGL((moe_combine_bwd_kernel<T, W, J, C>), dim3(blocks), dim3(kMoveBlock), 0, s,
                      static_cast<const T*>(a.x), a.ldx, static_cast<const T*>(a.ys), a.ldys,
-                     a.slot, a.source, a.weights, a.tokens, token_blocks, a.topk, a.rows,
-                     (int)a.cols, chunks, static_cast<T*>(a.out), a.dw);
+                     a.slot, a.source, a.weights, a.tokens, zero_blocks, a.topk, a.rows,
+                     (int)a.cols, static_cast<T*>(a.out), a.dw);
   return hipGetLastError();
 }
 template <typename T, int W, Cache C>
