@@ -50,12 +50,24 @@ __device__ __forceinline__ void st_param(void* p, bool f32, int c, float v) {
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef float sums_t __attribute__((ext_vector_type(4), aligned(4)));
 
-// The lane group (row of a turn) of this thread; the same for a whole wave where a row takes
-// one or more, so that row addresses are scalar.
+// Which lanes own a row. Narrow rows take 16 or 64 lanes (LPR); wide ones (LPR = 0) as many
+// whole waves as their pieces fill, a value of the launch, since rounding it up to a power of two
+// would leave almost half the lanes without elements just above one (8000x4104 bf16 forward 31.5
+// us, with five waves 27.1 us; 4000x9000 50.0 and 35.5 us; backward 8000x4104 56.5 and 51.5 us). For a whole wave or more the row is
+// the same in all lanes of a wave, so that row addresses are scalar.
+struct Lanes {
+  int per_row, lane, group, groups;       // lanes of a row, this one; the row of a turn, rows of it
+};
 template <int LPR>
-__device__ __forceinline__ int row_group() {
-  const int g = threadIdx.x / LPR;
-  return LPR >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
+__device__ __forceinline__ Lanes lanes_of(int row_waves) {
+  const int t = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(t / 64);
+  if constexpr (LPR == 0) {
+    const int g = wave / row_waves;
+    return {row_waves * 64, (wave - g * row_waves) * 64 + t % 64, g,
+            (int)(blockDim.x / 64) / row_waves};
+  } else {
+    return {LPR, t % LPR, LPR == 64 ? wave : t / LPR, (int)blockDim.x / LPR};
+  }
 }
 
 // The row of a group in the turn that starts at r0. A group past the last row works on that
@@ -67,24 +79,27 @@ __device__ __forceinline__ int64_t turn_row(int64_t r0, int group, int64_t rows)
 
 // This lane's pieces of a row, not yet cut at its end.
 template <Cache C, int LPR, typename T, int NV>
-__device__ __forceinline__ void ld_rows(const T* row, int lane, int cols, piece_t (&p)[NV]) {
+__device__ __forceinline__ void ld_rows(const T* row, const Lanes& l, int cols,
+                                        piece_t (&p)[NV]) {
 #pragma unroll
   for (int v = 0; v < NV; ++v)
-    p[v] = ld_raw<C, LPR == 16>(row, (v * LPR + lane) * Piece<T>::N, cols);
+    p[v] = ld_raw<C, LPR == 16>(row, (v * l.per_row + l.lane) * Piece<T>::N, cols);
 }
 
-// Sum over the LPR lanes of a row. Rows of several waves meet in LDS (`part`, one float per
-// wave of the workgroup); the caller alternates buffers so that one barrier per sum is
-// enough.
+// Sum over the lanes of a row. Rows of several waves meet in LDS (`part`, one float per wave of
+// the workgroup); the caller alternates buffers so that one barrier per sum is enough.
+constexpr int kMaxWaves = 16;
+__device__ __forceinline__ float waves_sum(const float* part, const Lanes& l) {
+  const int i = threadIdx.x % kMaxWaves, w = l.per_row / 64;
+  return lanes_sum<kMaxWaves>(i < w ? part[l.group * w + i] : 0.f);
+}
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v, float* part) {
-  v = lanes_sum<(LPR < 64 ? LPR : 64)>(v);
-  if constexpr (LPR > 64) {
-    constexpr int W = LPR / 64;
-    const int wave = row_group<64>();
-    if (threadIdx.x % 64 == 0) part[wave] = v;
+__device__ __forceinline__ float row_sum(float v, float* part, const Lanes& l) {
+  v = lanes_sum<(LPR == 16 ? 16 : 64)>(v);
+  if constexpr (LPR == 0) {
+    if (threadIdx.x % 64 == 0) part[threadIdx.x / 64] = v;
     __syncthreads();
-    v = lanes_sum<W>(part[wave / W * W + threadIdx.x % W]);
+    v = waves_sum(part, l);
   }
   return v;
 }
@@ -94,57 +109,51 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
 // 8192x4096 bf16: 45.0 us so, 45.3 us with twice as many workgroups of 512, 48.1 us with four
 // times as many of 256; of 1021x5003 f16 21.4, 22.5 and 22.6 us, and with half the workgroups
 // 24.6 us. The forward of 8192x4096 does not depend on its grid (23.0 to 23.7 us).
-constexpr int kFwdBlock = 256, kBwdBlock = 1024;
+constexpr int kFwdBlock = 256, kBwdBlock = 1024, kMaxBlock = 64 * kMaxWaves;
 constexpr int64_t kFwdGrid = 256 * 8, kBwdGrid = 256;
 
-constexpr int fwd_block(int lpr) { return lpr > kFwdBlock ? lpr : kFwdBlock; }
-
-// LPR lanes own a row; lane l holds the pieces l, l + LPR, ... (EPT elements). A workgroup
-// walks the rows with the grid's stride and loads the next row while it works on this one.
-template <typename T, int LPR, int EPT, int BLOCK, Cache LOAD>
-__global__ void __launch_bounds__(BLOCK)
+// Lane l of a row's n holds the pieces l, l + n, ... (EPT elements). A workgroup walks the rows
+// with the grid's stride; the other workgroups of its compute unit cover its waits, which takes
+// registers better than loading the next row ahead does (2000x16384 bf16 33.8 us, ahead 38.6 us;
+// 2000x12000 f32 39.7 and 56.5 us; 8192x4096 bf16 23.7 us either way). Holding gamma and beta is
+// worth theirs: read again for every row 8192x4096 bf16 takes 34.0 us.
+template <typename T, int LPR, int EPT, Cache LOAD>
+__global__ void __launch_bounds__(LPR ? kFwdBlock : kMaxBlock)
 layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const void* __restrict__ gamma,
-                     const void* __restrict__ beta, bool params_f32, int64_t rows, int cols, float eps,
-                     T* __restrict__ y, float* __restrict__ mean_out,
-                     float* __restrict__ rstd_out) {
-  constexpr int N = Piece<T>::N, NV = EPT / N, ROWS = BLOCK / LPR;
-  // gamma, beta and the next row stay in registers beside the row up to 16 elements a lane
-  constexpr bool kAhead = EPT <= 16;
-  __shared__ float part[2][BLOCK / 64];
-  const int lane = threadIdx.x % LPR, group = row_group<LPR>();
+                     const void* __restrict__ beta, bool params_f32, int64_t rows, int cols,
+                     int row_waves, float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+  constexpr int N = Piece<T>::N, NV = EPT / N;
+  // gamma and beta stay in registers beside the row up to 16 elements a lane
+  constexpr bool kHeld = EPT <= 16;
+  __shared__ float part[2][kMaxWaves];
+  const Lanes l = lanes_of<LPR>(row_waves);
   const float fcols = (float)cols;
-  const int64_t step = (int64_t)gridDim.x * ROWS;
-  piece_t cur[NV], next[NV];
-  if (kAhead)
-    ld_rows<LOAD, LPR>(x + turn_row((int64_t)blockIdx.x * ROWS, group, rows) * ldx, lane, cols,
-                        cur);
+  const int64_t step = (int64_t)gridDim.x * l.groups;
   float gm[NV][N], bt[NV][N];
-  if constexpr (kAhead) {
+  if constexpr (kHeld) {
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, gm[v]);
-      ld_params<T>(beta, params_f32, (v * LPR + lane) * N, cols, 0.f, bt[v]);
+      ld_params<T>(gamma, params_f32, (v * l.per_row + l.lane) * N, cols, 1.f, gm[v]);
+      ld_params<T>(beta, params_f32, (v * l.per_row + l.lane) * N, cols, 0.f, bt[v]);
     }
   }
-  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < rows; r0 += step) {
-    if (!kAhead)
-      ld_rows<LOAD, LPR>(x + turn_row(r0, group, rows) * ldx, lane, cols, cur);
-    else if (r0 + step < rows)
-      ld_rows<LOAD, LPR>(x + turn_row(r0 + step, group, rows) * ldx, lane, cols, next);
-    const int64_t r = r0 + group;
+  for (int64_t r0 = (int64_t)blockIdx.x * l.groups; r0 < rows; r0 += step) {
+    piece_t p[NV];
+    ld_rows<LOAD, LPR>(x + turn_row(r0, l.group, rows) * ldx, l, cols, p);
+    const int64_t r = r0 + l.group;
     float f[NV][N];
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      unpack(cut<T>(cur[v], (v * LPR + lane) * N, cols), f[v], T{});
+      unpack(cut<T>(p[v], (v * l.per_row + l.lane) * N, cols), f[v], T{});
 #pragma unroll
       for (int i = 0; i < N; ++i) s += f[v][i];
     }
-    const float mean = row_sum<LPR>(s, part[0]) / fcols;
+    const float mean = row_sum<LPR>(s, part[0], l) / fcols;
     float q = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * LPR + lane) * N;
+      const int c = (v * l.per_row + l.lane) * N;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         f[v][i] -= mean;
@@ -152,33 +161,44 @@ layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const void* __restric
         q = __builtin_fmaf(d, d, q);
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<LPR>(q, part[1]) / fcols + eps);
-    if (kAhead) {
-#pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        arrived(next[v]);
-        cur[v] = next[v];
-      }
-    }
+    const float rstd = 1.0f / sqrtf(row_sum<LPR>(q, part[1], l) / fcols + eps);
     if (r < rows) {
 #pragma unroll
       for (int v = 0; v < NV; ++v) {
         float o[N];
-        if constexpr (!kAhead) {
+        if constexpr (!kHeld) {
           __builtin_amdgcn_sched_barrier(0);
-          ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, gm[v]);
-          ld_params<T>(beta, params_f32, (v * LPR + lane) * N, cols, 0.f, bt[v]);
+          ld_params<T>(gamma, params_f32, (v * l.per_row + l.lane) * N, cols, 1.f, gm[v]);
+          ld_params<T>(beta, params_f32, (v * l.per_row + l.lane) * N, cols, 0.f, bt[v]);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = __builtin_fmaf(f[v][i] * rstd, gm[v][i], bt[v][i]);
-        st_row<kStream>(y + r * cols, (v * LPR + lane) * N, cols, pack(o, T{}));
+        st_row<kStream>(y + r * cols, (v * l.per_row + l.lane) * N, cols, pack(o, T{}));
       }
-      if (lane == 0) {
+      if (l.lane == 0) {
         if (mean_out) mean_out[r] = mean;
         if (rstd_out) rstd_out[r] = rstd;
       }
     }
   }
+}
+
+// Columns c to c + 3 of the groups' sums, added in the order of the groups; their number is known
+// to the loop, so that its reads are in flight together.
+template <int G>
+__device__ __forceinline__ f32x4_t sum_of(const float* fold, int width, int c) {
+  f32x4_t s = *reinterpret_cast<const f32x4_t*>(fold + c);
+#pragma unroll
+  for (int k = 1; k < G; ++k) s += *reinterpret_cast<const f32x4_t*>(fold + k * width + c);
+  return s;
+}
+template <int LPR>
+__device__ __forceinline__ f32x4_t groups_sum(const float* fold, int width, int groups, int c) {
+  if constexpr (LPR > 0) return sum_of<kMaxWaves>(fold, width, c);      // a wave's are one
+  if (groups == 2) return sum_of<2>(fold, width, c);      // 16 waves by the waves of a row
+  if (groups == 3) return sum_of<3>(fold, width, c);
+  if (groups == 4) return sum_of<4>(fold, width, c);
+  return groups == 5 ? sum_of<5>(fold, width, c) : sum_of<8>(fold, width, c);
 }
 
 // The gradient in one pass over dy and x, the next row loaded while this one is worked on.
@@ -198,30 +218,28 @@ template <typename T, int EPT> struct BwdFit {
   static constexpr bool kGammaLds = (kAhead ? 2 : 1) * kRow + kSums + EPT > 96;
 };
 
-template <typename T, int LPR, int EPT, Cache LOAD, Cache STORE>
-__global__ void __launch_bounds__(kBwdBlock)
+template <typename T, int LPR, int EPT, Cache LOAD, Cache STORE, bool RAGGED>
+__global__ void __launch_bounds__(kMaxBlock)
 layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
                      const float* __restrict__ mean, const float* __restrict__ rstd,
                      const void* __restrict__ gamma, bool params_f32, int64_t rows, int cols,
-                     T* __restrict__ dx, void* __restrict__ dgamma, void* __restrict__ dbeta,
+                     int row_waves, T* __restrict__ dx, void* __restrict__ dgamma, void* __restrict__ dbeta,
                      float* __restrict__ part, int part_ld) {
   using Fit = BwdFit<T, EPT>;
-  constexpr int BLOCK = kBwdBlock, WAVES = BLOCK / 64;
-  constexpr int N = Piece<T>::N, NV = EPT / N, ROWS = BLOCK / LPR;
+  constexpr int N = Piece<T>::N, NV = EPT / N;
   constexpr bool kGammaLds = Fit::kGammaLds, kHold = Fit::kHold, kAhead = Fit::kAhead;
-  __shared__ float red[2][2][WAVES];
-  constexpr int kFold = ROWS > 1 ? BLOCK * EPT : 1;
-  __shared__ __attribute__((aligned(16))) float fold[kGammaLds && kFold < LPR * EPT ? LPR * EPT : kFold];
-  const int lane = threadIdx.x % LPR, group = row_group<LPR>();
+  __shared__ float red[2][2][kMaxWaves];
+  // the groups' sums before they are added, or gamma of one row
+  __shared__ __attribute__((aligned(16))) float fold[kMaxBlock * EPT];
+  const Lanes l = lanes_of<LPR>(row_waves);
   const float fcols = (float)cols;
-  const int64_t step = (int64_t)gridDim.x * ROWS;
-  const bool ragged = cols % N != 0;
+  const int64_t step = (int64_t)gridDim.x * l.groups;
   piece_t cx[NV], cd[NV], nx[NV], nd[NV];      // this row of x and dy, and the next
   float mu = 0.f, rs = 0.f, nmu = 0.f, nrs = 0.f;
-  if (kAhead && (int64_t)blockIdx.x * ROWS < rows) {
-    const int64_t r = turn_row((int64_t)blockIdx.x * ROWS, group, rows);
-    ld_rows<LOAD, LPR>(x + r * ldx, lane, cols, cx);
-    ld_rows<LOAD, LPR>(dy + r * lddy, lane, cols, cd);
+  if (kAhead && (int64_t)blockIdx.x * l.groups < rows) {
+    const int64_t r = turn_row((int64_t)blockIdx.x * l.groups, l.group, rows);
+    ld_rows<LOAD, LPR>(x + r * ldx, l, cols, cx);
+    ld_rows<LOAD, LPR>(dy + r * lddy, l, cols, cd);
     mu = mean[r], rs = rstd[r];
   }
   float gm[kGammaLds ? 1 : NV][N], ag[NV][N], ab[NV][N];
@@ -229,48 +247,48 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
   for (int v = 0; v < NV; ++v) {
     if constexpr (kGammaLds) {
       float g[N];
-      ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, g);
-      if (group == 0)
+      ld_params<T>(gamma, params_f32, (v * l.per_row + l.lane) * N, cols, 1.f, g);
+      if (l.group == 0)
 #pragma unroll
-        for (int i = 0; i < N; ++i) fold[(v * LPR + lane) * N + i] = g[i];
+        for (int i = 0; i < N; ++i) fold[(v * l.per_row + l.lane) * N + i] = g[i];
     } else {
-      ld_params<T>(gamma, params_f32, (v * LPR + lane) * N, cols, 1.f, gm[v]);
+      ld_params<T>(gamma, params_f32, (v * l.per_row + l.lane) * N, cols, 1.f, gm[v]);
     }
 #pragma unroll
     for (int i = 0; i < N; ++i) ag[v][i] = ab[v][i] = 0.f;
   }
-  if (kGammaLds && ROWS > 1) __syncthreads();     // one row group's lanes read their own
+  if (kGammaLds && l.groups > 1) __syncthreads();     // one row group's lanes read their own
   auto gamma_of = [&](int v, int i) {
-    if constexpr (kGammaLds) return fold[(v * LPR + lane) * N + i];
+    if constexpr (kGammaLds) return fold[(v * l.per_row + l.lane) * N + i];
     else return gm[v][i];
   };
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * ROWS; r0 < rows; r0 += step, turn ^= 1) {
-    const int64_t r = r0 + group;
+  for (int64_t r0 = (int64_t)blockIdx.x * l.groups; r0 < rows; r0 += step, turn ^= 1) {
+    const int64_t r = r0 + l.group;
     const bool live = r < rows;
-    const int64_t q = turn_row(kAhead ? r0 + step : r0, group, rows);
+    const int64_t q = turn_row(kAhead ? r0 + step : r0, l.group, rows);
     if (!kAhead) {
       if constexpr (kHold) {
-        ld_rows<LOAD, LPR>(x + q * ldx, lane, cols, cx);
-        ld_rows<LOAD, LPR>(dy + q * lddy, lane, cols, cd);
+        ld_rows<LOAD, LPR>(x + q * ldx, l, cols, cx);
+        ld_rows<LOAD, LPR>(dy + q * lddy, l, cols, cd);
       }
       mu = mean[q], rs = rstd[q];
     } else if (r0 + step < rows) {
-      ld_rows<LOAD, LPR>(x + q * ldx, lane, cols, nx);
-      ld_rows<LOAD, LPR>(dy + q * lddy, lane, cols, nd);
+      ld_rows<LOAD, LPR>(x + q * ldx, l, cols, nx);
+      ld_rows<LOAD, LPR>(dy + q * lddy, l, cols, nd);
       nmu = mean[q], nrs = rstd[q];
     }
     // a group past the last row takes its turn (the barriers must meet) with dy = 0
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * LPR + lane) * N;
+      const int c = (v * l.per_row + l.lane) * N;
       float fx[N], fd[N];
       if constexpr (!kHold) {
         cx[v] = ld_raw<LOAD, false>(x + q * ldx, c, cols);
         cd[v] = ld_raw<LOAD, false>(dy + q * lddy, c, cols);
       }
-      if (ragged) {
+      if constexpr (RAGGED) {
         cx[v] = cut<T>(cx[v], c, cols);
         cd[v] = cut<T>(cd[v], c, cols);
       }
@@ -288,15 +306,14 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
       }
       if constexpr (!kHold || kGammaLds) __builtin_amdgcn_sched_barrier(0);
     }
-    s1 = lanes_sum<(LPR < 64 ? LPR : 64)>(s1);
-    s2 = lanes_sum<(LPR < 64 ? LPR : 64)>(s2);
-    if constexpr (LPR > 64) {
-      constexpr int W = LPR / 64;
-      const int wave = row_group<64>(), w = wave / W * W + threadIdx.x % W;
+    s1 = lanes_sum<(LPR == 16 ? 16 : 64)>(s1);
+    s2 = lanes_sum<(LPR == 16 ? 16 : 64)>(s2);
+    if constexpr (LPR == 0) {
+      const int wave = threadIdx.x / 64;
       if (threadIdx.x % 64 == 0) { red[turn][0][wave] = s1; red[turn][1][wave] = s2; }
       __syncthreads();
-      s1 = lanes_sum<W>(red[turn][0][w]);
-      s2 = lanes_sum<W>(red[turn][1][w]);
+      s1 = waves_sum(red[turn][0], l);
+      s2 = waves_sum(red[turn][1], l);
     }
     if (kAhead) {
 #pragma unroll
@@ -305,16 +322,20 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
     const float m1 = s1 / fcols, m2 = s2 / fcols;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int c = (v * LPR + lane) * N;
+      const int c = (v * l.per_row + l.lane) * N;
       float fx[N], fd[N], o[N];
       if constexpr (kHold) {
         // from the 16 bytes again: the floats of the first sums would not fit
         arrived(cx[v]);
         arrived(cd[v]);
       } else {
-        cx[v] = cut<T>(ld_raw<LOAD, false>(x + q * ldx, c, cols), c, cols);
-        cd[v] = cut<T>(ld_raw<LOAD, false>(dy + q * lddy, c, cols), c, cols);
-        if (!live) cd[v] = piece_t{0, 0, 0, 0};
+        cx[v] = ld_raw<LOAD, false>(x + q * ldx, c, cols);
+        cd[v] = ld_raw<LOAD, false>(dy + q * lddy, c, cols);
+        if constexpr (RAGGED) {
+          cx[v] = cut<T>(cx[v], c, cols);
+          cd[v] = cut<T>(cd[v], c, cols);
+        }
+        if (!live || c >= cols) cd[v] = piece_t{0, 0, 0, 0};
       }
       unpack(cx[v], fx, T{});
       unpack(cd[v], fd, T{});
@@ -325,7 +346,10 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
         ag[v][i] = __builtin_fmaf(fd[i], xh, ag[v][i]);
         ab[v][i] += fd[i];
       }
-      if (live && dx) st_row<STORE>(dx + r * cols, c, cols, pack(o, T{}));
+      if (live && dx) {
+        if constexpr (RAGGED) st_row<STORE>(dx + r * cols, c, cols, pack(o, T{}));
+        else if (c < cols) st_piece<STORE>(elem_at(dx + r * cols, c), pack(o, T{}));
+      }
       if constexpr (!kHold || kGammaLds) __builtin_amdgcn_sched_barrier(0);
     }
     if (kAhead) {
@@ -341,29 +365,41 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
     if (!out) continue;
     float (&acc)[NV][N] = which == 0 ? ag : ab;
     float* dst = part ? part + ((int64_t)which * gridDim.x + blockIdx.x) * part_ld : nullptr;
-    if constexpr (ROWS > 1) {
+    if (l.groups > 1) {
       __syncthreads();
+      const int width = l.per_row * EPT;
+      // the four groups of a wave of narrow rows are added among its lanes first
+      const int at = (LPR == 16 ? (int)threadIdx.x / 64 : l.group) * width;
+      const bool writes = LPR != 16 || threadIdx.x % 64 < 16;
 #pragma unroll
-      for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        if constexpr (LPR == 16)
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[v][i] = lanes_sum<64, 16>(acc[v][i]);
+        if (!writes) continue;
 #pragma unroll
         for (int i = 0; i < N; i += 4)
-          *reinterpret_cast<f32x4_t*>(&fold[(group * NV * LPR + v * LPR + lane) * N + i]) =
+          *reinterpret_cast<f32x4_t*>(&fold[at + (v * l.per_row + l.lane) * N + i]) =
               f32x4_t{acc[v][i], acc[v][i + 1], acc[v][i + 2], acc[v][i + 3]};
+      }
       __syncthreads();
-      for (int c = threadIdx.x; c < cols; c += BLOCK) {
-        float s = fold[c];
+      for (int c = threadIdx.x * 4; c < cols; c += blockDim.x * 4) {
+        const f32x4_t t = groups_sum<LPR>(fold, width, l.groups, c);
+        if (dst) {                       // part_ld is cols rounded up to 4
+          *reinterpret_cast<sums_t*>(dst + c) = t;
+        } else {
 #pragma unroll
-        for (int k = 1; k < ROWS; ++k) s += fold[k * LPR * EPT + c];
-        if (dst) dst[c] = s;
-        else st_param<T>(out, params_f32, c, s);
+          for (int k = 0; k < 4; ++k)
+            if (c + k < cols) st_param<T>(out, params_f32, c + k, t[k]);
+        }
       }
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
 #pragma unroll
         for (int i = 0; i < N; i += 4) {
-          const int c = (v * LPR + lane) * N + i;
-          if (dst) {                       // part_ld is cols rounded up to 4
+          const int c = (v * l.per_row + l.lane) * N + i;
+          if (dst) {
             if (c < cols)
               *reinterpret_cast<sums_t*>(dst + c) =
                   sums_t{acc[v][i], acc[v][i + 1], acc[v][i + 2], acc[v][i + 3]};
@@ -407,45 +443,57 @@ layernorm_bwd_params_kernel(const float* __restrict__ part, int blocks, int cols
   }
 }
 
-// Lanes and elements per lane of a row of `cols` elements.
-struct Shape { int lpr, ept; };
+// The kernel of a row of `cols` elements, the waves of a row where it has whole ones, and the
+// lanes of a row. A lane's elements are 8, 16 or 32: with 16 a wave's 128 registers hold what the
+// kernels keep.
+struct Shape { int lpr, ept, waves, lanes; };
 Shape row_shape(int64_t cols) {
-  if (cols <= 128) return {16, 8};
-  if (cols <= 512) return {64, 8};
-  if (cols <= 1024) return {64, 16};
-  if (cols <= 2048) return {128, 16};
-  if (cols <= 4096) return {256, 16};
-  if (cols <= 8192) return {512, 16};
-  if (cols <= 16384) return {1024, 16};
-  return {1024, 32};
+  if (cols <= 16 * 8) return {16, 8, 0, 16};
+  if (cols <= 64 * 8) return {64, 8, 1, 64};
+  if (cols <= 64 * 16) return {64, 16, 1, 64};
+  const int ept = cols <= kMaxBlock * 16 ? 16 : 32;
+  const int waves = (int)((cols + 64 * ept - 1) / (64 * ept));
+  return {0, ept, waves, 64 * waves};
 }
 
+// Rows of a turn: as many as the workgroup's size takes whole.
+int groups_of(const Shape& k, int block) { return std::max(1, block / k.lanes); }
+
 int64_t bwd_blocks(int64_t rows, int64_t cols) {
-  const int64_t per = kBwdBlock / row_shape(cols).lpr, want = (rows + per - 1) / per;
+  const int64_t per = groups_of(row_shape(cols), kBwdBlock), want = (rows + per - 1) / per;
   return want <= 4 ? 1 : std::min(want, kBwdGrid);     // 4 turns cost less than another launch
 }
 
 template <typename T, int LPR, int EPT, Cache LOAD>
-hipError_t fwd(const LayerNormArgs& a, hipStream_t s) {
-  constexpr int B = fwd_block(LPR);
-  const int64_t blocks = std::min<int64_t>((a.rows + B / LPR - 1) / (B / LPR), kFwdGrid);
-  hipLaunchKernelGGL((layernorm_fwd_kernel<T, LPR, EPT, B, LOAD>), dim3((unsigned)blocks), dim3(B),
-                     0, s, static_cast<const T*>(a.x), a.ldx, a.gamma, a.beta,
-                     a.param_dtype == kF32, a.rows, (int)a.cols, a.eps, static_cast<T*>(a.y),
-                     a.mean, a.rstd);
+hipError_t fwd(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
+  const int groups = groups_of(k, kFwdBlock);
+  const int64_t blocks = std::min<int64_t>((a.rows + groups - 1) / groups, kFwdGrid);
+  hipLaunchKernelGGL((layernorm_fwd_kernel<T, LPR, EPT, LOAD>), dim3((unsigned)blocks),
+                     dim3((unsigned)(groups * k.lanes)), 0, s, static_cast<const T*>(a.x), a.ldx,
+                     a.gamma, a.beta, a.param_dtype == kF32, a.rows, (int)a.cols, k.waves, a.eps,
+                     static_cast<T*>(a.y), a.mean, a.rstd);
+  return hipGetLastError();
+}
+
+// RAGGED: the width is no whole number of pieces. Without the code for that, the kernels have
+// registers to spare (8000x2048 f32 40.2 us, with it 47.2 us).
+template <typename T, int LPR, int EPT, Cache LOAD, Cache STORE, bool RAGGED>
+hipError_t bwd_kernel(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
+  const int64_t blocks = bwd_blocks(a.rows, a.cols);
+  float* part = blocks > 1 ? a.workspace : nullptr;
+  const int part_ld = (int)((a.cols + 3) / 4 * 4);
+  hipLaunchKernelGGL((layernorm_bwd_kernel<T, LPR, EPT, LOAD, STORE, RAGGED>), dim3((unsigned)blocks),
+                     dim3((unsigned)(groups_of(k, kBwdBlock) * k.lanes)), 0, s,
+                     static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx, a.mean,
+                     a.rstd, a.gamma, a.param_dtype == kF32, a.rows, (int)a.cols, k.waves,
+                     static_cast<T*>(a.y), a.dgamma, a.dbeta, part, part_ld);
   return hipGetLastError();
 }
 
 template <typename T, int LPR, int EPT, Cache LOAD, Cache STORE>
-hipError_t bwd(const LayerNormArgs& a, hipStream_t s) {
-  const int64_t blocks = bwd_blocks(a.rows, a.cols);
-  float* part = blocks > 1 ? a.workspace : nullptr;
-  const int part_ld = (int)((a.cols + 3) / 4 * 4);
-  hipLaunchKernelGGL((layernorm_bwd_kernel<T, LPR, EPT, LOAD, STORE>), dim3((unsigned)blocks),
-                     dim3(kBwdBlock), 0, s, static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x),
-                     a.ldx, a.mean, a.rstd, a.gamma, a.param_dtype == kF32, a.rows, (int)a.cols,
-                     static_cast<T*>(a.y), a.dgamma, a.dbeta, part, part_ld);
-  return hipGetLastError();
+hipError_t bwd(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
+  return a.cols % Piece<T>::N ? bwd_kernel<T, LPR, EPT, LOAD, STORE, true>(a, k, s)
+                              : bwd_kernel<T, LPR, EPT, LOAD, STORE, false>(a, k, s);
 }
 
 template <typename P>
@@ -471,30 +519,24 @@ hipError_t bwd_params(const LayerNormArgs& a, hipStream_t s) {
 constexpr int64_t kKeepGrad = 24 << 20, kKeepRows = 96 << 20;
 
 template <typename T, int LPR, int EPT>
-hipError_t by_size(const LayerNormArgs& a, bool backward, hipStream_t s) {
+hipError_t by_size(const LayerNormArgs& a, const Shape& k, bool backward, hipStream_t s) {
   const int64_t bytes = a.rows * a.cols * (int64_t)sizeof(T);
   if (!backward)
-    return bytes <= kKeepRows ? fwd<T, LPR, EPT, kKeep>(a, s) : fwd<T, LPR, EPT, kStream>(a, s);
-  if (bytes <= kKeepGrad) return bwd<T, LPR, EPT, kKeep, kKeep>(a, s);
-  return bytes <= kKeepRows ? bwd<T, LPR, EPT, kStream, kKeep>(a, s)
-                          : bwd<T, LPR, EPT, kStream, kStream>(a, s);
+    return bytes <= kKeepRows ? fwd<T, LPR, EPT, kKeep>(a, k, s)
+                              : fwd<T, LPR, EPT, kStream>(a, k, s);
+  if (bytes <= kKeepGrad) return bwd<T, LPR, EPT, kKeep, kKeep>(a, k, s);
+  return bytes <= kKeepRows ? bwd<T, LPR, EPT, kStream, kKeep>(a, k, s)
+                            : bwd<T, LPR, EPT, kStream, kStream>(a, k, s);
 }
 
 template <typename T>
 hipError_t by_shape(const LayerNormArgs& a, bool backward, hipStream_t s) {
   const Shape k = row_shape(a.cols);
-#define FP8LIN_LN(L, E) \
-  if (k.lpr == L && k.ept == E) return by_size<T, L, E>(a, backward, s);
-  FP8LIN_LN(16, 8)
-  FP8LIN_LN(64, 8)
-  FP8LIN_LN(64, 16)
-  FP8LIN_LN(128, 16)
-  FP8LIN_LN(256, 16)
-  FP8LIN_LN(512, 16)
-  FP8LIN_LN(1024, 16)
-  FP8LIN_LN(1024, 32)
-#undef FP8LIN_LN
-  return hipErrorInvalidValue;
+  if (k.lpr == 16) return by_size<T, 16, 8>(a, k, backward, s);
+  if (k.lpr == 64)
+    return k.ept == 8 ? by_size<T, 64, 8>(a, k, backward, s)
+                      : by_size<T, 64, 16>(a, k, backward, s);
+  return k.ept == 16 ? by_size<T, 0, 16>(a, k, backward, s) : by_size<T, 0, 32>(a, k, backward, s);
 }
 
 }  // namespace

@@ -189,12 +189,12 @@ template <int CTRL> __device__ __forceinline__ float dpp(float v) {
   return __int_as_float(
       __builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
 }
-template <int LANES>
+template <int LANES, int FROM = 1>      // FROM: lanes already summed
 __device__ __forceinline__ float lanes_sum(float v) {
-  if constexpr (LANES >= 2) v += dpp<0xB1>(v);        // quad_perm 1,0,3,2
-  if constexpr (LANES >= 4) v += dpp<0x4E>(v);        // quad_perm 2,3,0,1
-  if constexpr (LANES >= 8) v += dpp<0x141>(v);       // mirror of each 8 lanes
-  if constexpr (LANES >= 16) v += dpp<0x140>(v);      // mirror of each 16 lanes
+  if constexpr (LANES >= 2 && FROM < 2) v += dpp<0xB1>(v);        // quad_perm 1,0,3,2
+  if constexpr (LANES >= 4 && FROM < 4) v += dpp<0x4E>(v);        // quad_perm 2,3,0,1
+  if constexpr (LANES >= 8 && FROM < 8) v += dpp<0x141>(v);       // mirror of each 8 lanes
+  if constexpr (LANES >= 16 && FROM < 16) v += dpp<0x140>(v);     // mirror of each 16 lanes
   if constexpr (LANES >= 32) {
     const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false,
                                                     false);
