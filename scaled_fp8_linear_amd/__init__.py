@@ -18,6 +18,8 @@ from ._abi import (FP8_A_E5M2, FP8_AMAX_ACCUMULATE, FP8_BLOCK_1x128, FP8_E5M2, F
                    fp8_moe_sort_workspace, fp8_moe_dispatch, fp8_moe_dispatch_bwd,
                    fp8_moe_combine, fp8_moe_combine_bwd)
 from .autograd import Fp8Linear, fp8_autocast, fp8_state
+from .experts import (ExpertBlock, ExpertPlan, LayerNorm, expert_combine, expert_dispatch,
+                      expert_plan, layer_norm)
 from .state import DelayedScalingLinear
 
 __all__ = ["fp8_quantize_amax", "fp8_scale_update", "fp8_linear_fwd", "fp8_linear_dgrad",
@@ -32,4 +34,6 @@ __all__ = ["fp8_quantize_amax", "fp8_scale_update", "fp8_linear_fwd", "fp8_linea
            "fp8_state", "FP8_DT_BF16", "FP8_DT_F16", "FP8_DT_F32",
            "fp8_layernorm_fwd", "fp8_layernorm_bwd", "fp8_layernorm_bwd_workspace",
            "fp8_moe_rows", "fp8_moe_sort", "fp8_moe_sort_workspace", "fp8_moe_dispatch",
-           "fp8_moe_dispatch_bwd", "fp8_moe_combine", "fp8_moe_combine_bwd"]
+           "fp8_moe_dispatch_bwd", "fp8_moe_combine", "fp8_moe_combine_bwd",
+           "ExpertBlock", "ExpertPlan", "LayerNorm", "expert_combine", "expert_dispatch",
+           "expert_plan", "layer_norm"]
