@@ -268,3 +268,30 @@ def test_oracle_moe():
     assert np.allclose(y, x * np.array([1, 0.5, 0.5, 1])[:, None])
     dys, dw, _ = moe.combine_bwd(x, xs, slot, w, 16)
     assert np.allclose(dys[5], 0.5 * x[2]) and dw[1, 1] == 0 and np.isclose(dw[3, 0], (x[3] ** 2).sum())
+
+
+# ---------------------------------------------------------------------- the native binding
+
+def test_binding_refuses_what_is_no_tensor(lib):
+    x, s = torch.zeros((4, 8)), torch.zeros(4)
+    slot = torch.zeros((4, 1), dtype=i32)
+    _raises(lambda: m.fp8_layernorm_fwd([1.0, 2.0]), "x must be a tensor")
+    _raises(lambda: m.fp8_layernorm_fwd(None), "x is needed")
+    _raises(lambda: m.fp8_layernorm_bwd(None, x, s, s), "dy is needed")
+    _raises(lambda: m.fp8_moe_sort(None, 4), "expert_idx is needed")
+    _raises(lambda: m.fp8_moe_dispatch(x, slot, None), "source is needed")
+    _raises(lambda: m.fp8_moe_combine(x, slot, None), "weights is needed")
+    _raises(lambda: m.fp8_moe_combine_bwd(x, x, slot, torch.zeros(4, dtype=i32), None),
+            "weights is needed")
+    _raises(lambda: m.fp8_layernorm_fwd(x, 3), "gamma must be a tensor")
+    _raises(lambda: m.fp8_moe_sort(slot, 1 << 40), "32 bits")
+    with pytest.raises(TypeError):
+        m.fp8_moe_sort(slot, "four")
+    with pytest.raises(TypeError):
+        m.fp8_layernorm_fwd(x, eps="small")
+
+
+def test_expert_block_argument_checks():
+    for topk in (0, 5):
+        with pytest.raises(ValueError):
+            m.ExpertBlock(16, 32, 4, topk)
