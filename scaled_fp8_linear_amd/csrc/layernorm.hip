@@ -413,6 +413,131 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
   }
 }
 
+// The gradient of few rows, in two kernels: dx by rows, and dgamma and dbeta by columns, with dy
+// and x read again from the caches. Workgroups of a row or two would write more partial sums
+// than they read (8 bytes a column each).
+template <typename T, int LPR, int EPT>
+__global__ void __launch_bounds__(LPR ? kFwdBlock : kMaxBlock)
+layernorm_dx_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+                    const float* __restrict__ mean, const float* __restrict__ rstd,
+                    const void* __restrict__ gamma, bool params_f32, int64_t rows, int cols,
+                    int row_waves, T* __restrict__ dx) {
+  constexpr int N = Piece<T>::N, NV = EPT / N;
+  __shared__ float red[2][2][kMaxWaves];
+  const Lanes l = lanes_of<LPR>(row_waves);
+  const float fcols = (float)cols;
+  const int64_t step = (int64_t)gridDim.x * l.groups;
+  float gm[NV][N];
+#pragma unroll
+  for (int v = 0; v < NV; ++v)
+    ld_params<T>(gamma, params_f32, (v * l.per_row + l.lane) * N, cols, 1.f, gm[v]);
+  int turn = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * l.groups; r0 < rows; r0 += step, turn ^= 1) {
+    const int64_t r = turn_row(r0, l.group, rows);
+    piece_t cx[NV], cd[NV];
+    ld_rows<kKeep, LPR>(x + r * ldx, l, cols, cx);
+    ld_rows<kKeep, LPR>(dy + r * lddy, l, cols, cd);
+    const float mu = mean[r], rs = rstd[r];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int c = (v * l.per_row + l.lane) * N;
+      float fx[N], fd[N];
+      cx[v] = cut<T>(cx[v], c, cols);
+      cd[v] = cut<T>(cd[v], c, cols);
+      unpack(cx[v], fx, T{});
+      unpack(cd[v], fd, T{});
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float xh = (fx[i] - mu) * rs;
+        const float g = fd[i] * gm[v][i];
+        s1 += g;
+        s2 = __builtin_fmaf(g, xh, s2);
+      }
+    }
+    s1 = lanes_sum<(LPR == 16 ? 16 : 64)>(s1);
+    s2 = lanes_sum<(LPR == 16 ? 16 : 64)>(s2);
+    if constexpr (LPR == 0) {
+      const int wave = threadIdx.x / 64;
+      if (threadIdx.x % 64 == 0) { red[turn][0][wave] = s1; red[turn][1][wave] = s2; }
+      __syncthreads();
+      s1 = waves_sum(red[turn][0], l);
+      s2 = waves_sum(red[turn][1], l);
+    }
+    const float m1 = s1 / fcols, m2 = s2 / fcols;
+    if (r0 + l.group >= rows) continue;
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      float fx[N], fd[N], o[N];
+      unpack(cx[v], fx, T{});
+      unpack(cd[v], fd, T{});
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float xh = (fx[i] - mu) * rs;
+        o[i] = rs * __builtin_fmaf(-xh, m2, __builtin_fmaf(fd[i], gm[v][i], -m1));
+      }
+      st_row<kKeep>(dx + r * cols, (v * l.per_row + l.lane) * N, cols, pack(o, T{}));
+    }
+  }
+}
+
+// A workgroup has 64 columns: the lanes of 128 bytes (256 of float32) a row, and as many rows at
+// once as its lanes hold. A lane's rows are added in order, then the lanes, then the waves.
+template <typename T>
+__global__ void __launch_bounds__(kMaxBlock)
+layernorm_cols_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
+                      const float* __restrict__ mean, const float* __restrict__ rstd,
+                      int64_t rows, int cols, bool params_f32, void* __restrict__ dgamma,
+                      void* __restrict__ dbeta) {
+  constexpr int N = Piece<T>::N, LANES = 64 / N, ROWS = kMaxBlock / LANES;
+  __shared__ __attribute__((aligned(16))) float sums[kMaxWaves][2][64];
+  const int cl = threadIdx.x % LANES, c = blockIdx.x * 64 + cl * N;
+  float ag[N], ab[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) ag[i] = ab[i] = 0.f;
+  if (c < cols) {
+#pragma unroll 2
+    for (int64_t r = threadIdx.x / LANES; r < rows; r += ROWS) {
+      const piece_t px = ld_raw<kKeep>(x + r * ldx, c, cols);
+      const piece_t pd = ld_raw<kKeep>(dy + r * lddy, c, cols);
+      const float mu = mean[r], rs = rstd[r];
+      float fx[N], fd[N];
+      unpack(cut<T>(px, c, cols), fx, T{});
+      unpack(cut<T>(pd, c, cols), fd, T{});
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        ag[i] = __builtin_fmaf(fd[i], (fx[i] - mu) * rs, ag[i]);
+        ab[i] += fd[i];
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if constexpr (LANES == 8) {                  // 8 lanes on, within 16
+      ag[i] += dpp<0x128>(ag[i]);
+      ab[i] += dpp<0x128>(ab[i]);
+    }
+    ag[i] = lanes_sum<64, 16>(ag[i]);
+    ab[i] = lanes_sum<64, 16>(ab[i]);
+  }
+  if (threadIdx.x % 64 < LANES) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      sums[threadIdx.x / 64][0][cl * N + i] = ag[i];
+      sums[threadIdx.x / 64][1][cl * N + i] = ab[i];
+    }
+  }
+  __syncthreads();
+  const int which = threadIdx.x / 64, k = threadIdx.x % 64;
+  void* out = which == 0 ? dgamma : dbeta;
+  if (which < 2 && out && (int)blockIdx.x * 64 + k < cols) {
+    float t = 0.f;
+#pragma unroll
+    for (int w = 0; w < kMaxWaves; ++w) t += sums[w][which][k];
+    st_param<T>(out, params_f32, blockIdx.x * 64 + k, t);
+  }
+}
+
 // out[c] = sum over the blocks of part[which][block][c]. 16 lanes take 64 columns, 64 such
 // lane groups the blocks k, k + 64, ...; their sums are then added in order.
 constexpr int kParamsRows = 64;
@@ -496,6 +621,26 @@ hipError_t bwd(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
                               : bwd_kernel<T, LPR, EPT, LOAD, STORE, false>(a, k, s);
 }
 
+template <typename T, int LPR, int EPT>
+hipError_t bwd_columns(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
+  const T *dy = static_cast<const T*>(a.dy), *x = static_cast<const T*>(a.x);
+  const bool f32 = a.param_dtype == kF32;
+  if (a.y && a.rows > 0) {
+    const int groups = groups_of(k, kFwdBlock);
+    const int64_t blocks = std::min<int64_t>((a.rows + groups - 1) / groups, kFwdGrid);
+    hipLaunchKernelGGL((layernorm_dx_kernel<T, LPR, EPT>), dim3((unsigned)blocks),
+                       dim3((unsigned)(groups * k.lanes)), 0, s, dy, a.lddy, x, a.ldx, a.mean,
+                       a.rstd, a.gamma, f32, a.rows, (int)a.cols, k.waves, static_cast<T*>(a.y));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (!a.dgamma && !a.dbeta) return hipSuccess;
+  hipLaunchKernelGGL((layernorm_cols_kernel<T>), dim3((unsigned)((a.cols + 63) / 64)),
+                     dim3(kMaxBlock), 0, s, dy, a.lddy, x, a.ldx, a.mean, a.rstd, a.rows,
+                     (int)a.cols, f32, a.dgamma, a.dbeta);
+  return hipGetLastError();
+}
+
 template <typename P>
 hipError_t bwd_params(const LayerNormArgs& a, hipStream_t s) {
   const int part_ld = (int)((a.cols + 3) / 4 * 4);
@@ -518,12 +663,25 @@ hipError_t bwd_params(const LayerNormArgs& a, hipStream_t s) {
 //   16384x4096 bf16 77.7 us streamed (kept 80.6), 32768x4096 f32 293 us (312).
 constexpr int64_t kKeepGrad = 24 << 20, kKeepRows = 96 << 20;
 
+// Few rows take layernorm_dx_kernel and layernorm_cols_kernel: 203x13184 bf16 10.9 us (with
+// partial sums 19.7), 300x4096 8.3 (11.0), 1000x4096 14.0 (16.8), 500x512 7.1 (7.5); not 2000x4096
+// 21.4 (18.1), 1000x1300 12.6 (11.4), 600x4096 f32 16.8 (14.7). The second reading costs by the
+// bytes of a column, the partial sums by the width. One turn of one workgroup needs neither: 64x128
+// 5.4 us, by columns 6.0. Tensors that the caches do not keep are read once.
+bool by_columns(int64_t rows, int64_t cols, int64_t elem) {
+  const Shape k = row_shape(cols);
+  return k.ept <= 16 && rows > groups_of(k, kBwdBlock) && rows * elem <= 1024 + cols / 4 &&
+         rows * cols * elem <= kKeepGrad;
+}
+
 template <typename T, int LPR, int EPT>
 hipError_t by_size(const LayerNormArgs& a, const Shape& k, bool backward, hipStream_t s) {
   const int64_t bytes = a.rows * a.cols * (int64_t)sizeof(T);
   if (!backward)
     return bytes <= kKeepRows ? fwd<T, LPR, EPT, kKeep>(a, k, s)
                               : fwd<T, LPR, EPT, kStream>(a, k, s);
+  if constexpr (EPT <= 16)
+    if (by_columns(a.rows, a.cols, sizeof(T))) return bwd_columns<T, LPR, EPT>(a, k, s);
   if (bytes <= kKeepGrad) return bwd<T, LPR, EPT, kKeep, kKeep>(a, k, s);
   return bytes <= kKeepRows ? bwd<T, LPR, EPT, kStream, kKeep>(a, k, s)
                             : bwd<T, LPR, EPT, kStream, kStream>(a, k, s);
@@ -542,15 +700,22 @@ hipError_t by_shape(const LayerNormArgs& a, bool backward, hipStream_t s) {
 }  // namespace
 
 int64_t layernorm_bwd_workspace(int64_t rows, int64_t cols) {
+  // for either size of element: by_columns with the larger takes the fewer sizes
+  if (by_columns(rows, cols, sizeof(float))) return 0;
   const int64_t b = bwd_blocks(rows, cols);
   return b > 1 ? 2 * b * ((cols + 3) / 4 * 4) * (int64_t)sizeof(float) : 0;
 }
+
+namespace {
+int64_t elem_size(int dtype) { return dtype == kF32 ? 4 : 2; }
+}  // namespace
 
 hipError_t launch_layernorm(const LayerNormArgs& a, bool backward, hipStream_t s) {
   const hipError_t e = a.dtype == kBF16  ? by_shape<BF16>(a, backward, s)
                        : a.dtype == kF16 ? by_shape<F16>(a, backward, s)
                                          : by_shape<float>(a, backward, s);
-  if (e != hipSuccess || !backward || !a.workspace) return e;
+  if (e != hipSuccess || !backward || !a.workspace || by_columns(a.rows, a.cols, elem_size(a.dtype)))
+    return e;
   if (a.param_dtype == kBF16) return bwd_params<BF16>(a, s);
   return a.param_dtype == kF16 ? bwd_params<F16>(a, s) : bwd_params<float>(a, s);
 }
