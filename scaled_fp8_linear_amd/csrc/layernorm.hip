@@ -10,7 +10,9 @@
 // stays in registers between the sums, so the variance is the sum of the squared distances
 // from the mean (not a difference of two large sums) and x is read from memory once.
 // Everything here is bound by memory: 2 (forward) or 3 (backward) tensor reads and writes
-// against about 8 and 14 flops an element.
+// against about 8 and 14 flops an element. Measured on one MI355X, where a large copy reaches
+// 5.2 TB/s: forward 8192x4096 bf16 24.2 us, 5.5 TB/s; backward 8192x4096 bf16 40.6 us for the
+// rows, 4.9 TB/s, and 4.8 us for the partial sums; 4096x14336 f32 124 and 5.8 us, 5.7 TB/s.
 #include <algorithm>
 
 #include "launch.h"
@@ -208,6 +210,7 @@ __device__ __forceinline__ f32x4_t groups_sum(const float* fold, int width, int 
 // layernorm_bwd_params_kernel adds in a fixed order. A single workgroup writes dgamma and
 // dbeta itself. Every order is fixed, so results repeat.
 //
+// Loading ahead took 8192x4096 bf16 from 57.6 to 44.2 us, 4096x14336 f32 from 177 to 143 us.
 // A wave has 128 registers (16 waves a compute unit). What does not fit beside the two sums:
 // gamma (then in LDS), the next row (then not loaded ahead), and for the widest float32 rows
 // this row itself (then read again, from the cache, for dx).
