@@ -416,26 +416,29 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
   }
 }
 
-// The gradient of few rows, in two kernels: dx by rows, and dgamma and dbeta by columns, with dy
-// and x read again from the caches. Workgroups of a row or two would write more partial sums
-// than they read (8 bytes a column each).
+// The gradient of few rows: dx by rows, and dgamma and dbeta by columns, with dy and x read again
+// from the caches. Workgroups of a row or two would write more partial sums than they read (8
+// bytes a column each). Neither part needs the other, so one launch holds both kinds of
+// workgroup.
 template <typename T, int LPR, int EPT>
-__global__ void __launch_bounds__(LPR ? kFwdBlock : kMaxBlock)
-layernorm_dx_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
-                    const float* __restrict__ mean, const float* __restrict__ rstd,
-                    const void* __restrict__ gamma, bool params_f32, int64_t rows, int cols,
-                    int row_waves, T* __restrict__ dx) {
+__device__ __forceinline__ void dx_rows(int block, int blocks, const T* __restrict__ dy,
+                                        int64_t lddy, const T* __restrict__ x, int64_t ldx,
+                                        const float* __restrict__ mean,
+                                        const float* __restrict__ rstd,
+                                        const void* __restrict__ gamma, bool params_f32,
+                                        int64_t rows, int cols, int row_waves,
+                                        T* __restrict__ dx) {
   constexpr int N = Piece<T>::N, NV = EPT / N;
   __shared__ float red[2][2][kMaxWaves];
   const Lanes l = lanes_of<LPR>(row_waves);
   const float fcols = (float)cols;
-  const int64_t step = (int64_t)gridDim.x * l.groups;
+  const int64_t step = (int64_t)blocks * l.groups;
   float gm[NV][N];
 #pragma unroll
   for (int v = 0; v < NV; ++v)
     ld_params<T>(gamma, params_f32, (v * l.per_row + l.lane) * N, cols, 1.f, gm[v]);
   int turn = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * l.groups; r0 < rows; r0 += step, turn ^= 1) {
+  for (int64_t r0 = (int64_t)block * l.groups; r0 < rows; r0 += step, turn ^= 1) {
     const int64_t r = turn_row(r0, l.group, rows);
     piece_t cx[NV], cd[NV];
     ld_rows<kKeep, LPR>(x + r * ldx, l, cols, cx);
@@ -487,20 +490,23 @@ layernorm_dx_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict_
 // A workgroup has 64 columns: the lanes of 128 bytes (256 of float32) a row, and as many rows at
 // once as its lanes hold. A lane's rows are added in order, then the lanes, then the waves.
 template <typename T>
-__global__ void __launch_bounds__(kMaxBlock)
-layernorm_cols_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
-                      const float* __restrict__ mean, const float* __restrict__ rstd,
-                      int64_t rows, int cols, bool params_f32, void* __restrict__ dgamma,
-                      void* __restrict__ dbeta) {
-  constexpr int N = Piece<T>::N, LANES = 64 / N, ROWS = kMaxBlock / LANES;
-  __shared__ __attribute__((aligned(16))) float sums[kMaxWaves][2][64];
-  const int cl = threadIdx.x % LANES, c = blockIdx.x * 64 + cl * N;
+__device__ __forceinline__ void sum_cols(int block, const T* __restrict__ dy, int64_t lddy,
+                                         const T* __restrict__ x, int64_t ldx,
+                                         const float* __restrict__ mean,
+                                         const float* __restrict__ rstd, int64_t rows, int cols,
+                                         bool params_f32, void* __restrict__ dgamma,
+                                         void* __restrict__ dbeta) {
+  constexpr int N = Piece<T>::N, LANES = 64 / N;
+  __shared__ float sums[kMaxWaves][2][64];
+  const int cl = threadIdx.x % LANES, c = block * 64 + cl * N;
+  const int at_once = (int)blockDim.x / LANES;
   float ag[N], ab[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) ag[i] = ab[i] = 0.f;
   if (c < cols) {
+    // bound by what one compute unit reads: more rows in flight change nothing
 #pragma unroll 2
-    for (int64_t r = threadIdx.x / LANES; r < rows; r += ROWS) {
+    for (int64_t r = threadIdx.x / LANES; r < rows; r += at_once) {
       const piece_t px = ld_raw<kKeep>(x + r * ldx, c, cols);
       const piece_t pd = ld_raw<kKeep>(dy + r * lddy, c, cols);
       const float mu = mean[r], rs = rstd[r];
@@ -531,14 +537,33 @@ layernorm_cols_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restric
     }
   }
   __syncthreads();
+  // 128 sums; a workgroup has 256 lanes at least
   const int which = threadIdx.x / 64, k = threadIdx.x % 64;
   void* out = which == 0 ? dgamma : dbeta;
-  if (which < 2 && out && (int)blockIdx.x * 64 + k < cols) {
+  if (which < 2 && out && block * 64 + k < cols) {
+    const int waves = (int)blockDim.x / 64;
     float t = 0.f;
 #pragma unroll
-    for (int w = 0; w < kMaxWaves; ++w) t += sums[w][which][k];
-    st_param<T>(out, params_f32, blockIdx.x * 64 + k, t);
+    for (int w = 0; w < kMaxWaves; ++w) t += w < waves ? sums[w][which][k] : 0.f;
+    st_param<T>(out, params_f32, block * 64 + k, t);
   }
+}
+
+// The first `col_blocks` workgroups take columns, the others rows.
+template <typename T, int LPR, int EPT>
+__global__ void __launch_bounds__(kMaxBlock)
+layernorm_bwd_few_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x,
+                         int64_t ldx, const float* __restrict__ mean,
+                         const float* __restrict__ rstd, const void* __restrict__ gamma,
+                         bool params_f32, int64_t rows, int cols, int row_waves, int col_blocks,
+                         T* __restrict__ dx, void* __restrict__ dgamma,
+                         void* __restrict__ dbeta) {
+  const int block = blockIdx.x;
+  if (block < col_blocks)
+    sum_cols(block, dy, lddy, x, ldx, mean, rstd, rows, cols, params_f32, dgamma, dbeta);
+  else
+    dx_rows<T, LPR, EPT>(block - col_blocks, (int)gridDim.x - col_blocks, dy, lddy, x, ldx, mean,
+                         rstd, gamma, params_f32, rows, cols, row_waves, dx);
 }
 
 // out[c] = sum over the blocks of part[which][block][c]. 16 lanes take 64 columns, 64 such
@@ -626,21 +651,15 @@ hipError_t bwd(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
 
 template <typename T, int LPR, int EPT>
 hipError_t bwd_columns(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
-  const T *dy = static_cast<const T*>(a.dy), *x = static_cast<const T*>(a.x);
-  const bool f32 = a.param_dtype == kF32;
-  if (a.y && a.rows > 0) {
-    const int groups = groups_of(k, kFwdBlock);
-    const int64_t blocks = std::min<int64_t>((a.rows + groups - 1) / groups, kFwdGrid);
-    hipLaunchKernelGGL((layernorm_dx_kernel<T, LPR, EPT>), dim3((unsigned)blocks),
-                       dim3((unsigned)(groups * k.lanes)), 0, s, dy, a.lddy, x, a.ldx, a.mean,
-                       a.rstd, a.gamma, f32, a.rows, (int)a.cols, k.waves, static_cast<T*>(a.y));
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (!a.dgamma && !a.dbeta) return hipSuccess;
-  hipLaunchKernelGGL((layernorm_cols_kernel<T>), dim3((unsigned)((a.cols + 63) / 64)),
-                     dim3(kMaxBlock), 0, s, dy, a.lddy, x, a.ldx, a.mean, a.rstd, a.rows,
-                     (int)a.cols, f32, a.dgamma, a.dbeta);
+  const int groups = groups_of(k, kBwdBlock);
+  const int64_t row_blocks = a.y ? (a.rows + groups - 1) / groups : 0;
+  const int64_t col_blocks = a.dgamma || a.dbeta ? (a.cols + 63) / 64 : 0;
+  hipLaunchKernelGGL((layernorm_bwd_few_kernel<T, LPR, EPT>),
+                     dim3((unsigned)(row_blocks + col_blocks)),
+                     dim3((unsigned)(groups * k.lanes)), 0, s, static_cast<const T*>(a.dy), a.lddy,
+                     static_cast<const T*>(a.x), a.ldx, a.mean, a.rstd, a.gamma,
+                     a.param_dtype == kF32, a.rows, (int)a.cols, k.waves, (int)col_blocks,
+                     static_cast<T*>(a.y), a.dgamma, a.dbeta);
   return hipGetLastError();
 }
 
@@ -666,15 +685,15 @@ hipError_t bwd_params(const LayerNormArgs& a, hipStream_t s) {
 //   16384x4096 bf16 77.7 us streamed (kept 80.6), 32768x4096 f32 293 us (312).
 constexpr int64_t kKeepGrad = 24 << 20, kKeepRows = 96 << 20;
 
-// Few rows take layernorm_dx_kernel and layernorm_cols_kernel: 203x13184 bf16 10.9 us (with
-// partial sums 19.7), 300x4096 8.3 (11.0), 1000x4096 14.0 (16.8), 500x512 7.1 (7.5); not 2000x4096
-// 21.4 (18.1), 1000x1300 12.6 (11.4), 600x4096 f32 16.8 (14.7). The second reading costs by the
-// bytes of a column, the partial sums by the width. One turn of one workgroup needs neither: 64x128
-// 5.4 us, by columns 6.0. Tensors that the caches do not keep are read once.
+// Few rows take layernorm_bwd_few_kernel. The second reading costs by the rows, the partial sums
+// by the width and another launch: 33x3776 bf16 4.6 us (with partial sums 9.7), 203x13184 9.2
+// (19.7), 1000x512 6.5 (8.1), 2000x4096 16.1 (18.1), 1600x8192 21.6 (29.6), but 2000x512 11.6 (8.2)
+// and 3000x4096 22.3 (21.2); 500x72 f32 5.5 (8.0), 1021x5003 21.7 (26.6), but 1000x1300 14.9 (12.1).
+// Above kFewBytes the caches do not hold dy and x until then (600x16384 f32 38.8 us, 35.1).
+constexpr int64_t kFewBytes = 32 << 20;
 bool by_columns(int64_t rows, int64_t cols, int64_t elem) {
-  const Shape k = row_shape(cols);
-  return k.ept <= 16 && rows > groups_of(k, kBwdBlock) && rows * elem <= 1024 + cols / 4 &&
-         rows * cols * elem <= kKeepGrad;
+  return row_shape(cols).ept <= 16 && rows > 0 && rows * elem <= 2000 + cols / 2 &&
+         rows * cols * elem <= kFewBytes;
 }
 
 template <typename T, int LPR, int EPT>

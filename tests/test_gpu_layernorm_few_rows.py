@@ -26,7 +26,7 @@ def host(t):
     return t.detach().cpu().double().numpy()
 
 
-# one turn of one workgroup, one row more; the largest number of rows by columns, one more
+# sizes of one turn of a workgroup and one row more, and around earlier and present limits
 @pytest.mark.parametrize("rows,cols", [(1, 5), (64, 100), (65, 100), (16, 600), (17, 601), (8, 2000),
                                        (9, 2001), (2, 5003), (268, 193), (524, 100), (525, 100),
                                        (262, 97), (263, 97), (672, 1280), (673, 1280), (416, 2561),
@@ -88,3 +88,26 @@ def test_single_rows_of_f16(lib, cols):
     for a, w, b, n in zip(got, ln.backward(*args), ln.backward_bounds(*args, 2.0 ** -11, 2.0 ** -11),
                           ("dx", "dgamma", "dbeta")):
         assert_within(host(a), w, b + 2.0 ** -25, n)
+
+
+# the largest number of rows by columns and one more: 2-byte types up to 1000 + cols / 4 rows,
+# float32 half of that
+@pytest.mark.parametrize("rows,cols,dt", [(1025, 100, "bf16"), (1026, 100, "bf16"),
+                                          (1503, 2015, "f16"), (1504, 2015, "f16"),
+                                          (512, 97, "f32"), (513, 97, "f32"), (1125, 5003, "f32"),
+                                          (1126, 5003, "f32"), (2048, 8192, "bf16"),
+                                          (2049, 8192, "bf16")])
+def test_limits_of_few_rows(lib, rows, cols, dt):
+    g = torch.Generator().manual_seed(rows + cols)
+    x, dy = (torch.randn(rows, cols, generator=g).to(DT[dt]).cuda() for _ in range(2))
+    gamma = (1 + 0.3 * torch.randn(cols, generator=g)).cuda()
+    note(f"layernorm_bwd at the limit of few rows {rows}x{cols} {dt}")
+    _, mean, rstd = lib.fp8_layernorm_fwd(x, gamma)
+    got = lib.fp8_layernorm_bwd(dy, x, mean, rstd, gamma)
+    torch.cuda.synchronize()
+    args = (host(dy), host(x), host(mean), host(rstd), host(gamma))
+    for a, w, b, n in zip(got, ln.backward(*args),
+                          ln.backward_bounds(*args, torch.finfo(DT[dt]).eps / 2, 2.0 ** -24),
+                          ("dx", "dgamma", "dbeta")):
+        tol = b + 2.0 ** -25 if dt == "f16" and n == "dx" else b      # float16's subnormal step
+        assert_within(host(a), w, tol, n)
