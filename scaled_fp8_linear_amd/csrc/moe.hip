@@ -620,6 +620,9 @@ hipError_t combine_bwd_rows(const MoeArgs& a, hipStream_t s) {
 }
 template <typename T, int W, Cache C>
 hipError_t combine_bwd_choices(const MoeArgs& a, hipStream_t s) {
+  // choices a walk over the row: 8192 tokens, 8 of 64, width 4096 bf16 226 us with eight, 235 us
+  // with two walks of four; two steps of a row in flight only up to four (223 us with eight there,
+  // but 1000 tokens of width 2048 17.2 us against 15.1)
   if (a.topk <= 2) return combine_bwd_rows<T, W, 2, C>(a, s);
   return a.topk <= 4 ? combine_bwd_rows<T, W, 4, C>(a, s) : combine_bwd_rows<T, W, 8, C>(a, s);
 }
