@@ -341,7 +341,19 @@ template <typename T, int PIECES> struct Zero {
 // sorted rows: 8192 tokens to 8 of 64 experts, width 4096 bf16 in 108.6 us, 5.6 TB/s. They
 // stream (117.8 us kept, and no size was found where that cost); the tokens' rows are kept, 122
 // us with the sort against 136 us streamed.
-template <typename T, int PIECES>
+// The `bytes` first bytes (a multiple of the element, at most 16) of a piece.
+template <Cache C, typename T>
+__device__ __forceinline__ void st_first(T* p, piece_t v, int bytes) {
+  if (bytes >= 16) st_piece<C>(p, v);
+  else if (bytes > 0) st_row<C>(p, 0, bytes / (int)sizeof(T), v);
+}
+
+// LINES: rows whose width is no whole number of 128-byte lines. A store of a wave then covers
+// whole lines of its row, which begin somewhere else in every row, so the token's row is loaded
+// (from the cache) for each: 4000 tokens, 7 of 64, width 4097 bf16 with the sort 60.0 us, 71.0
+// without (width 4096: 56.2); 1066 tokens, 7 of 91, width 6030 f32 53.7 and 61.9; but 8192 tokens,
+// 2 of 8, width 5001 51.9 and 48.4, so from three choices on.
+template <typename T, int PIECES, bool LINES>
 __global__ void __launch_bounds__(kMoveBlock)
 moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restrict__ slot,
                     const int32_t* __restrict__ source, int64_t tokens, int topk, int64_t rows,
@@ -359,6 +371,25 @@ moe_dispatch_kernel(const T* __restrict__ x, int64_t ldx, const int32_t* __restr
   const int c0 = (int)(u % chunks) * kCols + lane * N;
   const T* src = x + t * ldx;
   const Choices choices(slot, nullptr, t, topk, rows);
+  if constexpr (LINES) {
+    for (int j = 0; j < topk; ++j) {
+      const int r = choices.row_of(j);
+      if (r < 0) continue;
+      T* dst = xs + (int64_t)r * cols;
+      const int before = (int)(((uintptr_t)dst & 127) / sizeof(T));
+      piece_t v[PIECES];
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i)
+        v[i] = ld_raw<kKeep>(src, max(c0 + i * 64 * N - before, 0), cols);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        const int c = c0 + i * 64 * N - before, from = max(c, 0);
+        st_first<kStream>(elem_at(dst, min(from, cols)), cut<T>(v[i], from, cols),
+                          (min(c + N, cols) - from) * (int)sizeof(T));
+      }
+    }
+    return;
+  }
   piece_t v[PIECES];
 #pragma unroll
   for (int i = 0; i < PIECES; ++i) v[i] = ld_raw<kKeep>(src, c0 + i * 64 * N, cols);
@@ -558,12 +589,13 @@ unsigned move_blocks(int64_t waves) { return (unsigned)((waves + kMoveWaves - 1)
 // Waves that are on the card at once. A launch of no more is bound by a wave's own waits.
 constexpr int64_t kResidentWaves = 256 * 32;
 
-template <typename T, int PIECES>
+template <typename T, int PIECES, bool LINES>
 hipError_t dispatch_rows(const MoeArgs& a, hipStream_t s) {
-  const uint32_t chunks = row_chunks<T>(a.cols, PIECES);
+  // a row's lines begin up to a line before it
+  const uint32_t chunks = row_chunks<T>(a.cols + (LINES ? 128 / (int)sizeof(T) : 0), PIECES);
   const int64_t zeros = Zero<T, PIECES>::waves(a.rows, a.cols);
   const unsigned blocks = move_blocks(a.tokens * chunks + zeros);
-  hipLaunchKernelGGL((moe_dispatch_kernel<T, PIECES>), dim3(blocks), dim3(kMoveBlock), 0, s,
+  hipLaunchKernelGGL((moe_dispatch_kernel<T, PIECES, LINES>), dim3(blocks), dim3(kMoveBlock), 0, s,
                      static_cast<const T*>(a.x), a.ldx, a.slot, a.source, a.tokens, a.topk, a.rows,
                      (int)a.cols, chunks, (uint32_t)zeros, static_cast<T*>(a.out));
   return hipGetLastError();
@@ -574,8 +606,9 @@ hipError_t dispatch_rows(const MoeArgs& a, hipStream_t s) {
 template <typename T>
 hipError_t dispatch(const MoeArgs& a, hipStream_t s) {
   const int64_t chunks = row_chunks<T>(a.cols, 1);
-  return chunks <= 1 || a.tokens * chunks <= kResidentWaves ? dispatch_rows<T, 1>(a, s)
-                                                            : dispatch_rows<T, 4>(a, s);
+  if (chunks <= 1 || a.tokens * chunks <= kResidentWaves) return dispatch_rows<T, 1, false>(a, s);
+  const bool lines = a.topk > 2 && a.cols * sizeof(T) % 128 != 0;
+  return lines ? dispatch_rows<T, 4, true>(a, s) : dispatch_rows<T, 4, false>(a, s);
 }
 
 // Tensors of rows up to 96 MiB together are kept in the caches, larger ones stream. Measured over

@@ -154,3 +154,25 @@ def test_exchanges_of_large_tensors(lib, tokens, topk, cols, dt):
         mag[kept] = prod.abs().sum(1)
         tol = (8 * np.ceil(cols / 256) + 24) * U * mag + 1e-30
         assert bool(((dw[:, j].double() - want).abs() <= tol).all())
+
+
+@pytest.mark.parametrize("tokens,topk,cols,dt,skip", [(2500, 3, 2049, "bf16", 1),
+                                                      (2500, 4, 2080, "f16", 7),
+                                                      (1500, 3, 1999, "f32", 5),
+                                                      (300, 3, 77, "bf16", 3)])
+def test_dispatch_into_a_cut_of_a_buffer(lib, tokens, topk, cols, dt, skip):
+    """An output that starts anywhere in a line, its rows ending anywhere: every element of it is
+    written, and nothing beside it."""
+    experts = 11
+    slot, source, _, _ = lib.fp8_moe_sort(torch.from_numpy(routing(5, tokens, topk, experts)).cuda(),
+                                          experts)
+    rows = source.numel()
+    x = torch.randn(tokens, cols + 3, device="cuda").to(DT[dt])[:, 2:cols + 2]
+    flat = torch.full((rows * cols + 200,), 7.0, dtype=DT[dt], device="cuda")
+    xs = flat[skip:skip + rows * cols].view(rows, cols)
+    note(f"moe_dispatch into a cut, tokens={tokens} cols={cols} {dt} skip={skip}")
+    lib.fp8_moe_dispatch(x, slot, source, xs=xs)
+    torch.cuda.synchronize()
+    live = source >= 0
+    assert torch.equal(xs[live], x[(source[live] // topk).long()]) and not xs[~live].any()
+    assert bool((flat[:skip] == 7).all()) and bool((flat[skip + rows * cols:] == 7).all())
