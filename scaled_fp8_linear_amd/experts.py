@@ -135,11 +135,11 @@ def expert_combine(ys, weights, plan: ExpertPlan):
 
 
 class ExpertBlock(torch.nn.Module):
-    """x + experts(layer_norm(x)): a router picks ``topk`` of ``experts`` two-layer MLPs for
-    each token. The MLPs are Fp8Linear layers, so inside ``fp8_autocast`` they run in FP8 and
-    outside in bf16. Tokens whose choice is masked (``expert_mask`` [experts] False) go to the
-    others. The experts' row ranges are read back to the host once per forward, since each
-    expert's products are launches of their own."""
+    """x + experts(layer_norm(x)) of bf16 tokens: a router picks ``topk`` of ``experts``
+    two-layer MLPs for each token. The MLPs are Fp8Linear layers, so inside ``fp8_autocast``
+    they run in FP8 and outside in bf16. Tokens whose choice is masked (``expert_mask``
+    [experts] False) go to the others. The experts' row ranges are read back to the host once
+    per forward, since each expert's products are launches of their own."""
 
     def __init__(self, cols: int, hidden: int, experts: int, topk: int, device=None,
                  eps: float = 1e-5):
@@ -167,7 +167,11 @@ class ExpertBlock(torch.nn.Module):
         return idx.masked_fill(gone, -1), weights
 
     def forward(self, x, expert_mask=None):
-        x2d = x.reshape(-1, x.shape[-1])
+        cols = self.norm.weight.shape[0]
+        if x.dtype != torch.bfloat16 or x.shape[-1] != cols:
+            raise ValueError(f"expected bfloat16 tokens of width {cols}, got {x.dtype} of shape "
+                             f"{tuple(x.shape)}")
+        x2d = x.reshape(-1, cols)
         h = self.norm(x2d)
         idx, weights = self.route(h, expert_mask)
         plan = expert_plan(idx, self.experts)

@@ -295,3 +295,6 @@ def test_expert_block_argument_checks():
     for topk in (0, 5):
         with pytest.raises(ValueError):
             m.ExpertBlock(16, 32, 4, topk)
+    block = m.ExpertBlock(16, 32, 4, 2)
+    _raises(lambda: block(torch.zeros((3, 16))), "bfloat16")
+    _raises(lambda: block(torch.zeros((3, 15), dtype=bf)), "width 16")
