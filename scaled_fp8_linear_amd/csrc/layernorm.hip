@@ -55,8 +55,9 @@ typedef float sums_t __attribute__((ext_vector_type(4), aligned(4)));
 // Which lanes own a row. Narrow rows take 16 or 64 lanes (LPR); wide ones (LPR = 0) as many
 // whole waves as their pieces fill, a value of the launch, since rounding it up to a power of two
 // would leave almost half the lanes without elements just above one (8000x4104 bf16 forward 31.5
-// us, with five waves 27.1 us; 4000x9000 50.0 and 35.5 us; backward 8000x4104 56.5 and 51.5 us). For a whole wave or more the row is
-// the same in all lanes of a wave, so that row addresses are scalar.
+// us, with five waves 27.1 us; 4000x9000 50.0 and 35.5 us; backward 8000x4104 56.5 and 51.5 us).
+// For a whole wave or more the row is the same in all lanes of a wave, so that row addresses are
+// scalar.
 struct Lanes {
   int per_row, lane, group, groups;       // lanes of a row, this one; the row of a turn, rows of it
 };
@@ -123,7 +124,8 @@ template <typename T, int LPR, int EPT, Cache LOAD>
 __global__ void __launch_bounds__(LPR ? kFwdBlock : kMaxBlock)
 layernorm_fwd_kernel(const T* __restrict__ x, int64_t ldx, const void* __restrict__ gamma,
                      const void* __restrict__ beta, bool params_f32, int64_t rows, int cols,
-                     int row_waves, float eps, T* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out) {
+                     int row_waves, float eps, T* __restrict__ y, float* __restrict__ mean_out,
+                     float* __restrict__ rstd_out) {
   constexpr int N = Piece<T>::N, NV = EPT / N;
   // gamma and beta stay in registers beside the row up to 16 elements a lane
   constexpr bool kHeld = EPT <= 16;
@@ -226,8 +228,8 @@ __global__ void __launch_bounds__(kMaxBlock)
 layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ x, int64_t ldx,
                      const float* __restrict__ mean, const float* __restrict__ rstd,
                      const void* __restrict__ gamma, bool params_f32, int64_t rows, int cols,
-                     int row_waves, T* __restrict__ dx, void* __restrict__ dgamma, void* __restrict__ dbeta,
-                     float* __restrict__ part, int part_ld) {
+                     int row_waves, T* __restrict__ dx, void* __restrict__ dgamma,
+                     void* __restrict__ dbeta, float* __restrict__ part, int part_ld) {
   using Fit = BwdFit<T, EPT>;
   constexpr int N = Piece<T>::N, NV = EPT / N;
   constexpr bool kGammaLds = Fit::kGammaLds, kHold = Fit::kHold, kAhead = Fit::kAhead;
@@ -635,8 +637,8 @@ hipError_t bwd_kernel(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
   const int64_t blocks = bwd_blocks(a.rows, a.cols);
   float* part = blocks > 1 ? a.workspace : nullptr;
   const int part_ld = (int)((a.cols + 3) / 4 * 4);
-  hipLaunchKernelGGL((layernorm_bwd_kernel<T, LPR, EPT, LOAD, STORE, RAGGED>), dim3((unsigned)blocks),
-                     dim3((unsigned)(groups_of(k, kBwdBlock) * k.lanes)), 0, s,
+  hipLaunchKernelGGL((layernorm_bwd_kernel<T, LPR, EPT, LOAD, STORE, RAGGED>),
+                     dim3((unsigned)blocks), dim3((unsigned)(groups_of(k, kBwdBlock) * k.lanes)), 0, s,
                      static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx, a.mean,
                      a.rstd, a.gamma, a.param_dtype == kF32, a.rows, (int)a.cols, k.waves,
                      static_cast<T*>(a.y), a.dgamma, a.dbeta, part, part_ld);
@@ -736,8 +738,8 @@ hipError_t launch_layernorm(const LayerNormArgs& a, bool backward, hipStream_t s
   const hipError_t e = a.dtype == kBF16  ? by_shape<BF16>(a, backward, s)
                        : a.dtype == kF16 ? by_shape<F16>(a, backward, s)
                                          : by_shape<float>(a, backward, s);
-  if (e != hipSuccess || !backward || !a.workspace || by_columns(a.rows, a.cols, elem_size(a.dtype)))
-    return e;
+  if (e != hipSuccess || !backward || !a.workspace) return e;
+  if (by_columns(a.rows, a.cols, elem_size(a.dtype))) return e;
   if (a.param_dtype == kBF16) return bwd_params<BF16>(a, s);
   return a.param_dtype == kF16 ? bwd_params<F16>(a, s) : bwd_params<float>(a, s);
 }
