@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "launch.h"
+#include "moe_rows.h"
 #include "rows.h"
 
 namespace fp8lin {
@@ -209,7 +210,7 @@ moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int experts, int bits,
         }
       }
     }
-    padded = (tot + multiple - 1) / multiple * multiple;
+    padded = padded_count(tot, multiple);
     pre = int2{padded, own};
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
@@ -266,7 +267,7 @@ moe_sort_kernel(const I* __restrict__ idx, int64_t pairs, int experts, int bits,
   for (int i = t;; i += kSortBlock) {
     const int x = (int)blockIdx.x + (int)gridDim.x * (i / 16);
     if (x >= experts) break;
-    for (int r = pad[x].x + i % 16; r < pad[x].y; r += 16) source[r] = -1;
+    each_padding_row(pad[x].x, pad[x].y, i % 16, [&](int r) { source[r] = -1; });
   }
   if constexpr (kOrder) {
     __syncthreads();
