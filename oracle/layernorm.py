@@ -10,7 +10,9 @@ terms is off by at most D U times the sum of the absolute values (first order); 
 chains are a lane's elements (at most 32), the lanes of a wave (6 steps) and the waves of a
 row (at most 16), so D = 64 covers a row sum with the roundings of its terms. The sums over
 rows split the rows over lanes and workgroups; their D grows slowly with the rows. The stored
-value is rounded once to its type, half a step relative to the value, ``half``.
+value is rounded once to its type: half a step relative to the value, ``half``, but never less
+than half the type's smallest subnormal, ``tiny`` (float16: 2^-25, which is what counts below
+2^-14; float32 and bfloat16 have theirs below 1e-39).
 """
 import numpy as np
 
@@ -38,8 +40,8 @@ def forward(x, gamma, beta, eps):
     return y, mean, rstd
 
 
-def forward_bounds(x, gamma, beta, eps, half):
-    """Bounds of (y, mean, rstd)."""
+def forward_bounds(x, gamma, beta, eps, half, tiny=0.0):
+    """Bounds of (y, mean, rstd); half, tiny: y's type."""
     x = np.asarray(x, np.float64)
     n = x.shape[1]
     y, mean, rstd = forward(x, gamma, beta, eps)
@@ -52,7 +54,8 @@ def forward_bounds(x, gamma, beta, eps, half):
     rel = np.minimum(rel * 1.01 + rel * rel, 1e300)
     e_y = (g[None, :] * rstd[:, None] * (e_mean[:, None] + U * d)
            + g[None, :] * d * (rstd * (rel + 3 * U))[:, None] + U * (np.abs(y) + b[None, :]))
-    return e_y * (1 + 2 * half) + half * np.abs(y) + 1e-30, e_mean + U * np.abs(mean), rel * rstd
+    return (e_y * (1 + 2 * half) + half * np.abs(y) + tiny + 1e-30, e_mean + U * np.abs(mean),
+            rel * rstd)
 
 
 def backward(dy, x, mean, rstd, gamma):
@@ -66,8 +69,8 @@ def backward(dy, x, mean, rstd, gamma):
     return dx, (dy * xh).sum(0), dy.sum(0)
 
 
-def backward_bounds(dy, x, mean, rstd, gamma, half, half_p):
-    """Bounds of (dx, dgamma, dbeta); half_p: the parameters' type."""
+def backward_bounds(dy, x, mean, rstd, gamma, half, half_p, tiny=0.0, tiny_p=0.0):
+    """Bounds of (dx, dgamma, dbeta); half, tiny: dx's type, half_p, tiny_p: the parameters'."""
     dy, x = np.asarray(dy, np.float64), np.asarray(x, np.float64)
     rows, n = x.shape
     rs = np.asarray(rstd, np.float64)[:, None]
@@ -80,6 +83,6 @@ def backward_bounds(dy, x, mean, rstd, gamma, half, half_p):
     e = np.abs(rs) * (4 * U * g + e1 + 3 * U * m1 + xh * e2 + 7 * U * xh * m2) + 2 * U * np.abs(dx)
     d = col_chain(rows)
     e_dg, e_db = (d + 3) * U * (np.abs(dy) * xh).sum(0), d * U * np.abs(dy).sum(0)
-    return (e * (1 + 2 * half) + half * np.abs(dx) + 1e-30,
-            e_dg * (1 + 2 * half_p) + half_p * np.abs(dgamma) + 1e-30,
-            e_db * (1 + 2 * half_p) + half_p * np.abs(dbeta) + 1e-30)
+    return (e * (1 + 2 * half) + half * np.abs(dx) + tiny + 1e-30,
+            e_dg * (1 + 2 * half_p) + half_p * np.abs(dgamma) + tiny_p + 1e-30,
+            e_db * (1 + 2 * half_p) + half_p * np.abs(dbeta) + tiny_p + 1e-30)
