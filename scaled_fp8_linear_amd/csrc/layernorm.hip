@@ -209,8 +209,8 @@ __device__ __forceinline__ f32x4_t groups_sum(const float* fold, int width, int 
 // Lanes own columns as in the forward, so each also sums dy xh and dy of its columns over the
 // workgroup's rows, in registers; at the end the workgroup's row groups are added in LDS in
 // group order and written as one row of partial sums, part[which][block][part_ld], which
-// layernorm_bwd_params_kernel adds in a fixed order. A single workgroup writes dgamma and
-// dbeta itself. Every order is fixed, so results repeat.
+// layernorm_bwd_params_kernel adds in a fixed order. A single workgroup (few rows of more than
+// 16384 columns, one group) writes dgamma and dbeta itself. Every order is fixed, so results repeat.
 //
 // Loading ahead took 8192x4096 bf16 from 57.6 to 44.2 us, 4096x14336 f32 from 177 to 143 us.
 // A wave has 128 registers (16 waves a compute unit). What does not fit beside the two sums:
@@ -388,16 +388,10 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
               f32x4_t{acc[v][i], acc[v][i + 1], acc[v][i + 2], acc[v][i + 3]};
       }
       __syncthreads();
-      for (int c = threadIdx.x * 4; c < cols; c += blockDim.x * 4) {
-        const f32x4_t t = groups_sum<LPR>(fold, width, l.groups, c);
-        if (dst) {                       // part_ld is cols rounded up to 4
-          *reinterpret_cast<sums_t*>(dst + c) = t;
-        } else {
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (c + k < cols) st_param<T>(out, params_f32, c + k, t[k]);
-        }
-      }
+      // rows of so few lanes that there are several groups never come to a single workgroup
+      // (by_columns takes those), so dst is there; part_ld is cols rounded up to 4
+      for (int c = threadIdx.x * 4; c < cols; c += blockDim.x * 4)
+        *reinterpret_cast<sums_t*>(dst + c) = groups_sum<LPR>(fold, width, l.groups, c);
     } else {
 #pragma unroll
       for (int v = 0; v < NV; ++v)
@@ -692,9 +686,12 @@ constexpr int64_t kKeepGrad = 24 << 20, kKeepRows = 96 << 20;
 // (19.7), 1000x512 6.5 (8.1), 2000x4096 16.1 (18.1), 1600x8192 21.6 (29.6), but 2000x512 11.6 (8.2)
 // and 3000x4096 22.3 (21.2); 500x72 f32 5.5 (8.0), 1021x5003 21.7 (26.6), but 1000x1300 14.9 (12.1).
 // Above kFewBytes the caches do not hold dy and x until then (600x16384 f32 38.8 us, 35.1).
+//
+// Up to 16384 columns this takes all that bwd_blocks gives to one workgroup, no rows at all among
+// it: those are at most 4 turns of 64 rows, and of 4 * 16384 elements, as a turn is.
 constexpr int64_t kFewBytes = 32 << 20;
 bool by_columns(int64_t rows, int64_t cols, int64_t elem) {
-  return row_shape(cols).ept <= 16 && rows > 0 && rows * elem <= 2000 + cols / 2 &&
+  return row_shape(cols).ept <= 16 && rows * elem <= 2000 + cols / 2 &&
          rows * cols * elem <= kFewBytes;
 }
 
