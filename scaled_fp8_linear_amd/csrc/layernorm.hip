@@ -209,8 +209,10 @@ __device__ __forceinline__ f32x4_t groups_sum(const float* fold, int width, int 
 // Lanes own columns as in the forward, so each also sums dy xh and dy of its columns over the
 // workgroup's rows, in registers; at the end the workgroup's row groups are added in LDS in
 // group order and written as one row of partial sums, part[which][block][part_ld], which
-// layernorm_bwd_params_kernel adds in a fixed order. A single workgroup (few rows of more than
-// 16384 columns, one group) writes dgamma and dbeta itself. Every order is fixed, so results repeat.
+// layernorm_bwd_params_kernel adds in a fixed order. A single workgroup (one row of more than 16384
+// columns, or none) writes dgamma and dbeta itself; two rows take another launch rather than another
+// turn (2x16388 bf16 18.9 us, in turns 35.5 us; 4x32768 f32 38.3 and 90.4 us). Every order is
+// fixed, so results repeat.
 //
 // Loading ahead took 8192x4096 bf16 from 57.6 to 44.2 us, 4096x14336 f32 from 177 to 143 us.
 // A wave has 128 registers (16 waves a compute unit). What does not fit beside the two sums:
@@ -610,7 +612,7 @@ int groups_of(const Shape& k, int block) { return std::max(1, block / k.lanes); 
 
 int64_t bwd_blocks(int64_t rows, int64_t cols) {
   const int64_t per = groups_of(row_shape(cols), kBwdBlock), want = (rows + per - 1) / per;
-  return want <= 4 ? 1 : std::min(want, kBwdGrid);     // 4 turns cost less than another launch
+  return std::max<int64_t>(1, std::min(want, kBwdGrid));
 }
 
 template <typename T, int LPR, int EPT, Cache LOAD>
@@ -688,7 +690,7 @@ constexpr int64_t kKeepGrad = 24 << 20, kKeepRows = 96 << 20;
 // Above kFewBytes the caches do not hold dy and x until then (600x16384 f32 38.8 us, 35.1).
 //
 // Up to 16384 columns this takes all that bwd_blocks gives to one workgroup, no rows at all among
-// it: those are at most 4 turns of 64 rows, and of 4 * 16384 elements, as a turn is.
+// it: that is one turn, at most 64 rows and 16384 elements.
 constexpr int64_t kFewBytes = 32 << 20;
 bool by_columns(int64_t rows, int64_t cols, int64_t elem) {
   return row_shape(cols).ept <= 16 && rows * elem <= 2000 + cols / 2 &&
