@@ -1,6 +1,6 @@
-"""The gradient of a few rows of more than 16384 columns, which one workgroup or a few take, and of no
-rows at any width: against the float64 oracle, with every output wanted alone, in given buffers, with
-a workspace of NaN, and again."""
+"""The gradient of a few rows of more than 16384 columns, which one workgroup or a few take, and of
+no rows at any width: against the float64 oracle, with every output wanted alone, in given buffers,
+with a workspace of NaN, and again."""
 import numpy as np
 import pytest
 
