@@ -116,38 +116,39 @@ __device__ __forceinline__ piece_t pack(const float (&f)[4], float) {
 // The piece at column c of a row of `cols` elements, in two steps, so that a kernel can have
 // several loads in flight: ld_raw issues one 16-byte load (of the row's last 16 bytes where
 // the piece is cut off by the row's end or lies past it), and cut moves a cut-off piece's
-// elements down and sets what is past the row to 0. Nothing outside the row is touched; rows
-// shorter than a piece (kShort: they may be) are read element by element.
-template <Cache C, bool kShort = true, typename T>
+// elements down and sets what is past the row to 0, or with FILL kOwn to elements of the row (any
+// of them; ld_raw has to be told too). Nothing outside the row is touched; rows shorter than a piece
+// (kShort: they may be) are read element by element.
+enum Fill { kZero = 0, kOwn = 1 };
+template <Cache C, bool kShort = true, Fill FILL = kZero, typename T>
 __device__ __forceinline__ piece_t ld_raw(const T* row, int c, int cols) {
   constexpr int N = Piece<T>::N;
   if (!kShort || cols >= N) return ld_piece<C>(elem_at(row, c + N <= cols ? c : cols - N));
   piece_t v = {0u, 0u, 0u, 0u};
-  if (c == 0) {
-    if constexpr (sizeof(T) == 4) {
+  if (c == 0 || FILL == kOwn) {
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < cols) v[i] = __builtin_bit_cast(uint32_t, row[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (i < cols) v[i / 2] |= (uint32_t)row[i].u << (16 * (i & 1));
+    for (int i = 0; i < N; ++i) {
+      if (i >= cols && FILL == kZero) continue;
+      const T* e = row + (i < cols ? i : 0);
+      if constexpr (sizeof(T) == 4) v[i] = __builtin_bit_cast(uint32_t, *e);
+      else v[i / 2] |= (uint32_t)e->u << (16 * (i & 1));
     }
   }
   return v;
 }
-template <typename T>
+template <typename T, Fill FILL = kZero>
 __device__ __forceinline__ piece_t cut(piece_t v, int c, int cols) {
   constexpr int N = Piece<T>::N;
+  constexpr bool own = FILL == kOwn;
   if (c + N <= cols || cols < N) return v;
   const int past = (c + N - cols) * (int)sizeof(T);        // bytes past the row's end
-  if (past >= 16) return piece_t{0u, 0u, 0u, 0u};
-  if (past & 8) v = piece_t{v[2], v[3], 0u, 0u};
-  if (past & 4) v = piece_t{v[1], v[2], v[3], 0u};
+  if (past >= 16) return own ? v : piece_t{0u, 0u, 0u, 0u};
+  if (past & 8) v = piece_t{v[2], v[3], own ? v[0] : 0u, own ? v[1] : 0u};
+  if (past & 4) v = piece_t{v[1], v[2], v[3], own ? v[0] : 0u};
   if constexpr (sizeof(T) == 2) {
     if (past & 2)
       v = piece_t{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16,
-                  v[3] >> 16};
+                  v[3] >> 16 | (own ? v[0] << 16 : 0u)};
   }
   return v;
 }
