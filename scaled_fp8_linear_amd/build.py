@@ -2,7 +2,8 @@
 ``_binding.so`` (the CPython side of the row operators) with g++ against torch's headers.
 
 Usage: ``python -m scaled_fp8_linear_amd.build`` (or ``__graft_entry__.build()``).
-Every call recompiles; object files go to ``scaled_fp8_linear_amd/_build/``.
+Every call recompiles; object files go to ``scaled_fp8_linear_amd/_build/``. Without g++ or torch's
+headers the library is still built, and the call ends with an error that says what is missing.
 """
 from __future__ import annotations
 
@@ -76,13 +77,21 @@ def build(verbose: bool = False) -> str:
     with ThreadPoolExecutor(min(8, len(SOURCES) + 1)) as ex:
         binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
-        binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), f"--offload-arch={ARCH}", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    # the library does not need the binding, so it is there even if the binding cannot be built;
+    # an older binding, which may not fit it, is not left beside it
+    try:
+        binding.result()
+    except Exception as e:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        raise RuntimeError(f"built {LIB}, but not {BINDING}, which the Python calls of the row "
+                           f"operators need: {e}") from e
     if verbose:
         print(f"built {LIB}\nbuilt {BINDING}")
     return LIB
