@@ -426,8 +426,8 @@ int fp8_layernorm_bwd_workspace(int64_t rows, int64_t cols, int64_t* bytes);
  * fp8_layernorm_bwd -- the gradient: with xh = (x - mean) * rstd and g = dy * gamma,
  *   dx = rstd * (g - mean_c(g) - xh * mean_c(g * xh)),
  *   dgamma = sum over rows of dy * xh, dbeta = sum over rows of dy,
- * in one pass over dy and x (for few rows a second one, for the sums). All sums run in a fixed
- * order (the same result on every call).
+ * in one pass over dy and x (a second one for the sums of few rows, and for dx of rows of more
+ * than 16384 columns). All sums run in a fixed order (the same result on every call).
  *
  *   dy, x        [rows, cols] of `dtype`, row strides lddy and ldx.
  *   mean, rstd   float32 [rows], of the forward.

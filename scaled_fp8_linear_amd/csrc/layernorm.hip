@@ -210,14 +210,18 @@ __device__ __forceinline__ f32x4_t groups_sum(const float* fold, int width, int 
 // workgroup's rows, in registers; at the end the workgroup's row groups are added in LDS in
 // group order and written as one row of partial sums, part[which][block][part_ld], which
 // layernorm_bwd_params_kernel adds in a fixed order. A single workgroup (one row of more than 16384
-// columns, or none) writes dgamma and dbeta itself; two rows take another launch rather than another
-// turn (2x16388 bf16 18.9 us, in turns 35.5 us; 4x32768 f32 38.3 and 90.4 us). Every order is
-// fixed, so results repeat.
+// columns, or none) writes dgamma and dbeta itself; two rows take another launch rather than
+// another turn (2x16388 bf16 18.9 us, in turns 35.5 us; 4x32768 f32 38.3 and 90.4 us). Every
+// order is fixed, so results repeat.
 //
 // Loading ahead took 8192x4096 bf16 from 57.6 to 44.2 us, 4096x14336 f32 from 177 to 143 us.
 // A wave has 128 registers (16 waves a compute unit). What does not fit beside the two sums:
-// gamma (then in LDS), the next row (then not loaded ahead), and for the widest float32 rows
-// this row itself (then read again, from the cache, for dx).
+// gamma (then in LDS), the next row (then not loaded ahead), and above 16384 columns, for every
+// type, this row itself (then read again, from the cache, for dx). The count leaves no room for
+// addresses and for cutting a row off: the compiler spills 3 registers a lane of float32 rows of
+// 513 to 1024 columns, 7 where they are cut off, 17 of cut-off float32 rows of 1025 to 16384
+// columns (4000x5003 62.6 us, 4000x5004 51.5 us), and 48 to 196 of all rows above 16384
+// (1000x20000 bf16 102 us for 120 MB).
 template <typename T, int EPT> struct BwdFit {
   static constexpr int kRow = 2 * EPT * (int)sizeof(T) / 4, kSums = 2 * EPT;
   static constexpr bool kHold = kRow + kSums < 96;
@@ -300,9 +304,9 @@ layernorm_bwd_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict
         cd[v] = cut<T>(cd[v], c, cols);
       }
       // past the row dy is 0 and x is some of the row's own values: nothing is added, and a NaN
-      // there is one that the row has anyway (with x = 0 instead, -mean * rstd may leave float32 for
-      // a row of one large value). Rows that do not stay in registers are cut to 0 and xh with them,
-      // which takes fewer (1000x20001 bf16 123.9 us, 129.6 us the other way)
+      // there is one that the row has anyway (with x = 0 instead, -mean * rstd may leave float32
+      // for a row of one large value). Rows that do not stay in registers are cut to 0 and xh
+      // with them, which takes fewer (1000x20001 bf16 123.9 us, 129.6 us the other way)
       if (!live || c >= cols) cd[v] = piece_t{0, 0, 0, 0};
       unpack(cx[v], fx, T{});
       unpack(cd[v], fd, T{});
@@ -637,8 +641,8 @@ hipError_t bwd_kernel(const LayerNormArgs& a, const Shape& k, hipStream_t s) {
   float* part = blocks > 1 ? a.workspace : nullptr;
   const int part_ld = (int)((a.cols + 3) / 4 * 4);
   hipLaunchKernelGGL((layernorm_bwd_kernel<T, LPR, EPT, LOAD, STORE, RAGGED>),
-                     dim3((unsigned)blocks), dim3((unsigned)(groups_of(k, kBwdBlock) * k.lanes)), 0, s,
-                     static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx, a.mean,
+                     dim3((unsigned)blocks), dim3((unsigned)(groups_of(k, kBwdBlock) * k.lanes)), 0,
+                     s, static_cast<const T*>(a.dy), a.lddy, static_cast<const T*>(a.x), a.ldx, a.mean,
                      a.rstd, a.gamma, a.param_dtype == kF32, a.rows, (int)a.cols, k.waves,
                      static_cast<T*>(a.y), a.dgamma, a.dbeta, part, part_ld);
   return hipGetLastError();
@@ -688,9 +692,9 @@ constexpr int64_t kKeepGrad = 24 << 20, kKeepRows = 96 << 20;
 
 // Few rows take layernorm_bwd_few_kernel. The second reading costs by the rows, the partial sums
 // by the width and another launch: 33x3776 bf16 4.6 us (with partial sums 9.7), 203x13184 9.2
-// (19.7), 1000x512 6.5 (8.1), 2000x4096 16.1 (18.1), 1600x8192 21.6 (29.6), but 2000x512 11.6 (8.2)
-// and 3000x4096 22.3 (21.2); 500x72 f32 5.5 (8.0), 1021x5003 21.7 (26.6), but 1000x1300 14.9 (12.1).
-// Above kFewBytes the caches do not hold dy and x until then (600x16384 f32 38.8 us, 35.1).
+// (19.7), 1000x512 6.5 (8.1), 2000x4096 15.7 (17.5), 1600x8192 21.5 (27.3), but 2000x512 11.6 (8.2)
+// and 3000x4096 22.3 (21.2); 500x72 f32 5.5 (8.0), 1021x5003 21.3 (29.0), but 1000x1300 14.9
+// (12.1). Above kFewBytes the caches do not hold dy and x until then (600x16384 f32 38.8 us, 35.1).
 //
 // Up to 16384 columns this takes all that bwd_blocks gives to one workgroup, no rows at all among
 // it: that is one turn, at most 64 rows and 16384 elements.

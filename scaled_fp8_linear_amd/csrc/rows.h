@@ -116,9 +116,9 @@ __device__ __forceinline__ piece_t pack(const float (&f)[4], float) {
 // The piece at column c of a row of `cols` elements, in two steps, so that a kernel can have
 // several loads in flight: ld_raw issues one 16-byte load (of the row's last 16 bytes where
 // the piece is cut off by the row's end or lies past it), and cut moves a cut-off piece's
-// elements down and sets what is past the row to 0, or with FILL kOwn to elements of the row (any
-// of them; ld_raw has to be told too). Nothing outside the row is touched; rows shorter than a piece
-// (kShort: they may be) are read element by element.
+// elements down and sets what is past the row to 0, or with FILL kOwn to elements of the row
+// (any of them; ld_raw has to be told too). Nothing outside the row is touched; rows shorter
+// than a piece (kShort: they may be) are read element by element.
 enum Fill { kZero = 0, kOwn = 1 };
 template <Cache C, bool kShort = true, Fill FILL = kZero, typename T>
 __device__ __forceinline__ piece_t ld_raw(const T* row, int c, int cols) {

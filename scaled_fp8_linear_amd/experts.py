@@ -8,8 +8,10 @@ A pre-norm expert block is
     ys = every expert's linears on its own rows     # Fp8Linear, rows a multiple of 16
     y  = expert_combine(ys, weights, plan)          # fp8_moe_combine / _combine_bwd
 
-Padding rows of xs are zero and so are the gradients of ys there, so an expert's linears run
-on padded rows without masks: they add nothing to amaxes, weight gradients or bias gradients.
+Padding rows of xs are zero and so are the gradients of ys there, so an expert's linears run on
+padded rows without masks: nothing is added to weight or bias gradients, and without biases (and
+with an activation that maps 0 to 0) nothing to amaxes. After a linear with a bias the padding
+rows hold the activation of the bias, which the amax of the next linear's input includes.
 Everything runs on the current stream; gradients of gradients are not defined.
 """
 from __future__ import annotations

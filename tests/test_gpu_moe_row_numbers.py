@@ -1,5 +1,6 @@
 """The expert sort into the largest buffer there is: two pairs of one expert, padded to 2^31 - 1
-rows (8.6 GB of row numbers), where a padded count or a step past the last row would leave 32 bits."""
+rows (8.6 GB of row numbers), where a padded count or a step past the last row would leave 32
+bits."""
 import pytest
 
 from tests.gpu_util import note

@@ -15,7 +15,7 @@ from scaled_fp8_linear_amd import build
 SOURCE = r"""
 #include "moe_rows.h"
 extern "C" int32_t padded(int32_t n, int32_t multiple) { return fp8lin::padded_count(n, multiple); }
-// the lane's rows into out, at most `room` of them; returns how many there would be (up to 4 room)
+// the lane's rows into out, `room` of them at most; returns how many there would be (to 4 room)
 extern "C" int32_t padding_rows(int32_t from, int32_t to, int32_t lane, int32_t* out, int32_t room) {
   int32_t n = 0;
   struct Enough {};
