@@ -519,6 +519,147 @@ int fp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ld
                         int64_t tokens, int32_t topk, int64_t rows, int64_t cols, int dtype,
                         void* dys, float* dw, void* stream);
 
+/*
+ * The router, the experts' products and the activation between them: an expert block routes its
+ * tokens (fp8_moe_route), sorts and dispatches them (above), and runs every expert's linears on
+ * its own rows, by the block recipe and without reading the row counts back to the host.
+ *
+ * Source: [NeMo] (the mixture-of-experts runs, dp=2 ep=2; TE's "recipe=block").
+ */
+
+/* Bytes of workspace fp8_moe_route needs (host arithmetic; 0 for few tokens). */
+int fp8_moe_route_workspace(int64_t tokens, int32_t experts, int64_t* bytes);
+
+/*
+ * fp8_moe_route -- the topk experts of each token and their weights, with the losses that keep
+ * the experts evenly used. With p = softmax(logits) and T = tokens_valid:
+ *
+ *   logits       [tokens, experts] of `dtype` (fp8_dtype), row stride ldl; 1 <= experts <= 512.
+ *   tokens_valid tokens at or past it are padding: their logits are not read, they choose nothing
+ *                and add to no count or loss.
+ *   topk         1 <= topk <= min(experts, 64).
+ *   expert_idx   int32 [tokens, topk] out: the experts of the largest logits in falling order,
+ *                equal ones by the lower index. A logit of -inf is never chosen; where a row has
+ *                fewer others, -1 (which fp8_moe_sort drops). NaN ranks above every number.
+ *   weights      float32 [tokens, topk] out: p of the choice, with normalize != 0 divided by the
+ *                sum over the token's choices; 0 where expert_idx is -1.
+ *   lse          float32 [tokens] out: log(sum exp(logits)); -inf for a row without a finite logit,
+ *                0 for padding.
+ *   counts       int32 [experts] out: the pairs that chose the expert.
+ *   losses       float32 [2] out: the balance loss experts / (T topk) sum_e counts[e] mean_t p[t, e]
+ *                (1 where evenly used) and the z-loss mean_t lse[t]^2 (rows without a finite logit
+ *                add nothing); both 0 for T = 0.
+ *   workspace    at least fp8_moe_route_workspace() bytes, 4-byte aligned; NULL if that is 0.
+ * All sums are float32, in a fixed order.
+ */
+int fp8_moe_route(const void* logits, int64_t ldl, int64_t tokens, int64_t tokens_valid,
+                  int32_t experts, int32_t topk, int dtype, int normalize, int32_t* expert_idx,
+                  float* weights, float* lse, int32_t* counts, float* losses, void* workspace,
+                  int64_t workspace_bytes, void* stream);
+
+/*
+ * fp8_moe_route_bwd -- the gradient of the weights and of both losses (counts are constants).
+ *   logits, lse, expert_idx, weights, counts   as of the forward, with the same sizes.
+ *   dweights     float32 [tokens, topk] or NULL (0); entries of dropped choices are not used.
+ *   dlosses      float32 [2] or NULL (0).
+ *   dlogits      [tokens, experts] of `dtype` out, dense; 0 for padding and for logits of -inf.
+ */
+int fp8_moe_route_bwd(const void* logits, int64_t ldl, const float* lse, const int32_t* expert_idx,
+                      const float* weights, const int32_t* counts, const float* dweights,
+                      const float* dlosses, int64_t tokens, int64_t tokens_valid, int32_t experts,
+                      int32_t topk, int dtype, int normalize, void* dlogits, void* stream);
+
+/* Activations of fp8_act_quantize. */
+typedef enum fp8_act { FP8_ACT_RELU = 0, FP8_ACT_SILU = 1, FP8_ACT_GELU = 2 } fp8_act;
+
+/*
+ * fp8_act_quantize -- the activation between two linears, quantized by the block recipe's 1x128
+ * tiles as it is made, and its input kept in 8 bits for the backward.
+ *
+ *   h            [rows, cols] of `dtype`, or with gated != 0 [rows, 2 cols] = [g | u]; row stride
+ *                ldh. cols a positive multiple of 128, below 2^17; rows below 2^23.
+ *   rows_valid   rows at or past it are padding: not read, taken as zeros.
+ *   act          FP8_ACT_RELU, FP8_ACT_SILU (x / (1 + exp(-x))) or FP8_ACT_GELU (the form with
+ *                tanh). a = act(h), or act(g) u.
+ *   q, scale     e4m3 [rows, cols], float32 [rows, cols/128]: a in tiles of 128 along a row.
+ *   q_t, scale_t e4m3 [cols, rows], float32 [cols, rows/128]: a transposed, in tiles of 128 along
+ *                the rows (rows a multiple of 128).
+ *   hq, hscale   e4m3 and float32 of h's width: h in tiles of 128 along a row, what
+ *                fp8_act_quantize_bwd takes.
+ * Each pair may be NULL; codes 16-byte aligned. A tile's scale is max(amax, 1e-12)/448, its
+ * codes those of the values times 448/max(amax, 1e-12), both factors within 2 units in the last
+ * place. A NaN is coded as NaN and does not enter amax; an infinity makes its tile's scale
+ * infinite.
+ */
+int fp8_act_quantize(const void* h, int64_t ldh, int64_t rows, int64_t rows_valid, int64_t cols,
+                     int act, int gated, int dtype, void* q, float* scale, void* q_t,
+                     float* scale_t, void* hq, float* hscale, void* stream);
+
+/*
+ * fp8_act_quantize_bwd -- the gradient dh of the activation from da and the 8-bit h: da act'(h),
+ * or [da u act'(g) | da act(g)].
+ *
+ *   da           [rows, cols] of `dtype`, row stride ldda; rows at or past rows_valid are not read.
+ *   hq, hscale   of fp8_act_quantize, w = cols or 2 cols wide.
+ *   q, scale     e4m3 [rows, w], float32 [rows, w/128]: dh in tiles of 128 along a row.
+ *   q_t, scale_t e4m3 [w, rows], float32 [w, rows/128]: dh transposed, in tiles along the rows.
+ *   dh           [rows, w] of `dtype`, dense: dh itself.
+ * Each pair and dh may be NULL.
+ */
+int fp8_act_quantize_bwd(const void* da, int64_t ldda, const void* hq, const float* hscale,
+                         int64_t rows, int64_t rows_valid, int64_t cols, int act, int gated,
+                         int dtype, void* q, float* scale, void* q_t, float* scale_t, void* dh,
+                         void* stream);
+
+/*
+ * fp8_grouped_linear_fwd -- y = x W_e^T for the rows of every expert e, in one launch (block
+ * recipe): y[r, n] = bf16_rne(sum_kb sx[r, kb] sw[e, n/128, kb] sum over the block qx qw).
+ *
+ *   qx, sx       e4m3 [rows, K], float32 [rows, K/128].
+ *   qw           e4m3, expert e's [N, K] at qw + e stride_w, row stride ldw (bytes; both multiples
+ *                of 16, ldw >= K).
+ *   sw           float32, expert e's [N/128, K/128] at sw + e stride_sw, row stride ldsw (elements).
+ *   offsets      int32 [experts + 1], counts int32 [experts], of fp8_moe_sort (on the device):
+ *                expert e's rows are offsets[e] .. offsets[e] + counts[e]. Any rows may belong to
+ *                an expert; offsets have to rise. Values outside the tensors are clamped.
+ *   rows, N, K   rows >= 0 below 2^23; N, K positive multiples of 128 below 2^17; ldw below 2^23.
+ *   max_rows     a bound on an expert's rows that the host knows, such as the token count (each
+ *                token picks an expert once), else `rows`. It chooses the kernel, and only the speed
+ *                depends on it.
+ *   y            bf16 [rows, N] out; 0 in every row that is no expert's.
+ */
+int fp8_grouped_linear_fwd(const void* qx, const void* qw, int64_t ldw, int64_t stride_w,
+                           const float* sx, const float* sw, int64_t ldsw, int64_t stride_sw,
+                           const int32_t* offsets, const int32_t* counts, int32_t experts,
+                           int64_t rows, int64_t N, int64_t K, int64_t max_rows, void* y,
+                           void* stream);
+
+/*
+ * fp8_grouped_linear_dgrad -- dx = g W_e, the same product with the contraction over N: qg e4m3
+ * [rows, N], sg [rows, N/128]; expert e's transposed codes [K, N] at qw_t + e stride_w with row
+ * stride ldw, scales [K/128, N/128] at sw_t + e stride_sw with row stride ldsw (one quantization
+ * of the stacked weights [experts N, K] gives them with ldw = experts N, stride_w = N); dx bf16
+ * [rows, K].
+ */
+int fp8_grouped_linear_dgrad(const void* qg, const void* qw_t, int64_t ldw, int64_t stride_w,
+                             const float* sg, const float* sw_t, int64_t ldsw, int64_t stride_sw,
+                             const int32_t* offsets, const int32_t* counts, int32_t experts,
+                             int64_t rows, int64_t N, int64_t K, int64_t max_rows, void* dx,
+                             void* stream);
+
+/*
+ * fp8_grouped_linear_wgrad -- dw[e] = g^T x over expert e's rows, every expert's in one launch.
+ *   qg_t, sg_t   e4m3 [N, rows], float32 [N, rows/128]; qx_t, sx_t the same with K: the transposed
+ *                copies of quantizing g and x, whose codes in padding rows are 0.
+ *   offsets      multiples of 128 (fp8_moe_sort with multiple = 128), so that no block of 128 rows
+ *                has two experts'; rows a multiple of 128.
+ *   dw           bf16 [experts, N, K] out; 0 for an expert without rows.
+ */
+int fp8_grouped_linear_wgrad(const void* qg_t, const void* qx_t, const float* sg_t,
+                             const float* sx_t, const int32_t* offsets, const int32_t* counts,
+                             int32_t experts, int64_t rows, int64_t N, int64_t K, void* dw,
+                             void* stream);
+
 /* Message for the last error returned on the calling thread ("" if none). */
 const char* fp8_last_error(void);
 

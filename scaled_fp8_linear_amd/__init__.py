@@ -16,7 +16,10 @@ from ._abi import (FP8_A_E5M2, FP8_AMAX_ACCUMULATE, FP8_BLOCK_1x128, FP8_E5M2, F
                    FP8_DT_BF16, FP8_DT_F16, FP8_DT_F32, fp8_layernorm_fwd, fp8_layernorm_bwd,
                    fp8_layernorm_bwd_workspace, fp8_moe_rows, fp8_moe_sort,
                    fp8_moe_sort_workspace, fp8_moe_dispatch, fp8_moe_dispatch_bwd,
-                   fp8_moe_combine, fp8_moe_combine_bwd)
+                   fp8_moe_combine, fp8_moe_combine_bwd, FP8_ACT_RELU, FP8_ACT_SILU, FP8_ACT_GELU,
+                   fp8_moe_route, fp8_moe_route_bwd, fp8_moe_route_workspace, fp8_act_quantize,
+                   fp8_act_quantize_bwd, fp8_grouped_linear_fwd, fp8_grouped_linear_dgrad,
+                   fp8_grouped_linear_wgrad)
 from .autograd import Fp8Linear, fp8_autocast, fp8_state
 from .experts import (ExpertBlock, ExpertPlan, LayerNorm, expert_combine, expert_dispatch,
                       expert_plan, layer_norm)
@@ -35,5 +38,8 @@ __all__ = ["fp8_quantize_amax", "fp8_scale_update", "fp8_linear_fwd", "fp8_linea
            "fp8_layernorm_fwd", "fp8_layernorm_bwd", "fp8_layernorm_bwd_workspace",
            "fp8_moe_rows", "fp8_moe_sort", "fp8_moe_sort_workspace", "fp8_moe_dispatch",
            "fp8_moe_dispatch_bwd", "fp8_moe_combine", "fp8_moe_combine_bwd",
+           "FP8_ACT_RELU", "FP8_ACT_SILU", "FP8_ACT_GELU", "fp8_moe_route", "fp8_moe_route_bwd",
+           "fp8_moe_route_workspace", "fp8_act_quantize", "fp8_act_quantize_bwd",
+           "fp8_grouped_linear_fwd", "fp8_grouped_linear_dgrad", "fp8_grouped_linear_wgrad",
            "ExpertBlock", "ExpertPlan", "LayerNorm", "expert_combine", "expert_dispatch",
            "expert_plan", "layer_norm"]

@@ -30,9 +30,13 @@ EXPORTS = ("fp8_quantize_amax", "fp8_scale_update", "fp8_linear_fwd", "fp8_linea
            "fp8_unpad_varlen", "fp8_linear_fwd_current",
            "fp8_layernorm_fwd", "fp8_layernorm_bwd_workspace", "fp8_layernorm_bwd",
            "fp8_moe_rows", "fp8_moe_sort_workspace", "fp8_moe_sort", "fp8_moe_dispatch",
-           "fp8_moe_dispatch_bwd", "fp8_moe_combine", "fp8_moe_combine_bwd")
+           "fp8_moe_dispatch_bwd", "fp8_moe_combine", "fp8_moe_combine_bwd",
+           "fp8_moe_route_workspace", "fp8_moe_route", "fp8_moe_route_bwd", "fp8_act_quantize",
+           "fp8_act_quantize_bwd", "fp8_grouped_linear_fwd", "fp8_grouped_linear_dgrad",
+           "fp8_grouped_linear_wgrad")
 FP8_DT_BF16, FP8_DT_F16, FP8_DT_F32 = 0, 1, 2
 FP8_LAYOUT_THD, FP8_LAYOUT_BSHD = 0, 1
+FP8_ACT_RELU, FP8_ACT_SILU, FP8_ACT_GELU = 0, 1, 2
 
 
 class Fp8Error(RuntimeError):
@@ -86,6 +90,20 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.fp8_moe_combine.argtypes = [_vp, _i64, _vp, _vp, _i64, _i32, _i64, _i64, _int, _vp, _vp]
     lib.fp8_moe_combine_bwd.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i32, _i64,
                                         _i64, _int, _vp, _vp, _vp]
+    lib.fp8_moe_route_workspace.argtypes = [_i64, _i32, _p64]
+    lib.fp8_moe_route.argtypes = [_vp, _i64, _i64, _i64, _i32, _i32, _int, _int, _vp, _vp, _vp, _vp,
+                                  _vp, _vp, _i64, _vp]
+    lib.fp8_moe_route_bwd.argtypes = [_vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _i64, _i32,
+                                      _i32, _int, _int, _vp, _vp]
+    lib.fp8_act_quantize.argtypes = [_vp, _i64, _i64, _i64, _i64, _int, _int, _int, _vp, _vp, _vp,
+                                     _vp, _vp, _vp, _vp]
+    lib.fp8_act_quantize_bwd.argtypes = [_vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _int, _int,
+                                         _vp, _vp, _vp, _vp, _vp, _vp]
+    grouped = [_vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i32, _i64, _i64, _i64, _i64,
+               _vp, _vp]
+    lib.fp8_grouped_linear_fwd.argtypes = lib.fp8_grouped_linear_dgrad.argtypes = grouped
+    lib.fp8_grouped_linear_wgrad.argtypes = [_vp, _vp, _vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64,
+                                             _vp, _vp]
     for name in EXPORTS:
         if name not in ("fp8_last_error", "fp8_version"):
             getattr(lib, name).restype = _int
@@ -665,6 +683,89 @@ def fp8_moe_combine_bwd(dy, ys, slot, source, weights, dys=None, dw=None, stream
     """The combine's gradients (dys [rows, cols], dw float32 [tokens, topk]) from dy
     [tokens, cols] and ys; padding rows of dys and dropped pairs of dw are 0."""
     return _native().moe_combine_bwd(dy, ys, slot, source, weights, dys, dw, stream)
+
+
+# ------------------------------------------------- router, activation, experts' products
+_ACTS = {"relu": FP8_ACT_RELU, "silu": FP8_ACT_SILU, "gelu": FP8_ACT_GELU}
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError(f"act must be one of {tuple(_ACTS)}, not {act!r}")
+    return _ACTS[act]
+
+
+def fp8_moe_route_workspace(tokens, experts):
+    """Bytes of workspace of fp8_moe_route."""
+    out = _i64(0)
+    _check("fp8_moe_route_workspace", load().fp8_moe_route_workspace(int(tokens), int(experts),
+                                                                     ctypes.byref(out)))
+    return out.value
+
+
+def fp8_moe_route(logits, topk, tokens_valid=None, normalize=True, expert_idx=None, weights=None,
+                  lse=None, counts=None, losses=None, workspace=None, stream=None):
+    """The topk experts of each token of logits [tokens, experts] (bf16, f16 or f32; rows may be
+    strided), ties to the lower index, -inf never chosen. Returns (expert_idx int32 [tokens, topk]
+    with -1 for no expert, weights float32 [tokens, topk] (softmax over the choices, or without
+    ``normalize`` the probabilities as they are), lse float32 [tokens], counts int32 [experts],
+    losses float32 [2]: the balance loss and the z-loss). Tokens at or past ``tokens_valid`` are
+    padding and choose nothing."""
+    return _native().moe_route(logits, topk, tokens_valid, normalize, expert_idx, weights, lse,
+                               counts, losses, workspace, stream)
+
+
+def fp8_moe_route_bwd(logits, lse, expert_idx, weights, counts, dweights=None, dlosses=None,
+                      tokens_valid=None, normalize=True, dlogits=None, stream=None):
+    """dlogits [tokens, experts] in the logits' dtype from dweights (float32 [tokens, topk]) and
+    dlosses (float32 [2]), either None for 0, and what the forward gave."""
+    return _native().moe_route_bwd(logits, lse, expert_idx, weights, counts, dweights, dlosses,
+                                   tokens_valid, normalize, dlogits, stream)
+
+
+def fp8_act_quantize(h, act="silu", gated=True, rows_valid=None, q=None, scale=None, q_t=None,
+                     scale_t=None, hq=None, hscale=None, want_q=True, want_q_t=True,
+                     want_checkpoint=True, stream=None):
+    """a = act(h), or ``gated`` act(g) u of h = [g | u], quantized as it is made; ``act`` is "relu",
+    "silu" or "gelu" (with tanh). h [rows, cols] or [rows, 2 cols] (bf16, f16 or f32; rows may be
+    strided). Returns (q [rows, cols], scale [rows, cols/128], q_t [cols, rows], scale_t
+    [cols, rows/128], hq and hscale: h in 8 bits for fp8_act_quantize_bwd), None for those not
+    wanted and not passed."""
+    return _native().act_quantize(h, _act(act), gated, rows_valid, q, scale, q_t, scale_t, hq,
+                                  hscale, want_q, want_q_t, want_checkpoint, stream)
+
+
+def fp8_act_quantize_bwd(da, hq, hscale, act="silu", gated=True, rows_valid=None, q=None,
+                         scale=None, q_t=None, scale_t=None, dh=None, want_q=True, want_q_t=True,
+                         want_dh=False, stream=None):
+    """The gradient of the activation from da [rows, cols] and the 8-bit h. Returns (q [rows, w],
+    scale, q_t [w, rows], scale_t, dh [rows, w] in da's dtype) with w the width of h, None for
+    those not wanted and not passed."""
+    return _native().act_quantize_bwd(da, hq, hscale, _act(act), gated, rows_valid, q, scale, q_t,
+                                      scale_t, dh, want_q, want_q_t, want_dh, stream)
+
+
+def fp8_grouped_linear_fwd(qx, qw, sx, sw, offsets, counts, y=None, max_rows=None, stream=None):
+    """y [rows, N] bf16 = the experts' rows of qx [rows, K] times their qw[e]^T, qw [experts, N, K]
+    (any expert and row strides), by the block recipe: sx [rows, K/128], sw [experts, N/128, K/128].
+    offsets and counts of fp8_moe_sort; rows of no expert are 0. ``max_rows``: a bound on an
+    expert's rows, such as the token count, by which the kernel is chosen."""
+    return _native().grouped_linear(False, qx, qw, sx, sw, offsets, counts, y, max_rows, stream)
+
+
+def fp8_grouped_linear_dgrad(qg, qw_t, sg, sw_t, offsets, counts, dx=None, max_rows=None,
+                             stream=None):
+    """dx [rows, K] bf16 = the experts' rows of qg [rows, N] times their weights: qw_t
+    [experts, K, N] (any expert and row strides), sg [rows, N/128], sw_t [experts, K/128, N/128].
+    Other arguments as fp8_grouped_linear_fwd's."""
+    return _native().grouped_linear(True, qg, qw_t, sg, sw_t, offsets, counts, dx, max_rows, stream)
+
+
+def fp8_grouped_linear_wgrad(qg_t, qx_t, sg_t, sx_t, offsets, counts, dw=None, stream=None):
+    """dw [experts, N, K] bf16: each expert's g^T x from the transposed copies qg_t [N, rows] and
+    qx_t [K, rows] with scales [N, rows/128], [K, rows/128]. offsets of fp8_moe_sort with
+    ``multiple`` = 128."""
+    return _native().grouped_wgrad(qg_t, qx_t, sg_t, sx_t, offsets, counts, dw, stream)
 
 
 def fp8_last_error() -> str:

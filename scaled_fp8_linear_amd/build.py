@@ -22,7 +22,7 @@ ROOT = os.path.dirname(PKG)
 
 SOURCES = ["abi.cpp", "quantize_amax.hip", "quantize_block.hip", "scale_update.hip",
            "pad_tokens.hip", "pad_varlen.hip", "gemm_fp8.hip", "bias.hip", "linear_small.hip",
-           "layernorm.hip", "moe.hip"]
+           "layernorm.hip", "moe.hip", "moe_route.hip", "act_quantize.hip", "grouped.hip"]
 
 ARCH = "gfx950"
 FLAGS = [

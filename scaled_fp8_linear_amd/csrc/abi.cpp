@@ -674,4 +674,231 @@ int fp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ld
   return hip_status(fp8lin::launch_moe_combine_bwd(a, as_stream(stream)), fn);
 }
 
+namespace {
+
+int check_route(const char* fn, const void* logits, int64_t ldl, int64_t tokens, int64_t valid,
+                int32_t experts, int32_t topk, int dtype) {
+  if (int e = check_moe_sizes(fn, tokens, topk)) return e;
+  if (int e = check_experts(fn, experts)) return e;
+  if (topk > experts)
+    return fail(FP8_ERR_SHAPE, "%s: topk=%d of %d experts", fn, topk, experts);
+  if (valid < 0 || valid > tokens)
+    return fail(FP8_ERR_SHAPE, "%s: tokens_valid=%lld outside [0, %lld]", fn, (long long)valid,
+                (long long)tokens);
+  if (int e = check_dtype(fn, dtype)) return e;
+  return check_rows(fn, "logits", logits, ldl, tokens, experts, dtype);
+}
+
+// A pair of outputs (or inputs) of which both or none are given.
+int check_pair(const char* fn, const char* what, const void* codes, const float* scale,
+               int64_t n) {
+  if (n > 0 && (codes == nullptr) != (scale == nullptr))
+    return fail(FP8_ERR_NULL, "%s: %s and its scales must both be given or both be NULL", fn, what);
+  if (!aligned16(codes) || !aligned_to(scale, 4))
+    return fail(FP8_ERR_ALIGN, "%s: %s must be 16-byte aligned and its scales 4-byte", fn, what);
+  return FP8_OK;
+}
+
+constexpr int64_t kMaxGroupedRows = (int64_t)1 << 23;
+
+int check_act(const char* fn, int64_t rows, int64_t valid, int64_t cols, int act, int dtype) {
+  if (rows < 0 || cols < 1 || cols % 128)
+    return fail(FP8_ERR_SHAPE, "%s: needs rows >= 0 and cols a positive multiple of 128 (got %lld x "
+                "%lld)", fn, (long long)rows, (long long)cols);
+  if (rows >= kMaxGroupedRows || cols >= kMaxContraction)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: 2^23 rows or 2^17 columns or more", fn);
+  if (valid < 0 || valid > rows)
+    return fail(FP8_ERR_SHAPE, "%s: rows_valid=%lld outside [0, %lld]", fn, (long long)valid,
+                (long long)rows);
+  if (act != FP8_ACT_RELU && act != FP8_ACT_SILU && act != FP8_ACT_GELU)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: unknown activation %d", fn, act);
+  return check_dtype(fn, dtype);
+}
+
+int check_grouped(const char* fn, const int32_t* offsets, const int32_t* counts, int32_t experts,
+                  int64_t rows, int64_t N, int64_t K) {
+  if (int e = check_experts(fn, experts)) return e;
+  if (rows < 0 || N < 1 || K < 1 || N % 128 || K % 128)
+    return fail(FP8_ERR_SHAPE, "%s: needs rows >= 0 and N, K positive multiples of 128 (got %lld x "
+                "%lld x %lld)", fn, (long long)rows, (long long)N, (long long)K);
+  if (rows >= kMaxGroupedRows || N >= kMaxContraction || K >= kMaxContraction)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: 2^23 rows, or N or K of 2^17, or more", fn);
+  if (!offsets || !counts) return fail(FP8_ERR_NULL, "%s: offsets or counts is NULL", fn);
+  if (!aligned_to(offsets, 4) || !aligned_to(counts, 4))
+    return fail(FP8_ERR_ALIGN, "%s: offsets and counts must be 4-byte aligned", fn);
+  return FP8_OK;
+}
+
+// y [rows, N] over contraction length K.
+int grouped(const char* fn, const void* x, const void* w, int64_t ldw, int64_t stride_w,
+            const float* sx, const float* sw, int64_t ldsw, int64_t stride_sw,
+            const int32_t* offsets, const int32_t* counts, int32_t experts, int64_t rows,
+            int64_t N, int64_t K, int64_t max_rows, void* y, void* stream) {
+  if (int e = check_grouped(fn, offsets, counts, experts, rows, N, K)) return e;
+  if (ldw < K || ldw % 16 || stride_w < 0 || stride_w % 16)
+    return fail(FP8_ERR_SHAPE, "%s: weight strides %lld and %lld (rows of %lld codes, multiples of "
+                "16)", fn, (long long)stride_w, (long long)ldw, (long long)K);
+  if (ldsw < K / 128 || stride_sw < 0)
+    return fail(FP8_ERR_SHAPE, "%s: scale strides %lld and %lld (rows of %lld scales)", fn,
+                (long long)stride_sw, (long long)ldsw, (long long)(K / 128));
+  if (ldw >= kMaxGroupedRows || ldsw >= kMaxGroupedRows ||
+      stride_w > (INT64_MAX >> 10) || stride_sw > (INT64_MAX >> 12))
+    return fail(FP8_ERR_UNSUPPORTED, "%s: a row stride of 2^23 or more, or experts too far apart",
+                fn);
+  if (max_rows < 0) return fail(FP8_ERR_SHAPE, "%s: max_rows=%lld", fn, (long long)max_rows);
+  if (rows == 0) return ok();
+  if (!x || !w || !sx || !sw || !y) return fail(FP8_ERR_NULL, "%s: NULL operand or scale pointer", fn);
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned_to(sx, 4) || !aligned_to(sw, 4))
+    return fail(FP8_ERR_ALIGN, "%s: operands and output must be 16-byte aligned, scales 4-byte", fn);
+  fp8lin::GroupedArgs a{};
+  a.x = static_cast<const uint8_t*>(x), a.w = static_cast<const uint8_t*>(w), a.sx = sx, a.sw = sw;
+  a.ldw = ldw, a.stride_w = stride_w, a.ldsw = ldsw, a.stride_sw = stride_sw;
+  a.offsets = offsets, a.counts = counts, a.experts = experts, a.rows = rows, a.N = N, a.K = K;
+  a.max_rows = max_rows < rows ? max_rows : rows;
+  a.y = static_cast<uint16_t*>(y);
+  return hip_status(fp8lin::launch_grouped_gemm(a, as_stream(stream)), fn);
+}
+
+}  // namespace
+
+int fp8_moe_route_workspace(int64_t tokens, int32_t experts, int64_t* bytes) {
+  const char* fn = "fp8_moe_route_workspace";
+  if (!bytes) return fail(FP8_ERR_NULL, "%s: bytes is NULL", fn);
+  if (int e = check_moe_sizes(fn, tokens, 1)) return e;
+  if (int e = check_experts(fn, experts)) return e;
+  *bytes = fp8lin::moe_route_workspace(tokens, experts);
+  return ok();
+}
+
+int fp8_moe_route(const void* logits, int64_t ldl, int64_t tokens, int64_t tokens_valid,
+                  int32_t experts, int32_t topk, int dtype, int normalize, int32_t* expert_idx,
+                  float* weights, float* lse, int32_t* counts, float* losses, void* workspace,
+                  int64_t workspace_bytes, void* stream) {
+  const char* fn = "fp8_moe_route";
+  if (int e = check_route(fn, logits, ldl, tokens, tokens_valid, experts, topk, dtype)) return e;
+  if (int e = check_out(fn, "expert_idx", expert_idx, tokens, 4)) return e;
+  if (int e = check_out(fn, "weights", weights, tokens, 4)) return e;
+  if (int e = check_out(fn, "lse", lse, tokens, 4)) return e;
+  if (int e = check_out(fn, "counts", counts, 1, 4)) return e;
+  if (int e = check_out(fn, "losses", losses, 1, 4)) return e;
+  const int64_t need = fp8lin::moe_route_workspace(tokens, experts);
+  if (int e = check_workspace(fn, workspace, workspace_bytes, need)) return e;
+  fp8lin::MoeRouteArgs a{};
+  a.logits = logits, a.ldl = ldl, a.tokens = tokens, a.valid = tokens_valid, a.experts = experts;
+  a.topk = topk, a.dtype = dtype, a.normalize = normalize != 0, a.idx = expert_idx;
+  a.weights = weights, a.lse = lse, a.counts = counts, a.losses = losses;
+  a.workspace = need ? static_cast<float*>(workspace) : nullptr;
+  return hip_status(fp8lin::launch_moe_route(a, as_stream(stream)), fn);
+}
+
+int fp8_moe_route_bwd(const void* logits, int64_t ldl, const float* lse, const int32_t* expert_idx,
+                      const float* weights, const int32_t* counts, const float* dweights,
+                      const float* dlosses, int64_t tokens, int64_t tokens_valid, int32_t experts,
+                      int32_t topk, int dtype, int normalize, void* dlogits, void* stream) {
+  const char* fn = "fp8_moe_route_bwd";
+  if (int e = check_route(fn, logits, ldl, tokens, tokens_valid, experts, topk, dtype)) return e;
+  if (int e = check_out(fn, "lse", lse, tokens, 4)) return e;
+  if (int e = check_out(fn, "expert_idx", expert_idx, tokens, 4)) return e;
+  if (int e = check_out(fn, "weights", weights, tokens, 4)) return e;
+  if (int e = check_out(fn, "counts", counts, 1, 4)) return e;
+  if (!aligned_to(dweights, 4) || !aligned_to(dlosses, 4))
+    return fail(FP8_ERR_ALIGN, "%s: dweights and dlosses must be 4-byte aligned", fn);
+  if (int e = check_out(fn, "dlogits", dlogits, tokens, elem_bytes(dtype))) return e;
+  if (tokens == 0) return ok();
+  if (logits == dlogits) return fail(FP8_ERR_UNSUPPORTED, "%s: dlogits must not be logits", fn);
+  fp8lin::MoeRouteArgs a{};
+  a.logits = logits, a.ldl = ldl, a.tokens = tokens, a.valid = tokens_valid, a.experts = experts;
+  a.topk = topk, a.dtype = dtype, a.normalize = normalize != 0;
+  a.idx = const_cast<int32_t*>(expert_idx), a.weights = const_cast<float*>(weights);
+  a.lse = const_cast<float*>(lse), a.counts = const_cast<int32_t*>(counts);
+  a.dweights = dweights, a.dlosses = dlosses, a.dlogits = dlogits;
+  return hip_status(fp8lin::launch_moe_route_bwd(a, as_stream(stream)), fn);
+}
+
+int fp8_act_quantize(const void* h, int64_t ldh, int64_t rows, int64_t rows_valid, int64_t cols,
+                     int act, int gated, int dtype, void* q, float* scale, void* q_t,
+                     float* scale_t, void* hq, float* hscale, void* stream) {
+  const char* fn = "fp8_act_quantize";
+  if (int e = check_act(fn, rows, rows_valid, cols, act, dtype)) return e;
+  if (int e = check_rows(fn, "h", h, ldh, rows_valid, gated ? 2 * cols : cols, dtype)) return e;
+  if (int e = check_pair(fn, "q", q, scale, rows)) return e;
+  if (int e = check_pair(fn, "q_t", q_t, scale_t, rows)) return e;
+  if (int e = check_pair(fn, "hq", hq, hscale, rows)) return e;
+  if (q_t && rows % 128)
+    return fail(FP8_ERR_SHAPE, "%s: q_t needs rows %% 128 == 0 (got %lld)", fn, (long long)rows);
+  if (rows == 0 || (!q && !q_t && !hq)) return ok();
+  fp8lin::ActArgs a{};
+  a.x = h, a.ldx = ldh, a.rows = rows, a.valid = rows_valid, a.cols = cols, a.act = act;
+  a.gated = gated != 0, a.dtype = dtype, a.q = static_cast<uint8_t*>(q), a.scale = scale;
+  a.q_t = static_cast<uint8_t*>(q_t), a.scale_t = scale_t, a.hq = static_cast<uint8_t*>(hq);
+  a.hscale = hscale;
+  return hip_status(fp8lin::launch_act_quantize(a, as_stream(stream)), fn);
+}
+
+int fp8_act_quantize_bwd(const void* da, int64_t ldda, const void* hq, const float* hscale,
+                         int64_t rows, int64_t rows_valid, int64_t cols, int act, int gated,
+                         int dtype, void* q, float* scale, void* q_t, float* scale_t, void* dh,
+                         void* stream) {
+  const char* fn = "fp8_act_quantize_bwd";
+  if (int e = check_act(fn, rows, rows_valid, cols, act, dtype)) return e;
+  if (int e = check_rows(fn, "da", da, ldda, rows_valid, cols, dtype)) return e;
+  if (rows_valid > 0 && (!hq || !hscale)) return fail(FP8_ERR_NULL, "%s: hq or hscale is NULL", fn);
+  if (int e = check_pair(fn, "hq", hq, hscale, rows_valid)) return e;
+  if (int e = check_pair(fn, "q", q, scale, rows)) return e;
+  if (int e = check_pair(fn, "q_t", q_t, scale_t, rows)) return e;
+  if (!aligned_to(dh, elem_bytes(dtype)))
+    return fail(FP8_ERR_ALIGN, "%s: dh is not aligned to its elements", fn);
+  if (q_t && rows % 128)
+    return fail(FP8_ERR_SHAPE, "%s: q_t needs rows %% 128 == 0 (got %lld)", fn, (long long)rows);
+  if ((q && q == hq) || (dh && dh == da))
+    return fail(FP8_ERR_UNSUPPORTED, "%s: outputs must not be inputs", fn);
+  if (rows == 0 || (!q && !q_t && !dh)) return ok();
+  fp8lin::ActArgs a{};
+  a.x = da, a.ldx = ldda, a.rows = rows, a.valid = rows_valid, a.cols = cols, a.act = act;
+  a.gated = gated != 0, a.dtype = dtype, a.q = static_cast<uint8_t*>(q), a.scale = scale;
+  a.q_t = static_cast<uint8_t*>(q_t), a.scale_t = scale_t;
+  a.hq = static_cast<uint8_t*>(const_cast<void*>(hq)), a.hscale = const_cast<float*>(hscale);
+  a.dh = dh;
+  return hip_status(fp8lin::launch_act_quantize_bwd(a, as_stream(stream)), fn);
+}
+
+int fp8_grouped_linear_fwd(const void* qx, const void* qw, int64_t ldw, int64_t stride_w,
+                           const float* sx, const float* sw, int64_t ldsw, int64_t stride_sw,
+                           const int32_t* offsets, const int32_t* counts, int32_t experts,
+                           int64_t rows, int64_t N, int64_t K, int64_t max_rows, void* y,
+                           void* stream) {
+  return grouped("fp8_grouped_linear_fwd", qx, qw, ldw, stride_w, sx, sw, ldsw, stride_sw, offsets,
+                 counts, experts, rows, N, K, max_rows, y, stream);
+}
+
+int fp8_grouped_linear_dgrad(const void* qg, const void* qw_t, int64_t ldw, int64_t stride_w,
+                             const float* sg, const float* sw_t, int64_t ldsw, int64_t stride_sw,
+                             const int32_t* offsets, const int32_t* counts, int32_t experts,
+                             int64_t rows, int64_t N, int64_t K, int64_t max_rows, void* dx,
+                             void* stream) {
+  return grouped("fp8_grouped_linear_dgrad", qg, qw_t, ldw, stride_w, sg, sw_t, ldsw, stride_sw,
+                 offsets, counts, experts, rows, K, N, max_rows, dx, stream);
+}
+
+int fp8_grouped_linear_wgrad(const void* qg_t, const void* qx_t, const float* sg_t,
+                             const float* sx_t, const int32_t* offsets, const int32_t* counts,
+                             int32_t experts, int64_t rows, int64_t N, int64_t K, void* dw,
+                             void* stream) {
+  const char* fn = "fp8_grouped_linear_wgrad";
+  if (int e = check_grouped(fn, offsets, counts, experts, rows, N, K)) return e;
+  if (rows % 128)
+    return fail(FP8_ERR_SHAPE, "%s: rows=%lld not a multiple of 128", fn, (long long)rows);
+  if (!dw) return fail(FP8_ERR_NULL, "%s: dw is NULL", fn);
+  if (rows > 0 && (!qg_t || !qx_t || !sg_t || !sx_t))
+    return fail(FP8_ERR_NULL, "%s: NULL operand or scale pointer", fn);
+  if (!aligned16(qg_t) || !aligned16(qx_t) || !aligned16(dw) || !aligned_to(sg_t, 4) ||
+      !aligned_to(sx_t, 4))
+    return fail(FP8_ERR_ALIGN, "%s: operands and output must be 16-byte aligned, scales 4-byte", fn);
+  fp8lin::GroupedArgs a{};
+  a.w = static_cast<const uint8_t*>(qg_t), a.x = static_cast<const uint8_t*>(qx_t);
+  a.sw = sg_t, a.sx = sx_t, a.offsets = offsets, a.counts = counts, a.experts = experts;
+  a.rows = rows, a.N = N, a.K = K, a.y = static_cast<uint16_t*>(dw);
+  return hip_status(fp8lin::launch_grouped_wgrad(a, as_stream(stream)), fn);
+}
+
 }  // extern "C"

@@ -1,4 +1,5 @@
-// CPython binding of the row operators (layer norm, expert exchange): the checks of tensors,
+// CPython binding of the row operators (layer norm, router, expert exchange, activation) and of the
+// experts' products: the checks of tensors,
 // their addresses, and the call of the C entry point, in one native call. For one token the
 // kernels take 3 us and their launch 2.7 us of host time; the same checks in Python took 3.4
 // us more. Entry points come in as addresses (bind), so the library is loaded once, elsewhere.
@@ -34,6 +35,14 @@ struct Entries {
   decltype(&fp8_moe_dispatch_bwd) moe_dispatch_bwd;
   decltype(&fp8_moe_combine) moe_combine;
   decltype(&fp8_moe_combine_bwd) moe_combine_bwd;
+  decltype(&fp8_moe_route_workspace) moe_route_workspace;
+  decltype(&fp8_moe_route) moe_route;
+  decltype(&fp8_moe_route_bwd) moe_route_bwd;
+  decltype(&fp8_act_quantize) act_quantize;
+  decltype(&fp8_act_quantize_bwd) act_quantize_bwd;
+  decltype(&fp8_grouped_linear_fwd) grouped_linear_fwd;
+  decltype(&fp8_grouped_linear_dgrad) grouped_linear_dgrad;
+  decltype(&fp8_grouped_linear_wgrad) grouped_linear_wgrad;
 } entry;
 // new(shape, dtype, device, stream); check(name, status); current_device(); raw_stream(device)
 PyObject *py_new, *py_check, *py_device, *py_raw_stream;
@@ -453,6 +462,269 @@ PyObject* moe_combine_bwd(PyObject* const* p) {
   return tuple({&dys, &dw});
 }
 
+// ------------------------------------------------------------------------- the router
+
+// A count of valid rows: all of them for None.
+int64_t valid_rows(PyObject* o, int64_t rows, const char* name) {
+  const int64_t v = o == Py_None ? rows : to_long(o);
+  if (v < 0 || v > rows)
+    bad(std::string(name) + "=" + str(v) + " outside [0, " + str(rows) + "]");
+  return v;
+}
+
+// logits, topk, tokens_valid, normalize, expert_idx, weights, lse, counts, losses, workspace, stream
+PyObject* moe_route(PyObject* const* p) {
+  const Arg x(p[0], "logits");
+  const int64_t ld = row_stride(x), tokens = x.t->size(0), experts = x.t->size(1);
+  const auto dev = x.t->device();
+  const auto dt = x.t->scalar_type();
+  const int32_t topk = to_i32(p[1], "topk");
+  if (topk < 1) bad("topk=" + str(topk) + " must be positive");
+  const int64_t valid = valid_rows(p[2], tokens, "tokens_valid");
+  const bool normalize = to_bool(p[3]);
+  if (experts > INT32_MAX) bad("logits: too many experts");
+  fits(Arg(p[4], "expert_idx"), {tokens, topk}, {at::kInt}, dev);
+  fits(Arg(p[5], "weights"), {tokens, topk}, {at::kFloat}, dev);
+  fits(Arg(p[6], "lse"), {tokens}, {at::kFloat}, dev);
+  fits(Arg(p[7], "counts"), {experts}, {at::kInt}, dev);
+  fits(Arg(p[8], "losses"), {2}, {at::kFloat}, dev);
+  PyObject* const stream = p[10];
+  void* s = launch_stream(*x.t, stream);
+  int64_t bytes = 0;
+  check("fp8_moe_route_workspace", entry.moe_route_workspace(tokens, (int32_t)experts, &bytes));
+  Out idx(p[4]), weights(p[5]), lse(p[6]), counts(p[7]), losses(p[8]), ws(p[9]);
+  idx.make({tokens, topk}, at::kInt, *x.t, stream);
+  weights.make({tokens, topk}, at::kFloat, *x.t, stream);
+  lse.make({tokens}, at::kFloat, *x.t, stream);
+  counts.make({experts}, at::kInt, *x.t, stream);
+  losses.make({2}, at::kFloat, *x.t, stream);
+  bytes = workspace(ws, bytes, *x.t, stream);
+  check("fp8_moe_route",
+        entry.moe_route(x.ptr(), ld, tokens, valid, (int32_t)experts, topk, dt_code(dt), normalize,
+                        static_cast<int32_t*>(idx.ptr), static_cast<float*>(weights.ptr),
+                        static_cast<float*>(lse.ptr), static_cast<int32_t*>(counts.ptr),
+                        static_cast<float*>(losses.ptr), ws.ptr, bytes, s));
+  return tuple({&idx, &weights, &lse, &counts, &losses});
+}
+
+// logits, lse, expert_idx, weights, counts, dweights, dlosses, tokens_valid, normalize, dlogits,
+// stream
+PyObject* moe_route_bwd(PyObject* const* p) {
+  const Arg x(p[0], "logits"), lse(p[1], "lse"), idx(p[2], "expert_idx"), w(p[3], "weights");
+  const Arg counts(p[4], "counts"), dw(p[5], "dweights"), dl(p[6], "dlosses");
+  const int64_t ld = row_stride(x), tokens = x.t->size(0), experts = x.t->size(1);
+  const auto dev = x.t->device();
+  const auto dt = x.t->scalar_type();
+  if (idx.need().dim() != 2)
+    bad("expert_idx must be 2-D [tokens, topk], got " + str(idx.t->sizes()));
+  const int64_t topk = idx.t->size(1);
+  if (topk > INT32_MAX || experts > INT32_MAX) bad("expert_idx: too many choices");
+  lse.need(), w.need(), counts.need();
+  fits(idx, {tokens, topk}, {at::kInt}, dev);
+  fits(lse, {tokens}, {at::kFloat}, dev);
+  fits(w, {tokens, topk}, {at::kFloat}, dev);
+  fits(counts, {experts}, {at::kInt}, dev);
+  fits(dw, {tokens, topk}, {at::kFloat}, dev);
+  fits(dl, {2}, {at::kFloat}, dev);
+  const int64_t valid = valid_rows(p[7], tokens, "tokens_valid");
+  const bool normalize = to_bool(p[8]);
+  fits(Arg(p[9], "dlogits"), {tokens, experts}, {dt}, dev);
+  void* s = launch_stream(*x.t, p[10]);
+  Out out(p[9]);
+  out.make({tokens, experts}, dt, *x.t, p[10]);
+  check("fp8_moe_route_bwd",
+        entry.moe_route_bwd(x.ptr(), ld, static_cast<float*>(lse.ptr()),
+                            static_cast<int32_t*>(idx.ptr()), static_cast<float*>(w.ptr()),
+                            static_cast<int32_t*>(counts.ptr()), static_cast<float*>(dw.ptr()),
+                            static_cast<float*>(dl.ptr()), tokens, valid, (int32_t)experts,
+                            (int32_t)topk, dt_code(dt), normalize, out.ptr, s));
+  return out.take();
+}
+
+// ------------------------------------------------------------------------- activation
+
+constexpr int64_t kTile = 128;               // codes per scale
+constexpr std::initializer_list<at::ScalarType> kCodes = {at::kByte, at::kFloat8_e4m3fn};
+
+// Codes [r, c] and their scales [r, c / 128], of which both or none are given.
+void fits_pair(const Arg& q, const Arg& scale, int64_t r, int64_t c, at::Device dev) {
+  if (bool(q) != bool(scale))
+    bad(std::string(q.name) + " and " + scale.name + " must both be given or both be None");
+  fits(q, {r, c}, kCodes, dev);
+  fits(scale, {r, c / kTile}, {at::kFloat}, dev);
+}
+struct OutPair {
+  Out q, scale;
+  OutPair(PyObject* a, PyObject* b) : q(a), scale(b) {}
+  void make(int64_t r, int64_t c, const at::Tensor& like, PyObject* stream, bool wanted) {
+    q.make({r, c}, at::kByte, like, stream, wanted);
+    scale.make({r, c / kTile}, at::kFloat, like, stream, wanted);
+  }
+  float* scales() const { return static_cast<float*>(scale.ptr); }
+};
+
+// h, act, gated, rows_valid, q, scale, q_t, scale_t, hq, hscale, want_q, want_q_t,
+// want_checkpoint, stream
+PyObject* act_quantize(PyObject* const* p) {
+  const Arg h(p[0], "h");
+  const int64_t ld = row_stride(h), rows = h.t->size(0), width = h.t->size(1);
+  const auto dev = h.t->device();
+  const int32_t act = to_i32(p[1], "act");
+  const bool gated = to_bool(p[2]);
+  if (gated && width % 2) bad("h [rows, 2 cols] has an odd width " + str(width));
+  const int64_t cols = gated ? width / 2 : width;
+  if (cols < 1 || cols % kTile) bad("h: cols=" + str(cols) + " must be a positive multiple of 128");
+  const int64_t valid = valid_rows(p[3], rows, "rows_valid");
+  const bool want_q = to_bool(p[10]), want_t = to_bool(p[11]), want_h = to_bool(p[12]);
+  fits_pair(Arg(p[4], "q"), Arg(p[5], "scale"), rows, cols, dev);
+  fits_pair(Arg(p[6], "q_t"), Arg(p[7], "scale_t"), cols, rows, dev);
+  fits_pair(Arg(p[8], "hq"), Arg(p[9], "hscale"), rows, width, dev);
+  if ((want_t || p[6] != Py_None) && rows % kTile)
+    bad("q_t needs rows to be a multiple of 128, got " + str(rows));
+  void* s = launch_stream(*h.t, p[13]);
+  OutPair q(p[4], p[5]), t(p[6], p[7]), c(p[8], p[9]);
+  q.make(rows, cols, *h.t, p[13], want_q);
+  t.make(cols, rows, *h.t, p[13], want_t);
+  c.make(rows, width, *h.t, p[13], want_h);
+  check("fp8_act_quantize",
+        entry.act_quantize(h.ptr(), ld, rows, valid, cols, act, gated,
+                           dt_code(h.t->scalar_type()), q.q.ptr, q.scales(), t.q.ptr, t.scales(),
+                           c.q.ptr, c.scales(), s));
+  return tuple({&q.q, &q.scale, &t.q, &t.scale, &c.q, &c.scale});
+}
+
+// da, hq, hscale, act, gated, rows_valid, q, scale, q_t, scale_t, dh, want_q, want_q_t, want_dh,
+// stream
+PyObject* act_quantize_bwd(PyObject* const* p) {
+  const Arg da(p[0], "da"), hq(p[1], "hq"), hscale(p[2], "hscale");
+  const int64_t ld = row_stride(da), rows = da.t->size(0), cols = da.t->size(1);
+  const auto dev = da.t->device();
+  const auto dt = da.t->scalar_type();
+  const int32_t act = to_i32(p[3], "act");
+  const bool gated = to_bool(p[4]);
+  if (cols < 1 || cols % kTile) bad("da: cols=" + str(cols) + " must be a positive multiple of 128");
+  const int64_t width = gated ? 2 * cols : cols;
+  const int64_t valid = valid_rows(p[5], rows, "rows_valid");
+  hq.need(), hscale.need();
+  fits_pair(hq, hscale, rows, width, dev);
+  fits_pair(Arg(p[6], "q"), Arg(p[7], "scale"), rows, width, dev);
+  fits_pair(Arg(p[8], "q_t"), Arg(p[9], "scale_t"), width, rows, dev);
+  fits(Arg(p[10], "dh"), {rows, width}, {dt}, dev);
+  const bool want_q = to_bool(p[11]), want_t = to_bool(p[12]), want_dh = to_bool(p[13]);
+  if ((want_t || p[8] != Py_None) && rows % kTile)
+    bad("q_t needs rows to be a multiple of 128, got " + str(rows));
+  void* s = launch_stream(*da.t, p[14]);
+  OutPair q(p[6], p[7]), t(p[8], p[9]);
+  Out dh(p[10]);
+  q.make(rows, width, *da.t, p[14], want_q);
+  t.make(width, rows, *da.t, p[14], want_t);
+  dh.make({rows, width}, dt, *da.t, p[14], want_dh);
+  check("fp8_act_quantize_bwd",
+        entry.act_quantize_bwd(da.ptr(), ld, hq.ptr(), static_cast<float*>(hscale.ptr()), rows,
+                               valid, cols, act, gated, dt_code(dt), q.q.ptr, q.scales(), t.q.ptr,
+                               t.scales(), dh.ptr, s));
+  return tuple({&q.q, &q.scale, &t.q, &t.scale, &dh});
+}
+
+// ------------------------------------------------------------------------- experts' products
+
+// Rows of codes and their scales, dense: [rows, cols], cols a positive multiple of 128.
+void code_rows(const Arg& q, const Arg& scale, int64_t& rows, int64_t& cols) {
+  if (q.need().dim() != 2)
+    bad(std::string(q.name) + " must be 2-D [rows, cols], got " + str(q.t->sizes()));
+  scale.need();
+  rows = q.t->size(0), cols = q.t->size(1);
+  fits_pair(q, scale, rows, cols, q.t->device());
+}
+
+// The experts' matrices [experts, r, c], each with contiguous rows; any expert and row strides.
+void stacked(const Arg& a, int64_t e, int64_t r, int64_t c, std::initializer_list<at::ScalarType> types,
+             at::Device dev, int64_t& ld, int64_t& stride) {
+  const at::Tensor& t = a.need();
+  const std::string n = a.name;
+  bool type_ok = false;
+  for (auto d : types) type_ok |= t.scalar_type() == d;
+  if (!type_ok) bad(n + " has dtype " + str(t.scalar_type()) + ", expected " + one_of(types));
+  if (t.sizes() != at::IntArrayRef({e, r, c}))
+    bad(n + " has shape " + str(t.sizes()) + ", expected " + str(at::IntArrayRef({e, r, c})));
+  if (t.device() != dev) bad(n + " is on " + str(t.device()) + ", the operands on " + str(dev));
+  if (c > 1 && t.stride(2) != 1) bad(n + ": its rows must be contiguous, stride " + str(t.stride(2)));
+  ld = r > 1 ? t.stride(1) : c;
+  stride = e > 1 ? t.stride(0) : 0;
+  if (ld < c) bad(n + ": rows overlap (stride " + str(ld) + ", " + str(c) + " columns)");
+}
+
+struct Groups {
+  Arg offsets, counts;
+  int64_t experts;
+  Groups(PyObject* o, PyObject* c, at::Device dev) : offsets(o, "offsets"), counts(c, "counts") {
+    if (counts.need().dim() != 1) bad("counts must be 1-D [experts], got " + str(counts.t->sizes()));
+    experts = counts.t->size(0);
+    if (experts > INT32_MAX - 1) bad("counts: too many experts");
+    fits(counts, {experts}, {at::kInt}, dev);
+    offsets.need();
+    fits(offsets, {experts + 1}, {at::kInt}, dev);
+  }
+  const int32_t* off() const { return static_cast<const int32_t*>(offsets.ptr()); }
+  const int32_t* cnt() const { return static_cast<const int32_t*>(counts.ptr()); }
+};
+
+// dgrad, x, w, sx, sw, offsets, counts, y, max_rows, stream
+PyObject* grouped_linear(PyObject* const* p) {
+  const bool dgrad = to_bool(p[0]);
+  const Arg x(p[1], dgrad ? "qg" : "qx"), w(p[2], dgrad ? "qw_t" : "qw");
+  const Arg sx(p[3], dgrad ? "sg" : "sx"), sw(p[4], dgrad ? "sw_t" : "sw");
+  int64_t rows, in, ldw, stride_w, ldsw, stride_sw;
+  code_rows(x, sx, rows, in);
+  const auto dev = x.t->device();
+  const Groups g(p[5], p[6], dev);
+  if (w.need().dim() != 3)
+    bad(std::string(w.name) + " must be 3-D [experts, out, in], got " + str(w.t->sizes()));
+  const int64_t out = w.t->size(1);
+  stacked(w, g.experts, out, in, kCodes, dev, ldw, stride_w);
+  stacked(sw, g.experts, out / kTile, in / kTile, {at::kFloat}, dev, ldsw, stride_sw);
+  fits(Arg(p[7], dgrad ? "dx" : "y"), {rows, out}, {at::kBFloat16}, dev);
+  const int64_t most = p[8] == Py_None ? rows : to_long(p[8]);
+  if (most < 0) bad("max_rows=" + str(most) + " is negative");
+  void* s = launch_stream(*x.t, p[9]);
+  Out y(p[7]);
+  y.make({rows, out}, at::kBFloat16, *x.t, p[9]);
+  const float *fx = static_cast<float*>(sx.ptr()), *fw = static_cast<float*>(sw.ptr());
+  if (dgrad)
+    check("fp8_grouped_linear_dgrad",
+          entry.grouped_linear_dgrad(x.ptr(), w.ptr(), ldw, stride_w, fx, fw, ldsw, stride_sw,
+                                     g.off(), g.cnt(), (int32_t)g.experts, rows, in, out, most,
+                                     y.ptr, s));
+  else
+    check("fp8_grouped_linear_fwd",
+          entry.grouped_linear_fwd(x.ptr(), w.ptr(), ldw, stride_w, fx, fw, ldsw, stride_sw,
+                                   g.off(), g.cnt(), (int32_t)g.experts, rows, out, in, most, y.ptr,
+                                   s));
+  return y.take();
+}
+
+// qg_t, qx_t, sg_t, sx_t, offsets, counts, dw, stream
+PyObject* grouped_wgrad(PyObject* const* p) {
+  const Arg g(p[0], "qg_t"), x(p[1], "qx_t"), sg(p[2], "sg_t"), sx(p[3], "sx_t");
+  int64_t n, k, rows, rows_x;
+  code_rows(g, sg, n, rows);
+  code_rows(x, sx, k, rows_x);
+  const auto dev = g.t->device();
+  if (rows_x != rows)
+    bad("qg_t has " + str(rows) + " rows of tokens, qx_t " + str(rows_x));
+  if (x.t->device() != dev) bad("qx_t is on " + str(x.t->device()) + ", qg_t on " + str(dev));
+  const Groups e(p[4], p[5], dev);
+  fits(Arg(p[6], "dw"), {e.experts, n, k}, {at::kBFloat16}, dev);
+  void* s = launch_stream(*g.t, p[7]);
+  Out dw(p[6]);
+  dw.make({e.experts, n, k}, at::kBFloat16, *g.t, p[7]);
+  check("fp8_grouped_linear_wgrad",
+        entry.grouped_linear_wgrad(g.ptr(), x.ptr(), static_cast<float*>(sg.ptr()),
+                                   static_cast<float*>(sx.ptr()), e.off(), e.cnt(),
+                                   (int32_t)e.experts, rows, n, k, dw.ptr, s));
+  return dw.take();
+}
+
 // ------------------------------------------------------------------------- the module
 
 template <PyObject* (*F)(PyObject* const*), int NARGS>
@@ -490,6 +762,14 @@ PyObject* bind(PyObject* const* p) {
   take("fp8_moe_dispatch_bwd", entry.moe_dispatch_bwd);
   take("fp8_moe_combine", entry.moe_combine);
   take("fp8_moe_combine_bwd", entry.moe_combine_bwd);
+  take("fp8_moe_route_workspace", entry.moe_route_workspace);
+  take("fp8_moe_route", entry.moe_route);
+  take("fp8_moe_route_bwd", entry.moe_route_bwd);
+  take("fp8_act_quantize", entry.act_quantize);
+  take("fp8_act_quantize_bwd", entry.act_quantize_bwd);
+  take("fp8_grouped_linear_fwd", entry.grouped_linear_fwd);
+  take("fp8_grouped_linear_dgrad", entry.grouped_linear_dgrad);
+  take("fp8_grouped_linear_wgrad", entry.grouped_linear_wgrad);
   PyObject** const held[] = {&py_new, &py_check, &py_device, &py_raw_stream};
   for (int i = 0; i < 4; ++i) {
     PyObject* old = *held[i];
@@ -506,6 +786,9 @@ PyMethodDef methods[] = {FP8LIN_FN(bind, 5),          FP8LIN_FN(layernorm_fwd, 9
                          FP8LIN_FN(layernorm_bwd, 14), FP8LIN_FN(moe_sort, 9),
                          FP8LIN_FN(moe_dispatch, 5),   FP8LIN_FN(moe_dispatch_bwd, 4),
                          FP8LIN_FN(moe_combine, 5),    FP8LIN_FN(moe_combine_bwd, 8),
+                         FP8LIN_FN(moe_route, 11),     FP8LIN_FN(moe_route_bwd, 11),
+                         FP8LIN_FN(act_quantize, 14),  FP8LIN_FN(act_quantize_bwd, 15),
+                         FP8LIN_FN(grouped_linear, 10), FP8LIN_FN(grouped_wgrad, 8),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods,
                       nullptr, nullptr, nullptr, nullptr};

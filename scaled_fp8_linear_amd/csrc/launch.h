@@ -113,4 +113,58 @@ hipError_t launch_moe_dispatch(const MoeArgs& a, hipStream_t s);      // x -> ou
 hipError_t launch_moe_combine(const MoeArgs& a, hipStream_t s);       // ys -> out [tokens, cols]
 hipError_t launch_moe_combine_bwd(const MoeArgs& a, hipStream_t s);   // x = dy -> out, dw
 
+// Router: logits [tokens, experts] of `dtype`, rows >= valid are padding. Forward: idx, weights,
+// lse, counts, losses out; workspace of moe_route_workspace() bytes (null if that is 0).
+// Backward: dlogits out (dense), dweights and dlosses may be null.
+struct MoeRouteArgs {
+  const void* logits;
+  int64_t ldl, tokens, valid;
+  int32_t experts, topk;
+  int dtype;
+  bool normalize;
+  int32_t* idx;
+  float *weights, *lse;
+  int32_t* counts;
+  float *losses, *workspace;
+  const float *dweights, *dlosses;
+  void* dlogits;
+};
+int64_t moe_route_workspace(int64_t tokens, int32_t experts);
+hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s);
+hipError_t launch_moe_route_bwd(const MoeRouteArgs& a, hipStream_t s);
+
+// Activation and its quantized copies. act: 0 relu, 1 silu, 2 gelu (tanh); gated: h = [g | u] of
+// 2 cols columns, a = act(g) u. rows >= valid are padding (read as zeros). q, q_t, hq (with their
+// scales) may each be null. Backward: x = da [rows, cols], hq and hscale in; q, q_t and dh (all
+// of h's width) out, each may be null.
+struct ActArgs {
+  const void* x;
+  int64_t ldx, rows, valid, cols;
+  int act, dtype;
+  bool gated;
+  uint8_t *q, *q_t, *hq;
+  float *scale, *scale_t, *hscale;
+  void* dh;
+};
+hipError_t launch_act_quantize(const ActArgs& a, hipStream_t s);
+hipError_t launch_act_quantize_bwd(const ActArgs& a, hipStream_t s);
+
+// Products of experts' rows. x codes [rows, K] with scales [rows, K/128]; expert e's weight codes
+// at w + e stride_w, [N, K] with row stride ldw, scales at sw + e stride_sw, [N/128, K/128] with
+// row stride ldsw; y bf16 [rows, N]: expert e's rows are offsets[e] .. offsets[e] + counts[e],
+// all others are 0.
+struct GroupedArgs {
+  const uint8_t *x, *w;
+  const float *sx, *sw;
+  int64_t ldw, stride_w, ldsw, stride_sw;
+  const int32_t *offsets, *counts;
+  int32_t experts;
+  int64_t rows, N, K, max_rows;
+  uint16_t* y;
+};
+hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s);
+// dw[e] bf16 [N, K] = sum over the expert's rows; w = g codes [N, rows], x codes [K, rows], scales
+// [N, rows/128] and [K, rows/128].
+hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s);
+
 }  // namespace fp8lin
