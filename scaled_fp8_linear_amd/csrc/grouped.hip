@@ -14,14 +14,12 @@
 
 #include "common.h"
 #include "launch.h"
+#include "mfma_tile.h"
 
 namespace fp8lin {
 
 namespace {
 
-typedef int v8i __attribute__((ext_vector_type(8)));
-typedef float v4f __attribute__((ext_vector_type(4)));
-typedef unsigned v4u __attribute__((ext_vector_type(4)));
 typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(1)));
 
 constexpr int kBlock = 128;                  // codes per scale
@@ -105,63 +103,457 @@ grouped_few_kernel(GroupedArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Weight gradient: a wave makes 64 x 64 elements of dw, operands from memory to registers.
-__global__ void __launch_bounds__(256)
-grouped_wgrad_kernel(GroupedArgs a) {
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-  const int r16 = lane & 15, g4 = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.y * 128 + 64 * (wave >> 1);
-  const int64_t k0 = (int64_t)blockIdx.x * 128 + 64 * (wave & 1);
-  const int e = blockIdx.z;
-  const Span s = expert_span(a.offsets, a.counts, e, a.rows);
-  const int64_t rblocks = a.rows / kBlock;
-  const int64_t b0 = s.first / kBlock, b1 = s.end > s.first ? (s.end + kBlock - 1) / kBlock : b0;
-  v4f acc[4][4] = {};
-  for (int64_t b = b0; b < b1; ++b) {
-    v8i g[4];
-    float sg[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      g[j] = frag(a.w + (n0 + 16 * j + r16) * a.rows + b * kBlock + 32 * g4);
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sg[j][r] = a.sw[(n0 + 16 * j + 4 * g4 + r) * rblocks + b];
+// Tiles: 256 x 256 (RT = 8) or 128 x 256 (RT = 4) elements of the output by 8 waves, two per SIMD,
+// each of RT x 4 16x16 tiles; a K stage of 128 codes per MFMA in one of two LDS slots. Within a
+// stage, fragments, folds and loads go as in gemm_fp8_mx16bw_kernel: a wave holds the stage's 4 B
+// fragments and streams its A rows through a ring of 4, two ahead; the barrier comes RT - 2 rows
+// into the stage, once all of its A rows are read, publishes stage s + 1 and frees the stage's slot
+// for stage s + 2.
+//
+// What differs is where the work comes from. A workgroup walks its tiles as one stream of stages:
+// a cursor two stages ahead issues the loads (of whichever tile they belong to, each with its own
+// buffer resources, so that experts may lie anywhere in 64 bits and a row past the expert's end
+// reads zeros), and the multiplying side only needs to know how many stages a tile has. That number
+// may be any, 1 included (an expert's few rows in the weight gradient). A row's scales of 4 stages
+// come in one 16-byte load a lane into one of two LDS regions when a tile reaches stage 4 i; where
+// less than 4 are left the load takes in what follows in memory, or zeros past the tensor's end
+// (the range check goes by dwords), and nobody reads that.
+//
+// BROWS 128: rows of experts times their weights (one B scale per 128 columns). Rows of no expert
+// are tiles without stages, whose outputs are 0. BROWS 1: weight gradients (a B scale per column).
+constexpr int kStageK = 128;
+constexpr int kTileWgs = 256;                // one workgroup per CU
+constexpr int kBN = 256, kTileWaves = 8, kTileThreads = 64 * kTileWaves;
+constexpr int kMaxSpans = kMoeMaxExperts + 2;
+constexpr int kBatch = 256;                  // tiles of a workgroup's list
+
+template <int BROWS, int RT>
+__global__ void __launch_bounds__(kTileThreads, 1)
+grouped_tile_kernel(GroupedArgs a) {
+  constexpr int WN = 4, CT = 4, WTN = 16 * CT, WTM = 16 * RT, BM = 2 * WTM, BN = kBN;
+  constexpr int kRing = 4;
+  constexpr int SB = (BM + BN) * kStageK;               // bytes of a slot
+  constexpr int kRegion = 16 * kTileThreads;            // 16 bytes of scales per lane
+  constexpr int kRowsPerInst = 1024 / kStageK;          // 8
+  constexpr int kInstA = BM / (kRowsPerInst * kTileWaves), kInstB = BN / (kRowsPerInst * kTileWaves);
+  constexpr int kDma = kInstA + kInstB;
+  constexpr int kStores = RT * CT / 2;                  // of a wave's epilogue
+  constexpr int kMf = RT * CT, kBarrierAt = (RT - 2) * CT, kTail = kMf - kBarrierAt;
+  constexpr int L = 2;                                  // fold lag (MFMAs)
+  constexpr int kGroup = 4, kGroupM = 8;
+  constexpr bool PF = BROWS == 128;                     // scales read a stage ahead
+  static_assert(WTN * WN == BN && RT % kRing == 0 && kDma <= kTail, "tile");
+  static_assert(kBatch <= kTileThreads, "a lane works out a tile");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SB + 2 * kRegion];
+  __shared__ int first_tile[kMaxSpans + 1];             // spans: row tiles before it
+  uint8_t* const regions = smem + 2 * SB;
+
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int cols = BROWS == 128 ? (int)a.N : (int)a.K;  // of the output
+  const int tiles_n = (cols + BN - 1) / BN;
+  const int kblocks = (int)(BROWS == 128 ? a.K : a.rows) / kStageK;   // of an operand's row
+  const uint32_t lda = (uint32_t)(BROWS == 128 ? a.K : a.rows);       // bytes
+  const uint32_t ldb = (uint32_t)(BROWS == 128 ? a.ldw : a.rows);
+  const uint32_t ldsb = (uint32_t)(BROWS == 128 ? a.ldsw : kblocks);  // elements
+  const int64_t ldd = cols;
+
+  // the spans of rows: before the first expert, the experts, after the last
+  const int spans = BROWS == 128 ? a.experts + 2 : a.experts;
+  auto span_of = [&](int i) -> Span {
+    if constexpr (BROWS == 128) {
+      if (i == 0) return {0, 0, expert_span(a.offsets, a.counts, 0, a.rows).first};
+      if (i == spans - 1) {
+        const int64_t b = expert_span(a.offsets, a.counts, a.experts - 1, a.rows).next;
+        return {b, b, a.rows};
+      }
+      return expert_span(a.offsets, a.counts, i - 1, a.rows);
+    } else {
+      return expert_span(a.offsets, a.counts, i, a.rows);
     }
+  };
+  const int tiles_m = BROWS == 128 ? 0 : ((int)a.N + BM - 1) / BM;    // of an expert's gradient
+  if constexpr (BROWS == 128) {
+    for (int i = t; i < spans; i += kTileThreads) {
+      const Span s = span_of(i);
+      first_tile[i + 1] = (int)((s.next - s.first + BM - 1) / BM);
+    }
+    if (t == 0) first_tile[0] = 0;
+    __syncthreads();
+    if (wave == 0) {                           // running sums, 64 spans at a time
+      int base = 0;
+      for (int i0 = 0; i0 < spans; i0 += 64) {
+        int v = i0 + lane < spans ? first_tile[i0 + lane + 1] : 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t k = k0 + 16 * i + r16;
-      const v8i x = frag(a.x + k * a.rows + b * kBlock + 32 * g4);
-      const float sx = a.sx[k * rblocks + b];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const v4f p = mfma(g[j], x);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = fmaf(p[r], sx * sg[j][r], acc[i][j][r]);
+        for (int off = 1; off < 64; off *= 2) {
+          const int o = __shfl_up(v, off, 64);
+          if (lane >= off) v += o;
+        }
+        if (i0 + lane < spans) first_tile[i0 + lane + 1] = base + v;
+        base += __shfl(v, 63, 64);
       }
     }
+    __syncthreads();
   }
-  uint16_t* out = a.y + (int64_t)e * a.N * a.K;
+  const int row_tiles = BROWS == 128 ? __builtin_amdgcn_readfirstlane(first_tile[spans])
+                                     : spans * tiles_m;
+  const int total = row_tiles * tiles_n;
+  // Workgroups are dispatched round-robin over the 8 XCDs: 32 consecutive tiles at a time go to
+  // one XCD, whose L2 then serves the rows and columns that they share.
+  const int wg = (int)(blockIdx.x & 7) * (kTileWgs / 8) + (int)(blockIdx.x >> 3);
+  const int count = wg < total ? (total - wg + kTileWgs - 1) / kTileWgs : 0;
+
+  // The workgroup's tiles, up to kBatch at a time, worked out by a lane each: the divisions and
+  // 64-bit sums of it would not fit beside the accumulators.
+  struct Tile {
+    int nk, m0, n0, e;                         // stages, first row and column, expert
+    int rows, live, ncols, kb0;                // rows of the output, those with products, columns,
+  };                                           // first K block
+  __shared__ __attribute__((aligned(16))) Tile list[kBatch];
+  auto make_tile = [&](int ti) __attribute__((always_inline)) {
+    const int id = ti * kTileWgs + wg;
+    Tile w;
+    int i, local, mt;
+    if constexpr (BROWS == 128) {
+      const int rt = id / tiles_n;
+      int lo = 0, hi = spans;                  // the last span that begins at or before rt
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if (first_tile[mid] <= rt) lo = mid;
+        else hi = mid;
+      }
+      i = lo;
+      mt = first_tile[i + 1] - first_tile[i];
+      local = id - first_tile[i] * tiles_n;
+    } else {
+      i = id / (tiles_m * tiles_n);
+      mt = tiles_m;
+      local = id - i * tiles_m * tiles_n;
+    }
+    const int group = local / (kGroupM * tiles_n), first = group * kGroupM;
+    const int gs = min(mt - first, kGroupM), in = local - first * tiles_n;
+    const int m = (first + in % gs) * BM;
+    w.n0 = in / gs * BN;
+    w.ncols = min(cols - w.n0, BN);
+    const Span s = span_of(i);
+    if constexpr (BROWS == 128) {
+      w.e = i - 1;
+      w.m0 = (int)s.first + m;
+      w.rows = (int)min(s.next - w.m0, (int64_t)BM);
+      w.live = (int)max(min(s.end - w.m0, (int64_t)BM), (int64_t)0);
+      w.kb0 = 0;
+      w.nk = w.live > 0 ? kblocks : 0;
+    } else {
+      w.e = i;
+      w.m0 = m;
+      w.rows = w.live = min((int)a.N - m, BM);
+      w.kb0 = (int)(s.first / kBlock);
+      w.nk = s.end > s.first ? (int)((s.end + kBlock - 1) / kBlock) - w.kb0 : 0;
+      if (w.nk == 0) w.live = 0;
+    }
+    list[ti % kBatch] = w;
+  };
+  auto tile_of = [&](int ti) __attribute__((always_inline)) -> Tile {         // in scalar registers
+    const v4i* q = reinterpret_cast<const v4i*>(&list[ti % kBatch]);
+    const v4i lo = q[0], hi = q[1];
+    auto u = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+    return {u(lo[0]), u(lo[1]), u(lo[2]), u(lo[3]), u(hi[0]), u(hi[1]), u(hi[2]), u(hi[3])};
+  };
+
+  // ---- the loading side
+  int batch_end = 0;
+  const int lrow = kRowsPerInst * wave + (lane >> 3);
+  const int lchunk = (lane & 7) ^ row_swizzle(lrow);
+  const uint32_t lane_a = (uint32_t)lrow * lda + 16u * lchunk;
+  const uint32_t lane_b = (uint32_t)lrow * ldb + 16u * lchunk;
+  const uint32_t inst_a = (uint32_t)(kRowsPerInst * kTileWaves) * lda;
+  const uint32_t inst_b = (uint32_t)(kRowsPerInst * kTileWaves) * ldb;
+  // lane p of the workgroup loads the scales of tile row p < BM, lane 256 + c those of column
+  // (or block of columns) c
+  const int p = 64 * wave + lane;
+  const bool sc_from_a = wave < 4;
+  uint32_t sc_lane = kOutOfRange;              // others are below 2^27
+  if (p < BM) sc_lane = (uint32_t)p * (uint32_t)kblocks * 4u;
+  else if (p >= 256 && p < 256 + BN / BROWS) sc_lane = (uint32_t)(p - 256) * ldsb * 4u;
+  struct Res { const void *a, *b, *s; uint32_t na, nb, ns; int nk; };  // bases, bytes, stages
+  auto res_of = [&](int ti) __attribute__((always_inline)) -> Res {
+    if (ti >= batch_end) return {a.x, a.x, a.x, 0, 0, 0, 0};          // nothing: reads zeros
+    const Tile w = tile_of(ti);
+    const uint32_t in_row = (uint32_t)w.nk * kStageK;
+    Res r;
+    r.nk = w.nk;
+    r.na = (uint32_t)(w.live - 1) * lda + in_row;
+    r.nb = (uint32_t)(w.ncols - 1) * ldb + in_row;
+    if constexpr (BROWS == 128) {
+      r.a = a.x + (int64_t)w.m0 * a.K;
+      r.b = a.w + w.e * a.stride_w + (int64_t)w.n0 * a.ldw;
+    } else {
+      r.a = a.w + (int64_t)w.m0 * a.rows + (int64_t)w.kb0 * kStageK;
+      r.b = a.x + (int64_t)w.n0 * a.rows + (int64_t)w.kb0 * kStageK;
+    }
+    if (sc_from_a) {
+      r.s = BROWS == 128 ? a.sx + (int64_t)w.m0 * kblocks
+                         : a.sw + (int64_t)w.m0 * kblocks + w.kb0;
+      r.ns = ((uint32_t)(w.live - 1) * (uint32_t)kblocks + (uint32_t)w.nk) * 4u;
+    } else {
+      r.s = BROWS == 128 ? a.sw + w.e * a.stride_sw + w.n0 / kBlock * a.ldsw
+                         : a.sx + (int64_t)w.n0 * kblocks + w.kb0;
+      r.ns = ((uint32_t)(w.ncols / BROWS - 1) * ldsb + (uint32_t)w.nk) * 4u;
+    }
+    return r;
+  };
+  auto dma = [&](int d, uint8_t* slot, const Res& r, int kb) __attribute__((always_inline)) {
+    const uint32_t k0 = (uint32_t)kb * kStageK, lds = lds_addr(slot) + 1024u * wave;
+    // added up here, so that no register holds each sum; a stage past the last block reads zeros
+    uint32_t at = kb < r.nk ? (d < kInstA ? lane_a : lane_b) : kOutOfRange;
+    asm volatile("" : "+v"(at));
+    if (d < kInstA)
+      dma16_so(make_rsrc(r.a, r.na), at + d * inst_a, k0, lds + 1024u * kTileWaves * d);
+    else
+      dma16_so(make_rsrc(r.b, r.nb), at + (d - kInstA) * inst_b, k0,
+               lds + BM * kStageK + 1024u * kTileWaves * (d - kInstA));
+  };
+  // the scales of K blocks kb .. kb + 3 into region rg (zeros if not `on`)
+  auto dma_scales = [&](int rg, const Res& r, int kb, bool on) __attribute__((always_inline)) {
+    const uint32_t off = on ? 4u * kb : kOutOfRange / 2;
+    dma16(make_rsrc(r.s, r.ns), sc_lane + off, lds_addr(regions) + (uint32_t)(rg * kRegion) +
+                                                   1024u * wave);
+  };
+
+  // ---- the multiplying side
+  const int r16 = lane & 15, g4 = lane >> 4;
+  const int sw = row_swizzle(r16);
+  const uint32_t fa0 = (uint32_t)(wm * WTM + r16) * kStageK + 16 * ((2 * g4) ^ sw);
+  const uint32_t fa1 = (uint32_t)(wm * WTM + r16) * kStageK + 16 * ((2 * g4 + 1) ^ sw);
+  const uint32_t fb0 = fa0 + (uint32_t)(BM + wn * WTN - wm * WTM) * kStageK;
+  const uint32_t fb1 = fa1 + (uint32_t)(BM + wn * WTN - wm * WTM) * kStageK;
+  auto rd = [&](uint32_t lo_at, uint32_t hi_at) __attribute__((always_inline)) {
+    const v4u lo = lds16(lo_at);
+    const v4u hi = lds16(hi_at);
+    return v8i{(int)lo.x, (int)lo.y, (int)lo.z, (int)lo.w,
+               (int)hi.x, (int)hi.y, (int)hi.z, (int)hi.w};
+  };
+  struct Bases { uint32_t a0, a1, b0, b1; };
+  auto bases = [&](const uint8_t* sm) __attribute__((always_inline)) {
+    uint32_t b = lds_addr(sm);
+    asm volatile("" : "+s"(b));
+    Bases q{b + fa0, b + fa1, b + fb0, b + fb1};
+    asm volatile("" : "+v"(q.a0), "+v"(q.a1), "+v"(q.b0), "+v"(q.b1));
+    return q;
+  };
+  auto rdA = [&](const Bases& q, int i) __attribute__((always_inline)) {
+    return rd(q.a0 + 16u * i * kStageK, q.a1 + 16u * i * kStageK);
+  };
+  auto rdB = [&](const Bases& q, int j) __attribute__((always_inline)) {
+    return rd(q.b0 + 16u * j * kStageK, q.b1 + 16u * j * kStageK);
+  };
+  const int pa_lane = wm * WTM + r16;
+  const int pb_lane = BROWS == 1 ? 256 + wn * WTN + 4 * g4 : 256 + wn * WTN / 128;
+  typedef const __attribute__((address_space(3))) float lds_f32;
+  float fa[RT], fn[PF ? RT : 1], fb[BROWS == 1 ? 4 * CT : 1];
+  // the scales of the group's stage q: of the lane's rows, times the wave's B scale where there is
+  // one, else also of its columns
+  auto rd_scales = [&](float* fs, int rg, int q) __attribute__((always_inline)) {
+    const uint32_t r = lds_addr(regions) + (uint32_t)(rg * kRegion) + 4u * q;
+    uint32_t ba = r + 16u * pa_lane, bb = r + 16u * pb_lane;
+    asm volatile("" : "+v"(ba), "+v"(bb));
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < RT; ++i) fs[i] = *(lds_f32*)(uintptr_t)(ba + 256u * i);
+    if constexpr (BROWS == 1) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < CT; ++j)
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        out[(n0 + 16 * j + 4 * g4 + r) * a.K + k0 + 16 * i + r16] =
-            (uint16_t)f32_to_bf16_bits(acc[i][j][r]);
+        for (int x = 0; x < 4; ++x) fb[4 * j + x] = *(lds_f32*)(uintptr_t)(bb + 256u * j + 16u * x);
+    } else {
+      const float f = *(lds_f32*)(uintptr_t)bb;
+#pragma unroll
+      for (int i = 0; i < RT; ++i) fs[i] *= f;
+    }
+  };
+
+  v4f acc[RT][CT];
+  v8i Bq[CT], Aq[kRing];
+  auto fold = [&](auto FIRST_, int x, const v4f& P) __attribute__((always_inline)) {
+    const int i = x / CT, j = x % CT;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float f = BROWS == 1 ? fa[i] * fb[4 * j + r] : fa[i];
+      acc[i][j][r] = decltype(FIRST_)::value ? P[r] * f : fmaf(P[r], f, acc[i][j][r]);
+    }
+  };
+  Res cur, nxt;             // of this tile and of the next with products
+  int rg = 0;               // region of this stage's scales
+  // Stage s of a tile's `ns`, from slot `mine`; `other` holds the next one. FIRST (s = 0): the last
+  // tile's outputs were stored since the next stage's loads were issued, and may stay under way.
+  // There is no branch in it: folds that the compiler moves past one keep all products in registers.
+  auto stage = [&](auto FIRST_, int s, int ns, int nk, uint8_t* mine, uint8_t* other)
+                   __attribute__((always_inline)) {
+    v4f P[L + 1];
+    const v4f z = {};
+    const Bases qm = bases(mine);
+    Bases qo{};
+    if constexpr (!PF) rd_scales(fa, rg, (s < nk ? s : nk - 1) % kGroup);
+    // the next stage: of the same group of scales, the next group, or the next tile
+    const bool last = s + 1 == ns, turn = last || (s + 1) % kGroup == 0;
+    const int rg1 = turn ? rg ^ 1 : rg;
+    const int s2 = s + 2 < ns ? s + 2 : s + 2 - ns;      // the stage that is loaded
+    const Res r = s + 2 < ns ? cur : nxt;
+#pragma unroll
+    for (int x = 0; x < kMf; ++x) {
+      const int i = x / CT, j = x % CT;
+      P[x % (L + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(Bq[j], Aq[i % kRing], z,
+                                                                        0, 0, 0, 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (x >= L) fold(FIRST_, x - L, P[(x - L) % (L + 1)]);
+      if (j == 0 && i + 2 < RT) Aq[(i + 2) % kRing] = rdA(qm, i + 2);
+      if (x == kBarrierAt - 1) {
+        wait_vm_lgkm<decltype(FIRST_)::value ? kStores : 0>();
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        qo = bases(other);
+      }
+      if (x >= kBarrierAt) {
+        const int y = x - kBarrierAt;
+#pragma unroll
+        for (int d = y * kDma / kTail; d < (y + 1) * kDma / kTail; ++d) dma(d, mine, r, s2);
+        if constexpr (PF)
+          if (y == 1) rd_scales(fn, rg1, last ? 0 : (s + 1 < nk ? s + 1 : s) % kGroup);
+        if (y == 0) Aq[0] = rdA(qo, 0);
+        if (y == CT) Aq[1] = rdA(qo, 1);
+        if (i == RT - 1) Bq[j] = rdB(qo, j);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+#pragma unroll
+    for (int x = kMf - L; x < kMf; ++x) fold(FIRST_, x, P[x % (L + 1)]);
+    if constexpr (PF) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i) fa[i] = fn[i];
+    }
+    // If stage s + 2 begins a group of scales, they go into the region that is not stage s + 1's
+    // (its last reads, of stage s, were done before this stage's barrier); else nobody reads there.
+    dma_scales(rg1 ^ 1, r, s2, s2 % kGroup == 0);
+    rg = rg1;
+  };
+
+  // A lane's 8 neighbouring columns of a row in one 16-byte store; rows and columns outside the
+  // tile's are dropped by the range check, rows without products written as 0 whatever their sums.
+  auto epilogue = [&](const Tile& w) __attribute__((always_inline)) {
+    uint16_t* d = BROWS == 128 ? a.y + (int64_t)w.m0 * ldd + w.n0
+                               : a.y + ((int64_t)w.e * a.N + w.m0) * ldd + w.n0;
+    const v4i r = make_rsrc(d, (uint32_t)(((int64_t)(w.rows - 1) * ldd + w.ncols) * 2));
+    __amdgpu_buffer_rsrc_t rsD = __builtin_amdgcn_make_buffer_rsrc(
+        reinterpret_cast<void*>((uint64_t)(uint32_t)r[0] | (uint64_t)(uint32_t)r[1] << 32), 0, r[2],
+        kRsrcWord3);
+    int mrow = wm * WTM + r16;
+    int ncol = wn * WTN + 16 * (g4 & 1) + 8 * (g4 >> 1);
+    asm volatile("" : "+v"(mrow), "+v"(ncol));  // nothing of it is kept over the next tile
+    const uint32_t base = ((uint32_t)mrow * (uint32_t)ldd + (uint32_t)ncol) * 2u;
+#pragma unroll
+    for (int i = 0; i < RT; ++i) {
+      const bool live = mrow + 16 * i < w.live;
+#pragma unroll
+      for (int jp = 0; jp < CT / 2; ++jp) {
+        const int j = 2 * jp;
+        const uint32_t p0j = pack_bf16x2(acc[i][j][0], acc[i][j][1]);
+        const uint32_t p1j = pack_bf16x2(acc[i][j][2], acc[i][j][3]);
+        const uint32_t p0k = pack_bf16x2(acc[i][j + 1][0], acc[i][j + 1][1]);
+        const uint32_t p1k = pack_bf16x2(acc[i][j + 1][2], acc[i][j + 1][3]);
+        const auto w0 = __builtin_amdgcn_permlane16_swap(p0j, p0k, false, false);
+        const auto w1 = __builtin_amdgcn_permlane16_swap(p1j, p1k, false, false);
+        v4i o = {(int)w0[0], (int)w1[0], (int)w0[1], (int)w1[1]};
+        if (!live) o = v4i{0, 0, 0, 0};
+        const bool in = mrow + 16 * i < w.rows && ncol + 32 * jp < w.ncols;
+        __builtin_amdgcn_raw_buffer_store_b128(
+            o, rsD, in ? base + (uint32_t)(16 * i) * (uint32_t)ldd * 2u + 64u * jp : kOutOfRange, 0,
+            0);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  auto zero_tile = [&](const Tile& w) {
+    uint16_t* d = BROWS == 128 ? a.y + (int64_t)w.m0 * ldd + w.n0
+                               : a.y + ((int64_t)w.e * a.N + w.m0) * ldd + w.n0;
+    const int pieces = w.ncols / 8;            // 16 bytes each
+    for (int i = t; i < w.rows * pieces; i += kTileThreads)
+      *reinterpret_cast<uint4*>(d + (int64_t)(i / pieces) * ldd + 8 * (i % pieces)) =
+          make_uint4(0, 0, 0, 0);
+  };
+
+  for (int first = 0; first < count; first += kBatch) {
+    batch_end = min(count, first + kBatch);
+    if (first > 0) {                           // every wave is through with the last batch
+      asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+      __syncthreads();
+    }
+    if (first + t < batch_end) make_tile(first + t);
+    __syncthreads();
+    auto with_products = [&](int ti) __attribute__((always_inline)) {   // tile ti or a later one
+      while (ti < batch_end && tile_of(ti).nk == 0) ++ti;
+      return ti;
+    };
+    // A tile has at least two stages, so that what is loaded two stages ahead is its own or the next
+    // tile's. The second of a tile of one block multiplies zeros with that block's scales.
+    uint8_t *mine = smem, *other = smem + SB;
+    int ti = with_products(first), tn = with_products(ti + 1);
+    cur = res_of(ti), nxt = res_of(tn);
+    rg = 0;
+    dma_scales(0, cur, 0, true);
+#pragma unroll
+    for (int d = 0; d < kDma; ++d) dma(d, mine, cur, 0);
+#pragma unroll
+    for (int d = 0; d < kDma; ++d) dma(d, other, cur, 1);
+    wait_vm<0>();           // both stages: the first barrier does not wait for the second
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    {
+      const Bases q = bases(mine);
+#pragma unroll
+      for (int j = 0; j < CT; ++j) Bq[j] = rdB(q, j);
+      Aq[0] = rdA(q, 0);
+      Aq[1] = rdA(q, 1);
+      if constexpr (PF) rd_scales(fa, 0, 0);
+    }
+    while (ti < batch_end) {
+      const int nk = tile_of(ti).nk, ns = max(nk, 2);
+      stage(std::true_type{}, 0, ns, nk, mine, other);
+      for (int s = 1; s < ns; ++s) {
+        uint8_t* const m = mine;
+        mine = other, other = m;
+        stage(std::false_type{}, s, ns, nk, mine, other);
+      }
+      uint8_t* const m = mine;
+      mine = other, other = m;
+      epilogue(tile_of(ti));
+      ti = tn, tn = with_products(tn + 1);
+      cur = nxt, nxt = res_of(tn);
+    }
+    // rows of no expert, gradients of experts without rows
+    for (int z = first; z < batch_end; ++z)
+      if (tile_of(z).nk == 0) zero_tile(tile_of(z));
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // no load may land after exit
 }
 
 }  // namespace
 
 hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
+  if (a.max_rows > 64) {
+    if (a.max_rows > 128)
+      hipLaunchKernelGGL((grouped_tile_kernel<128, 8>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
+    else
+      hipLaunchKernelGGL((grouped_tile_kernel<128, 4>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(grouped_few_kernel, dim3((unsigned)(a.N / kFewCols), a.experts + 1),
                      dim3(64 * kFewWaves), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL(grouped_wgrad_kernel,
-                     dim3((unsigned)(a.K / 128), (unsigned)(a.N / 128), a.experts), dim3(256), 0, s,
-                     a);
+  hipLaunchKernelGGL((grouped_tile_kernel<1, 8>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
   return hipGetLastError();
 }
 
