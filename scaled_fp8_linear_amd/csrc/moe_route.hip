@@ -25,7 +25,8 @@ namespace fp8lin {
 
 namespace {
 
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512, kRouteWaves = kRouteThreads / 64;
+constexpr int kRouteBwdThreads = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int CTRL> __device__ __forceinline__ uint32_t dpp_u(uint32_t v) {
@@ -90,29 +91,39 @@ template <typename T> __device__ __forceinline__ T masked_logit() {
   return __builtin_bit_cast(T, (B)(Logit<T>::kInf | (B)((B)1 << (8 * sizeof(B) - 1))));
 }
 
+// A token's experts over G lanes, NV each: pieces of V neighbouring experts, piece after piece
+// over the lanes, so that a group's loads are whole lines.
+template <int G, int NV> struct Lanes {
+  static constexpr int V = NV < 4 ? NV : 4;
+  static constexpr int kMaxK = G * NV < kMoeMaxTopk ? G * NV : kMoeMaxTopk;
+  static constexpr int kSlots = (kMaxK + G - 1) / G;            // choices per lane
+  static __device__ __forceinline__ int expert(int gl, int i) {
+    return i / V * (G * V) + gl * V + i % V;
+  }
+};
+
 // A lane's logits, -inf past the last expert and in rows that are not live.
-template <int NV, typename T>
-__device__ __forceinline__ void load_logits(const T* row, int c0, int E, bool live, T (&x)[NV]) {
+template <int G, int NV, typename T>
+__device__ __forceinline__ void load_logits(const T* row, int gl, int E, bool live, T (&x)[NV]) {
+  using L = Lanes<G, NV>;
 #pragma unroll
   for (int i = 0; i < NV; ++i) x[i] = masked_logit<T>();
   if (!live) return;
-  if (c0 + NV <= E) {
-    __builtin_memcpy(x, row + c0, sizeof(x));
-  } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (c0 + i < E) x[i] = row[c0 + i];
+  for (int i = 0; i < NV; i += L::V) {
+    const int c = L::expert(gl, i);
+    if (c + L::V <= E) {
+      __builtin_memcpy(&x[i], row + c, L::V * sizeof(T));
+    } else {
+#pragma unroll
+      for (int j = 0; j < L::V; ++j)
+        if (c + j < E) x[i + j] = row[c + j];
+    }
   }
 }
 
-template <int G, int NV> struct Lanes {
-  static constexpr int kGroups = kRouteThreads / G;             // tokens of a workgroup's step
-  static constexpr int kMaxK = G * NV < kMoeMaxTopk ? G * NV : kMoeMaxTopk;
-  static constexpr int kSlots = (kMaxK + G - 1) / G;            // choices per lane
-};
-
-// counts[e] and prob[e] (sums over the tokens) -> counts and the two losses; all lanes of the
-// workgroup (at most 1024) call it. `lds`: 16 floats.
+// The losses from a workgroup's sums over the experts, cp (a lane's part of sum_e counts[e] prob[e])
+// and over the tokens, z (the whole). All lanes of at most 16 waves call it.
 __device__ __forceinline__ void write_losses(float* lds, float cp, float z, float scale,
                                              int64_t valid, float* losses) {
   const int t = threadIdx.x, waves = (blockDim.x + 63) / 64;
@@ -127,20 +138,29 @@ __device__ __forceinline__ void write_losses(float* lds, float cp, float z, floa
   }
 }
 
+// LDS written by lanes of this wave is read by others of it: the hardware keeps a wave's LDS
+// operations in order, the fence keeps the compiler's order the same.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// Partial sums of a workgroup: {sum of p, pairs} per expert, then {sum of lse^2, 0}.
+struct Part { float p; int c; };
+
 template <typename T, int G, int NV>
 __global__ void __launch_bounds__(kRouteThreads)
 moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int64_t valid, int E,
                  int k, bool normalize, int32_t* __restrict__ idx, float* __restrict__ weights,
                  float* __restrict__ lse, int32_t* __restrict__ counts,
-                 float* __restrict__ losses, float* __restrict__ part, float loss_scale) {
+                 float* __restrict__ losses, Part* __restrict__ part, float loss_scale) {
   using L = Lanes<G, NV>;
   using Bits = typename Logit<T>::Bits;
   constexpr bool k16 = sizeof(T) == 2;
-  __shared__ float s_prob[kRouteThreads / 64][G * NV];
-  __shared__ int s_cnt[kRouteThreads / 64][G * NV];
-  __shared__ float s_z[kRouteThreads / 64], s_red[16];
+  constexpr int kTokens = kRouteThreads / G;                    // of a step
+  __shared__ Part sums[kRouteWaves][G * NV];
+  __shared__ float s_z[kRouteWaves], s_red[16];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, gl = lane % G;
-  const int c0 = gl * NV;
   float psum[NV];
   int cnt[NV];
 #pragma unroll
@@ -148,25 +168,25 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
   float zsum = 0.f;
 
   // whole waves stay in the loop, so that the lane exchanges see every lane
-  for (int64_t base = (int64_t)blockIdx.x * L::kGroups; base < tokens;
-       base += (int64_t)gridDim.x * L::kGroups) {
+  for (int64_t base = (int64_t)blockIdx.x * kTokens; base < tokens;
+       base += (int64_t)gridDim.x * kTokens) {
     const int64_t tok = base + t / G;
     const bool live = tok < valid;
     T raw[NV];
-    load_logits<NV>(logits + tok * ldl, c0, E, live, raw);
+    load_logits<G>(logits + tok * ldl, gl, E, live, raw);
     float x[NV];
     uint32_t key[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       x[i] = to_f32(raw[i]);
       key[i] = order_key<Bits, Logit<T>::kInf>(__builtin_bit_cast(Bits, raw[i]));
-      if (k16 && key[i]) key[i] = key[i] << 16 | (uint32_t)(0xFFFF - (c0 + i));
+      if (k16 && key[i]) key[i] = key[i] << 16 | (uint32_t)(0xFFFF - L::expert(gl, i));
     }
-    float top = -INFINITY, inv_total = 0.f, row_lse = -INFINITY, wsum = 0.f;
-    int rec_idx[L::kSlots];
-    float rec_w[L::kSlots];
+    float top = -INFINITY;
+    int rec_e[L::kSlots];                      // this lane's choices j = s G + gl
+    float rec_v[L::kSlots];
 #pragma unroll
-    for (int s = 0; s < L::kSlots; ++s) rec_idx[s] = -1, rec_w[s] = 0.f;
+    for (int s = 0; s < L::kSlots; ++s) rec_e[s] = -1, rec_v[s] = -INFINITY;
     for (int j = 0; j < k; ++j) {
       uint32_t m = key[0];
 #pragma unroll
@@ -182,45 +202,49 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
         uint32_t low = 0u;
 #pragma unroll
         for (int i = NV - 1; i >= 0; --i)
-          if (key[i] == gm) low = (uint32_t)(0xFFFF - (c0 + i));
+          if (key[i] == gm) low = (uint32_t)(0xFFFF - L::expert(gl, i));
         e = 0xFFFF - (int)lanes_max_u32<G>(low);
         v = __uint_as_float(key_bits(gm));
       }
       if (gm == 0) e = -1, v = -INFINITY;
-      if (j == 0) {
-        top = v;
-        float total = 0.f, px[NV];
+      if (j == 0) top = v;
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          px[i] = gm == 0 ? 0.f : __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
-          total += px[i];
-        }
-        total = lanes_sum<G>(total);
-        if (gm != 0) {
-          inv_total = 1.0f / total;
-          row_lse = top + __logf(total);
-          if (gl == 0) zsum += row_lse * row_lse;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) psum[i] += px[i] * inv_total;
+      for (int i = 0; i < NV; ++i) {
+        const bool mine = k16 ? key[i] == gm && gm != 0 : e == L::expert(gl, i);
+        if (mine) key[i] = 0u;
+        cnt[i] += mine ? 1 : 0;
       }
-      const float w = e < 0 ? 0.f : __builtin_amdgcn_exp2f((v - top) * kLog2e);
-      wsum += w;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (e == c0 + i) key[i] = 0u, cnt[i] += 1;
 #pragma unroll
       for (int s = 0; s < L::kSlots; ++s)
-        if (j == s * G + gl) rec_idx[s] = e, rec_w[s] = w;
+        if (j == s * G + gl) rec_e[s] = e, rec_v[s] = v;
     }
+    const bool none = top == -INFINITY;        // no expert left (not so for NaN)
+    float total = 0.f, wsum = 0.f, w[L::kSlots];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      x[i] = none ? 0.f : __builtin_amdgcn_exp2f((x[i] - top) * kLog2e);
+      total += x[i];
+    }
+    total = lanes_sum<G>(total);
+    const float inv = none ? 0.f : __builtin_amdgcn_rcpf(total);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) psum[i] += x[i] * inv;
+#pragma unroll
+    for (int s = 0; s < L::kSlots; ++s) {
+      w[s] = rec_e[s] < 0 ? 0.f : __builtin_amdgcn_exp2f((rec_v[s] - top) * kLog2e);
+      wsum += w[s];
+    }
+    wsum = lanes_sum<G>(wsum);
+    const float f = !normalize ? inv : none ? 0.f : __builtin_amdgcn_rcpf(wsum);
+    const float row_lse = none ? -INFINITY : top + __logf(total);
+    if (gl == 0 && !none) zsum += row_lse * row_lse;
     if (tok < tokens) {
-      const float f = !normalize ? inv_total : wsum == 0.f ? 0.f : 1.0f / wsum;
 #pragma unroll
       for (int s = 0; s < L::kSlots; ++s) {
         const int j = s * G + gl;
         if (j < k) {
-          idx[tok * k + j] = rec_idx[s];
-          weights[tok * k + j] = rec_w[s] * f;
+          idx[tok * k + j] = rec_e[s];
+          weights[tok * k + j] = w[s] * f;
         }
       }
       if (gl == 0) lse[tok] = live ? row_lse : 0.f;
@@ -235,74 +259,80 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
       psum[i] += __shfl_xor(psum[i], off, 64);
       cnt[i] += __shfl_xor(cnt[i], off, 64);
     }
-    if (lane < G) s_prob[wave][c0 + i] = psum[i], s_cnt[wave][c0 + i] = cnt[i];
+    if (lane < G) sums[wave][L::expert(gl, i)] = {psum[i], cnt[i]};
   }
   zsum = lanes_sum<64>(zsum);
   if (lane == 0) s_z[wave] = zsum;
   __syncthreads();
-  const float z = s_z[0] + s_z[1] + s_z[2] + s_z[3];
+  float z = 0.f;
+#pragma unroll
+  for (int w = 0; w < kRouteWaves; ++w) z += s_z[w];
   float cp = 0.f;
   for (int e = t; e < E; e += kRouteThreads) {
-    const float p = s_prob[0][e] + s_prob[1][e] + s_prob[2][e] + s_prob[3][e];
-    const int c = s_cnt[0][e] + s_cnt[1][e] + s_cnt[2][e] + s_cnt[3][e];
+    Part s = {0.f, 0};
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) s.p += sums[w][e].p, s.c += sums[w][e].c;
     if (gridDim.x == 1) {
-      counts[e] = c;
-      cp += (float)c * p;
+      counts[e] = s.c;
+      cp += (float)s.c * s.p;
     } else {
-      part[(int64_t)blockIdx.x * E + e] = p;
-      reinterpret_cast<int32_t*>(part)[((int64_t)gridDim.x + blockIdx.x) * E + e] = c;
+      part[(int64_t)blockIdx.x * (E + 1) + e] = s;
     }
   }
-  if (gridDim.x == 1) {
-    write_losses(s_red, cp, z, loss_scale, valid, losses);
-  } else if (t == 0) {
-    part[2 * (int64_t)gridDim.x * E + blockIdx.x] = z;
-  }
+  if (gridDim.x == 1) write_losses(s_red, cp, z, loss_scale, valid, losses);
+  else if (t == 0) part[(int64_t)blockIdx.x * (E + 1) + E] = {z, 0};
 }
 
-// Adds the partial sums of `blocks` workgroups: lanes t, t + E', t + 2 E', ... (E' = E rounded up
-// to a power of two) take an expert's blocks in turn, and one of them adds their sums up.
+// Adds the partial sums of `blocks` workgroups: `ways` lanes share an expert (or the column behind
+// the experts) and take its blocks in turn, 8 loads at a time, since one workgroup's time is that
+// of its loads; then one lane adds theirs up.
 __global__ void __launch_bounds__(1024)
-moe_route_losses_kernel(const float* __restrict__ part, int blocks, int E, int width,
+moe_route_losses_kernel(const Part* __restrict__ part, int blocks, int E, int width,
                         int32_t* __restrict__ counts, float* __restrict__ losses, int64_t valid,
                         float loss_scale) {
-  __shared__ float s_p[1024], s_red[16];
-  __shared__ int s_c[1024];
-  const int32_t* cpart = reinterpret_cast<const int32_t*>(part) + (int64_t)blocks * E;
-  const float* zpart = part + 2 * (int64_t)blocks * E;
+  __shared__ Part sums[1024];
+  __shared__ float s_red[16], s_z;
   const int t = threadIdx.x, e = t % width, r = t / width, ways = 1024 / width;
-  float p = 0.f;
-  int c = 0;
-  if (e < E)
-    for (int b = r; b < blocks; b += ways) {
-      p += part[(int64_t)b * E + e];
-      c += cpart[(int64_t)b * E + e];
+  Part s = {0.f, 0};
+  if (e <= E && r < ways) {
+    constexpr int kAhead = 8;
+    for (int b0 = r; b0 < blocks; b0 += kAhead * ways) {
+      Part v[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int b = b0 + i * ways;
+        v[i] = part[(int64_t)min(b, blocks - 1) * (E + 1) + e];
+        if (b >= blocks) v[i] = {0.f, 0};
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) s.p += v[i].p, s.c += v[i].c;
     }
-  s_p[t] = p, s_c[t] = c;
-  float z = 0.f;
-  for (int b = t; b < blocks; b += 1024) z += zpart[b];
+  }
+  sums[t] = s;
   __syncthreads();
   float cp = 0.f;
-  if (t < E) {
-    p = 0.f, c = 0;
-    for (int i = 0; i < ways; ++i) p += s_p[i * width + t], c += s_c[i * width + t];
-    counts[t] = c;
-    cp = (float)c * p;
+  if (t <= E) {
+    s = {0.f, 0};
+    for (int i = 0; i < ways; ++i) s.p += sums[i * width + t].p, s.c += sums[i * width + t].c;
+    if (t < E) {
+      counts[t] = s.c;
+      cp = (float)s.c * s.p;
+    } else {
+      s_z = s.p;
+    }
   }
   __syncthreads();
-  z = lanes_sum<64>(z);
-  if ((t & 63) == 0) s_p[t >> 6] = z;
-  __syncthreads();
-  z = 0.f;
-  for (int w = 0; w < 16; ++w) z += s_p[w];
-  write_losses(s_red, cp, z, loss_scale, valid, losses);
+  write_losses(s_red, cp, s_z, loss_scale, valid, losses);
 }
 
 // dl[t, e] = p (A (c[e] - sum_e p c) + B lse - [not normalized] sum_j w dw)
 //            + [e = idx[t, j]] w_j (dw_j - [normalized] sum_j w dw)
-// with A = dlosses[0] E / (T^2 k) and B = dlosses[1] 2 / T, c the counts.
+// with A = dlosses[0] E / (T^2 k) and B = dlosses[1] 2 / T, c the counts. The softmax is made again
+// from the row itself: exp(l - lse) would lose what lse rounds off, all of log E in a row of the
+// type's lowest values. The choices' terms reach the lanes that own the experts through LDS, a row
+// of it for each token, within the wave.
 template <typename T, int G, int NV>
-__global__ void __launch_bounds__(kRouteThreads)
+__global__ void __launch_bounds__(kRouteBwdThreads)
 moe_route_bwd_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int64_t valid,
                      int E, int k, bool normalize, const float* __restrict__ lse,
                      const int32_t* __restrict__ idx, const float* __restrict__ weights,
@@ -310,96 +340,124 @@ moe_route_bwd_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, 
                      const float* __restrict__ dlosses, float a_scale, float b_scale,
                      T* __restrict__ dlogits) {
   using L = Lanes<G, NV>;
-  const int t = threadIdx.x, lane = t & 63, gl = lane % G, c0 = gl * NV;
-  const float A = dlosses ? dlosses[0] * a_scale : 0.f;
-  const float B = dlosses ? dlosses[1] * b_scale : 0.f;
-  float c[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) c[i] = c0 + i < E ? (float)counts[c0 + i] : 0.f;
-  const int64_t tok = (int64_t)blockIdx.x * L::kGroups + t / G;
+  constexpr int kTokens = kRouteBwdThreads / G;
+  __shared__ __attribute__((aligned(16))) float rows[kTokens][G * NV];
+  const int t = threadIdx.x, lane = t & 63, gl = lane % G;
+  const int64_t tok = (int64_t)blockIdx.x * kTokens + t / G;
   const bool live = tok < valid;
   T x[NV];
-  load_logits<NV>(logits + tok * ldl, c0, E, live, x);
-  // The softmax is made again from the row itself: exp(l - lse) would lose what lse rounds off,
-  // all of log E in a row of the type's lowest values.
-  float top = to_f32(x[0]);
-  bool any = top > -INFINITY || top != top;
+  load_logits<G>(logits + tok * ldl, gl, E, live, x);
+  const float A = dlosses ? dlosses[0] * a_scale : 0.f;
+  const float B = dlosses ? dlosses[1] * b_scale : 0.f;
+  const float l = live ? lse[tok] : 0.f;
+  float* const row = rows[t / G];
+  float dot = 0.f;
+  if (dweights) {
+    int e[L::kSlots];
+    float w[L::kSlots], dw[L::kSlots];
 #pragma unroll
-  for (int i = 1; i < NV; ++i) {
-    const float v = to_f32(x[i]);
-    any |= v > -INFINITY || v != v;
-    top = __builtin_fmaxf(top, v);
-  }
-  top = lanes_max<G>(top);
-  const bool none = lanes_max_u32<G>(any) == 0u;    // no expert left: p = 0
-  const float l = none ? 0.f : lse[tok];
-  int rec_idx[L::kSlots];
-  float rec_w[L::kSlots], rec_v[L::kSlots], dot = 0.f;
-#pragma unroll
-  for (int s = 0; s < L::kSlots; ++s) {
-    const int j = s * G + gl;
-    rec_idx[s] = -1, rec_w[s] = 0.f, rec_v[s] = 0.f;
-    if (live && j < k && dweights) {
-      const int e = idx[tok * k + j];
-      if (e >= 0 && e < E)
-        rec_idx[s] = e, rec_w[s] = weights[tok * k + j], rec_v[s] = dweights[tok * k + j];
+    for (int s = 0; s < L::kSlots; ++s) {
+      const int j = s * G + gl;
+      e[s] = -1, w[s] = 0.f, dw[s] = 0.f;
+      if (live && j < k) {
+        e[s] = idx[tok * k + j];
+        w[s] = weights[tok * k + j];
+        dw[s] = dweights[tok * k + j];
+      }
     }
-    dot += rec_w[s] * rec_v[s];
+#pragma unroll
+    for (int i = 0; i < NV; i += L::V)
+#pragma unroll
+      for (int j = 0; j < L::V; ++j) row[L::expert(gl, i) + j] = 0.f;
+#pragma unroll
+    for (int s = 0; s < L::kSlots; ++s) {
+      if (e[s] < 0 || e[s] >= E) e[s] = -1, w[s] = 0.f, dw[s] = 0.f;
+      dot += w[s] * dw[s];
+    }
+    dot = lanes_sum<G>(dot);
+    wave_lds_fence();                          // the zeros of this wave's rows come first
+#pragma unroll
+    for (int s = 0; s < L::kSlots; ++s)
+      if (e[s] >= 0) unsafeAtomicAdd(&row[e[s]], w[s] * (dw[s] - (normalize ? dot : 0.f)));
+    wave_lds_fence();
   }
-  dot = lanes_sum<G>(dot);
-  float p[NV], pc = 0.f, total = 0.f, d[NV];
+  float top = to_f32(x[0]);
+#pragma unroll
+  for (int i = 1; i < NV; ++i) top = __builtin_fmaxf(top, to_f32(x[i]));
+  top = lanes_max<G>(top);
+  if (top == -INFINITY) top = 0.f;             // then the sum is 0, or NaN where the row has one
+  float p[NV], pc = 0.f, total = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    p[i] = none ? 0.f : __builtin_amdgcn_exp2f((to_f32(x[i]) - top) * kLog2e);
-    pc += p[i] * c[i];
+    p[i] = __builtin_amdgcn_exp2f((to_f32(x[i]) - top) * kLog2e);
     total += p[i];
   }
   total = lanes_sum<G>(total);
-  total = none ? 0.f : 1.0f / total;
-  pc = lanes_sum<G>(pc) * total;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) p[i] *= total;
+  const bool none = total == 0.f;              // no expert left: p = 0
+  const float inv = none ? 0.f : __builtin_amdgcn_rcpf(total);
   const float rest = none ? 0.f : B * l - (normalize ? 0.f : dot);
+  float d[NV];
+  if (dlosses) {
+    float c[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) d[i] = p[i] * (A * (c[i] - pc) + rest);
-  if (dweights) {
-#pragma unroll
-    for (int s = 0; s < L::kSlots; ++s) {
-      const float g = rec_w[s] * (rec_v[s] - (normalize ? dot : 0.f));
-      for (int j = 0; j < G && s * G + j < k; ++j) {
-        const int from = (lane & ~(G - 1)) | j;
-        const int e = __shfl(rec_idx[s], from, 64);
-        const float v = __shfl(g, from, 64);
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (e == c0 + i) d[i] += v;
-      }
+    for (int i = 0; i < NV; ++i) {
+      const int e = L::expert(gl, i);
+      c[i] = e < E ? (float)counts[e] : 0.f;
+      pc += p[i] * c[i];
     }
-  }
-  if (tok >= tokens) return;
-  T* out = dlogits + tok * E + c0;
-  T o[NV];
+    pc = lanes_sum<G>(pc) * inv;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) o[i] = from_f32<T>(d[i]);
-  if (c0 + NV <= E) {
-    __builtin_memcpy(out, o, sizeof(o));
+    for (int i = 0; i < NV; ++i) d[i] = p[i] * inv * fmaf(A, c[i] - pc, rest);
   } else {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (c0 + i < E) out[i] = o[i];
+    for (int i = 0; i < NV; ++i) d[i] = p[i] * inv * rest;
+  }
+  if (dweights) {
+#pragma unroll
+    for (int i = 0; i < NV; i += L::V)
+#pragma unroll
+      for (int j = 0; j < L::V; ++j) d[i + j] += row[L::expert(gl, i) + j];
+  }
+  if (tok >= tokens) return;
+#pragma unroll
+  for (int i = 0; i < NV; i += L::V) {
+    const int c = L::expert(gl, i);
+    T o[L::V];
+#pragma unroll
+    for (int j = 0; j < L::V; ++j) o[j] = from_f32<T>(d[i + j]);
+    T* const out = dlogits + tok * E + c;
+    if (c + L::V <= E) {
+      __builtin_memcpy(out, o, sizeof(o));
+    } else {
+#pragma unroll
+      for (int j = 0; j < L::V; ++j)
+        if (c + j < E) out[j] = o[j];
+    }
   }
 }
 
-// Lanes of a token and experts of a lane.
-template <typename F>
+// Lanes of a token and experts of a lane. A round of the forward's choice takes NV steps and log2 G
+// exchanges for 64 / G tokens, so wider rows take more lanes; the backward has no rounds and the
+// fewer lanes, the fewer exchanges.
+template <bool BWD, typename F>
 hipError_t by_experts(int E, F f) {
-  if (E <= 8) return f(std::integral_constant<int, 8>{}, std::integral_constant<int, 1>{});
-  if (E <= 16) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{});
-  if (E <= 32) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 2>{});
-  if (E <= 64) return f(std::integral_constant<int, 16>{}, std::integral_constant<int, 4>{});
-  if (E <= 128) return f(std::integral_constant<int, 32>{}, std::integral_constant<int, 4>{});
-  if (E <= 256) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 4>{});
-  return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 8>{});
+  auto with = [&](auto g, auto nv) { return f(g, nv); };
+#define FP8LIN_LANES(G, NV) \
+  with(std::integral_constant<int, G>{}, std::integral_constant<int, NV>{})
+  if (E <= 8) return FP8LIN_LANES(8, 1);
+  if (E <= 16) return FP8LIN_LANES(16, 1);
+  if (E <= 32) return FP8LIN_LANES(16, 2);
+  if (E <= 64) return FP8LIN_LANES(16, 4);
+  if constexpr (BWD) {
+    if (E <= 128) return FP8LIN_LANES(16, 8);
+    if (E <= 256) return FP8LIN_LANES(16, 16);
+    return FP8LIN_LANES(32, 16);
+  } else {
+    if (E <= 128) return FP8LIN_LANES(32, 4);
+    if (E <= 256) return FP8LIN_LANES(32, 8);
+    return FP8LIN_LANES(64, 8);
+  }
+#undef FP8LIN_LANES
 }
 
 template <typename F> hipError_t by_dtype(int dtype, F f) {
@@ -408,12 +466,11 @@ template <typename F> hipError_t by_dtype(int dtype, F f) {
   return f(0.0f);
 }
 
-int group_lanes(int E) { return E <= 8 ? 8 : E <= 64 ? 16 : E <= 128 ? 32 : 64; }
-
-// Workgroups of the forward: one that also writes the losses for few tokens, else up to 256.
+// Workgroups of the forward: one, which also writes the losses, for up to two steps of tokens,
+// else up to 256.
 constexpr int64_t kRouteMaxBlocks = 256;
 int64_t route_blocks(int64_t tokens, int32_t E) {
-  const int64_t per = kRouteThreads / group_lanes(E);
+  const int64_t per = kRouteThreads / (E <= 8 ? 8 : E <= 64 ? 16 : E <= 256 ? 32 : 64);
   const int64_t steps = (tokens + per - 1) / per;
   if (steps <= 2) return 1;
   return steps < kRouteMaxBlocks ? steps : kRouteMaxBlocks;
@@ -423,7 +480,7 @@ int64_t route_blocks(int64_t tokens, int32_t E) {
 
 int64_t moe_route_workspace(int64_t tokens, int32_t experts) {
   const int64_t blocks = route_blocks(tokens, experts);
-  return blocks == 1 ? 0 : blocks * (2 * (int64_t)experts + 1) * 4;
+  return blocks == 1 ? 0 : blocks * ((int64_t)experts + 1) * (int64_t)sizeof(Part);
 }
 
 hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s) {
@@ -432,37 +489,37 @@ hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s) {
   const float scale = (float)((double)a.experts / (t * t * a.topk));
   hipError_t e = by_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
-    return by_experts(a.experts, [&](auto g, auto nv) {
+    return by_experts<false>(a.experts, [&](auto g, auto nv) {
       hipLaunchKernelGGL((moe_route_kernel<T, decltype(g)::value, decltype(nv)::value>),
                          dim3((unsigned)blocks), dim3(kRouteThreads), 0, s,
                          static_cast<const T*>(a.logits), a.ldl, a.tokens, a.valid, a.experts,
                          a.topk, a.normalize, a.idx, a.weights, a.lse, a.counts, a.losses,
-                         a.workspace, scale);
+                         reinterpret_cast<Part*>(a.workspace), scale);
       return hipGetLastError();
     });
   });
   if (e != hipSuccess || blocks == 1) return e;
   int width = 1;
-  while (width < a.experts) width *= 2;
-  hipLaunchKernelGGL(moe_route_losses_kernel, dim3(1), dim3(1024), 0, s, a.workspace, (int)blocks,
-                     a.experts, width, a.counts, a.losses, a.valid, scale);
+  while (width < a.experts + 1) width *= 2;
+  hipLaunchKernelGGL(moe_route_losses_kernel, dim3(1), dim3(1024), 0, s,
+                     reinterpret_cast<const Part*>(a.workspace), (int)blocks, a.experts, width,
+                     a.counts, a.losses, a.valid, scale);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_route_bwd(const MoeRouteArgs& a, hipStream_t s) {
-  const int64_t per = kRouteThreads / group_lanes(a.experts);
-  const int64_t blocks = (a.tokens + per - 1) / per;
-  if (blocks == 0) return hipSuccess;
   const double t = (double)(a.valid > 0 ? a.valid : 1);
   const float sa = (float)((double)a.experts / (t * t * a.topk)), sb = (float)(2.0 / t);
   return by_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
-    return by_experts(a.experts, [&](auto g, auto nv) {
-      hipLaunchKernelGGL((moe_route_bwd_kernel<T, decltype(g)::value, decltype(nv)::value>),
-                         dim3((unsigned)blocks), dim3(kRouteThreads), 0, s,
-                         static_cast<const T*>(a.logits), a.ldl, a.tokens, a.valid, a.experts,
-                         a.topk, a.normalize, a.lse, a.idx, a.weights, a.counts, a.dweights,
-                         a.dlosses, sa, sb, static_cast<T*>(a.dlogits));
+    return by_experts<true>(a.experts, [&](auto g, auto nv) {
+      constexpr int G = decltype(g)::value, kTokens = kRouteBwdThreads / G;
+      hipLaunchKernelGGL((moe_route_bwd_kernel<T, G, decltype(nv)::value>),
+                         dim3((unsigned)((a.tokens + kTokens - 1) / kTokens)),
+                         dim3(kRouteBwdThreads), 0, s, static_cast<const T*>(a.logits), a.ldl,
+                         a.tokens, a.valid, a.experts, a.topk, a.normalize, a.lse, a.idx,
+                         a.weights, a.counts, a.dweights, a.dlosses, sa, sb,
+                         static_cast<T*>(a.dlogits));
       return hipGetLastError();
     });
   });
