@@ -20,8 +20,6 @@ namespace fp8lin {
 
 namespace {
 
-typedef unsigned v4u_any __attribute__((ext_vector_type(4), aligned(1)));
-
 constexpr int kBlock = 128;                  // codes per scale
 
 // The rows of expert e: first, one past the last, one past its padding.
@@ -33,78 +31,222 @@ __device__ __forceinline__ Span expert_span(const int32_t* offsets, const int32_
   return {a, min(a + max((int64_t)counts[e], (int64_t)0), b), b};
 }
 
-__device__ __forceinline__ v8i frag(const uint8_t* p) {   // a lane's 32 codes
-  const v4u_any* q = reinterpret_cast<const v4u_any*>(p);
-  const v4u lo = q[0], hi = q[1];
-  return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
-             (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
 __device__ __forceinline__ v4f mfma(v8i b, v8i a) {
   const v4f z = {};
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(b, a, z, 0, 0, 0, 0, 0, 0);
 }
 
-// ---------------------------------------------------------------------------
-// Few rows per expert: a workgroup makes 32 columns of an expert's rows, its 8 waves taking the
-// K blocks in turn, and adds their sums up through LDS. Operands go from memory to registers.
-constexpr int kFewWaves = 8, kFewCols = 32, kFewRows = 16;
+// The spans of rows: 0 before the first expert, 1 .. experts the experts, experts + 1 after the last.
+__device__ __forceinline__ Span span_of(const GroupedArgs& a, int i) {
+  if (i == 0) return {0, 0, expert_span(a.offsets, a.counts, 0, a.rows).first};
+  if (i <= a.experts) return expert_span(a.offsets, a.counts, i - 1, a.rows);
+  const int64_t b = expert_span(a.offsets, a.counts, a.experts - 1, a.rows).next;
+  return {b, b, a.rows};
+}
+constexpr int kMaxSpans = kMoeMaxExperts + 2;
 
-__global__ void __launch_bounds__(64 * kFewWaves)
+// ---------------------------------------------------------------------------
+// Few rows per expert, where the time is that of reading the weights once. An item is 16 NT columns
+// of 16 MT rows of an expert; a workgroup's 4 waves take a quarter of the K blocks each and add
+// their sums up through LDS. A wave streams its blocks through a ring of D slots of its own in LDS,
+// loaded straight from memory, so that neither registers nor barriers limit what is under way, and
+// goes on with the next item's blocks while an item is finished. (Loads into registers: a line
+// arrives in two halves, which the L1 cannot hold for long enough; 29 us for two experts' 14336 x
+// 4096 with 2 blocks ahead, 39 with 4.) XR: rows of x that a slot holds; lanes of rows past it
+// multiply another row's codes, for nobody.
+constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves;
+
+template <int MT, int NT, int XR, int D>
+__global__ void __launch_bounds__(kFewThreads)
 grouped_few_kernel(GroupedArgs a) {
-  __shared__ float sums[kFewWaves][kFewRows][kFewCols + 1];
-  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  constexpr int kRows = MT > 1 ? 16 * MT : XR, kCols = 16 * NT;
+  constexpr int kW = kCols * kBlock, kX = kRows * kBlock, kSlot = kW + kX + 256;
+  constexpr int kInstW = kCols / 8, kInstX = kRows / 8, kPer = kInstW + kInstX + 1;
+  constexpr int kPitch = kCols + 1;
+  static_assert(kRows <= 64 && (MT == 1 || XR == 16), "a lane a row's scale");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kFewWaves * D * kSlot];
+  __shared__ float sums[kFewWaves][kRows * kPitch];
+  const int t = threadIdx.x, lane = t & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  const int64_t n0 = (int64_t)blockIdx.x * kFewCols;
-  const int e = blockIdx.y;
-  const int64_t kblocks = a.K / kBlock;
-  if (e == a.experts) {                      // the rows past the last expert's and before the first's
-    const Span last = expert_span(a.offsets, a.counts, a.experts - 1, a.rows);
-    const Span head = expert_span(a.offsets, a.counts, 0, a.rows);
-    for (int64_t i = t; i < (a.rows - last.next) * kFewCols; i += blockDim.x)
-      a.y[(last.next + i / kFewCols) * a.N + n0 + i % kFewCols] = 0;
-    for (int64_t i = t; i < head.first * kFewCols; i += blockDim.x)
-      a.y[i / kFewCols * a.N + n0 + i % kFewCols] = 0;
-    return;
-  }
-  const Span s = expert_span(a.offsets, a.counts, e, a.rows);
-  const uint8_t* w = a.w + e * a.stride_w + n0 * a.ldw + 32 * g4;
-  const float* sw = a.sw + e * a.stride_sw + n0 / kBlock * a.ldsw;
-  for (int64_t m0 = s.first; m0 < s.end; m0 += kFewRows) {
-    const bool live = m0 + r16 < s.end;
-    const int64_t row = live ? m0 + r16 : s.first;
-    const uint8_t* x = a.x + row * a.K + 32 * g4;
-    v4f acc[2] = {};
-    for (int64_t kb = wave; kb < kblocks; kb += kFewWaves) {
-      v8i xa = frag(x + kb * kBlock);
-      const float f = (live ? a.sx[row * kblocks + kb] : 0.f) * sw[kb];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const v4f p = mfma(frag(w + (16 * j + r16) * a.ldw + kb * kBlock), xa);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[j][r] = fmaf(p[r], f, acc[j][r]);
+  const int col_blocks = (int)(a.N / kCols);
+  const int kblocks = (int)(a.K / kBlock);
+  const int kb0 = kblocks * wave / kFewWaves, nb = kblocks * (wave + 1) / kFewWaves - kb0;
+  uint8_t* const ring = smem + wave * D * kSlot;
+
+  // The items in the order of spans, rows, columns; this workgroup's are every gridDim.x-th. A lane
+  // holds one of 64 spans at a time.
+  struct Item { int span, first, end, m0, n0; };         // span -1: no more
+  struct Cursor {
+    int base, span;                                      // spans base .. base + 63 are in `l`
+    Span l;
+    uint64_t left;                                       // those with rows, from `span` on
+    int at;                                              // ours within the items from `span` on
+  };
+  auto spans_from = [&](Cursor& c, int base) __attribute__((always_inline)) {
+    c.base = base;
+    c.l = {0, 0, 0};
+    if (base + lane < a.experts + 2) c.l = span_of(a, base + lane);
+    c.left = __ballot(c.l.end > c.l.first);
+  };
+  auto next_item = [&](Cursor& c) __attribute__((always_inline)) -> Item {
+    for (;;) {
+      while (c.left == 0) {
+        if (c.base + 64 >= a.experts + 2) return {-1, 0, 0, 0, 0};
+        spans_from(c, c.base + 64);
       }
+      const int from = __builtin_ctzll(c.left);
+      const int first = __builtin_amdgcn_readlane((int)c.l.first, from);
+      const int end = __builtin_amdgcn_readlane((int)c.l.end, from);
+      const int items = (end - first + kRows - 1) / kRows * col_blocks;
+      if (c.at < items) {
+        const Item w = {c.base + from, first, end, first + c.at / col_blocks * kRows,
+                        c.at % col_blocks * kCols};
+        c.at += (int)gridDim.x;
+        return w;
+      }
+      c.at -= items;
+      c.left &= c.left - 1;
+    }
+  };
+
+  const int lrow = lane >> 3;                            // 8 rows of 128 bytes an instruction
+  auto chunk = [&](int row) { return 16u * ((lane & 7) ^ row_swizzle(row & 15)); };
+  v4i rsW, rsX, rsS;                                     // of the item that is loaded
+  int pb = 0;                                            // its next block of this wave's
+  Cursor pc, cc;                                         // the loading and the adding side's
+  pc.at = cc.at = (int)blockIdx.x;
+  auto seek = [&]() __attribute__((always_inline)) {
+    const Item w = next_item(pc);
+    pb = 0;
+    const int e = w.span - 1;
+    const uint32_t live = (uint32_t)min(w.end - w.m0, kRows);
+    const bool none = w.span < 0;
+    rsW = make_rsrc(none ? a.w : a.w + e * a.stride_w + w.n0 * a.ldw,
+                    none ? 0u : (uint32_t)(kCols - 1) * (uint32_t)a.ldw + (uint32_t)a.K);
+    rsX = make_rsrc(none ? a.x : a.x + (int64_t)w.m0 * a.K, none ? 0u : live * (uint32_t)a.K);
+    rsS = make_rsrc(none ? a.sx : a.sx + (int64_t)w.m0 * kblocks,
+                    none ? 0u : live * (uint32_t)kblocks * 4u);
+  };
+  auto load = [&](uint32_t lds) __attribute__((always_inline)) {
+    const uint32_t k0 = (uint32_t)(kb0 + pb) * kBlock;
+#pragma unroll
+    for (int q = 0; q < kInstW; ++q) {
+      const int row = 8 * q + lrow;
+      dma16_so(rsW, (uint32_t)row * (uint32_t)a.ldw + chunk(row), k0, lds + 1024u * q);
     }
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) sums[wave][r16][16 * j + 4 * g4 + r] = acc[j][r];
-    __syncthreads();
-    const int m = t / kFewCols, n = t % kFewCols;        // 512 lanes: 16 x 32
-    if (m0 + m < s.end) {
-      float v = 0.f;
-#pragma unroll
-      for (int q = 0; q < kFewWaves; ++q) v += sums[q][m][n];
-      a.y[(m0 + m) * a.N + n0 + n] = (uint16_t)f32_to_bf16_bits(v);
+    for (int q = 0; q < kInstX; ++q) {
+      const int row = 8 * q + lrow;
+      dma16_so(rsX, (uint32_t)row * (uint32_t)a.K + chunk(row), k0, lds + kW + 1024u * q);
     }
-    __syncthreads();
+    dma4(rsS, ((uint32_t)lane * (uint32_t)kblocks + (uint32_t)(kb0 + pb)) * 4u, lds + kW + kX);
+    if (++pb >= nb) seek();
+  };
+
+  const int xrow = XR < 16 ? r16 % XR : r16;
+  auto frag = [&](uint32_t at, int row) __attribute__((always_inline)) {   // a lane's 32 codes
+    const int sw = row_swizzle(row);
+    const v4u lo = lds16(at + (uint32_t)row * kBlock + 16 * ((2 * g4) ^ sw));
+    const v4u hi = lds16(at + (uint32_t)row * kBlock + 16 * ((2 * g4 + 1) ^ sw));
+    return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
+               (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+  };
+
+  spans_from(pc, 0);
+  cc = pc;
+  cc.at = (int)blockIdx.x;
+  if (nb > 0) {
+    seek();
+    for (int d = 0; d < D; ++d) load(lds_addr(ring + d * kSlot));
   }
-  for (int64_t i = t; i < (s.next - s.end) * kFewCols; i += blockDim.x)   // padding rows
-    a.y[(s.end + i / kFewCols) * a.N + n0 + i % kFewCols] = 0;
+  uint32_t slot = 0;
+  for (Item w = next_item(cc); w.span >= 0; w = next_item(cc)) {
+    // as constants, so that scalar loads fetch them, which do not count among the blocks' loads
+    const auto* const wscale = (const __attribute__((address_space(4))) float*)(uintptr_t)(
+        a.sw + (int64_t)(w.span - 1) * a.stride_sw + w.n0 / kBlock * a.ldsw + kb0);
+    v4f acc[MT][NT] = {};
+    for (int b = 0; b < nb; ++b) {
+      const float g = wscale[b];
+      wait_vm<(D - 1) * kPer>();
+      const uint32_t at = lds_addr(ring) + slot * kSlot;
+      v8i W[NT], X[MT];
+      float f[MT];
+#pragma unroll
+      for (int j = 0; j < NT; ++j) W[j] = frag(at + 16 * j * kBlock, r16);
+#pragma unroll
+      for (int h = 0; h < MT; ++h) {
+        X[h] = frag(at + kW + 16 * h * kBlock, xrow);
+        f[h] = *(const __attribute__((address_space(3))) float*)(uintptr_t)(at + kW + kX + 64 * h +
+                                                                            4 * xrow) * g;
+      }
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot has been read
+      load(at);
+      slot = slot + 1 == D ? 0 : slot + 1;
+#pragma unroll
+      for (int h = 0; h < MT; ++h)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const v4f p = mfma(W[j], X[h]);
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[h][j][r] = fmaf(p[r], f[h], acc[h][j][r]);
+        }
+    }
+    if (XR == 16 || r16 < XR) {
+#pragma unroll
+      for (int h = 0; h < MT; ++h)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            sums[wave][(16 * h + r16) * kPitch + 16 * j + 4 * g4 + r] = acc[h][j][r];
+    }
+    // barriers of LDS only: the next item's loads stay under way
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    const int live = min(w.end - w.m0, kRows);
+    for (int q = 2 * t; q < live * kCols; q += 2 * kFewThreads) {
+      const int m = q / kCols, n = q % kCols;
+      float lo = 0.f, hi = 0.f;
+#pragma unroll
+      for (int v = 0; v < kFewWaves; ++v) lo += sums[v][m * kPitch + n], hi += sums[v][m * kPitch + n + 1];
+      *reinterpret_cast<uint32_t*>(a.y + (int64_t)(w.m0 + m) * a.N + w.n0 + n) = pack_bf16x2(lo, hi);
+    }
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+  // rows of nobody
+  for (int i = 0; i < a.experts + 2; i += 64) {
+    Cursor z;
+    spans_from(z, i);
+    for (uint64_t m = __ballot(z.l.next > z.l.end); m; m &= m - 1) {
+      const int from = __builtin_ctzll(m);
+      const int end = __builtin_amdgcn_readlane((int)z.l.end, from);
+      const int next = __builtin_amdgcn_readlane((int)z.l.next, from);
+      uint4* const y = reinterpret_cast<uint4*>(a.y + (int64_t)end * a.N);
+      const int64_t pieces = (int64_t)(next - end) * (a.N / 8);
+      for (int64_t q = (int64_t)blockIdx.x * kFewThreads + t; q < pieces;
+           q += (int64_t)gridDim.x * kFewThreads)
+        y[q] = make_uint4(0, 0, 0, 0);
+    }
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // no load may land after exit
+}
+
+template <int MT, int NT, int XR, int D>
+hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
+  // two workgroups a CU, where there are items for them
+  const int64_t items = (a.N / (16 * NT)) * ((a.rows + 15) / 16);
+  hipLaunchKernelGGL((grouped_few_kernel<MT, NT, XR, D>), dim3((unsigned)min(items, (int64_t)512)),
+                     dim3(kFewThreads), 0, s, a);
+  return hipGetLastError();
 }
 
 // ---------------------------------------------------------------------------
 // Tiles: 256 x 256 (RT = 8) or 128 x 256 (RT = 4) elements of the output by 8 waves, two per SIMD,
-// each of RT x 4 16x16 tiles; a K stage of 128 codes per MFMA in one of two LDS slots. Within a
+// each of RT x 4 16x16 tiles; a K stage of 128 codes per MFMA in one of kSlots LDS slots. Within a
 // stage, fragments, folds and loads go as in gemm_fp8_mx16bw_kernel: a wave holds the stage's 4 B
 // fragments and streams its A rows through a ring of 4, two ahead; the barrier comes RT - 2 rows
 // into the stage, once all of its A rows are read, publishes stage s + 1 and frees the stage's slot
@@ -122,18 +264,20 @@ grouped_few_kernel(GroupedArgs a) {
 // BROWS 128: rows of experts times their weights (one B scale per 128 columns). Rows of no expert
 // are tiles without stages, whose outputs are 0. BROWS 1: weight gradients (a B scale per column).
 constexpr int kStageK = 128;
+#ifndef REV
+#define REV false
+#endif
 constexpr int kTileWgs = 256;                // one workgroup per CU
 constexpr int kBN = 256, kTileWaves = 8, kTileThreads = 64 * kTileWaves;
-constexpr int kMaxSpans = kMoeMaxExperts + 2;
-constexpr int kBatch = 256;                  // tiles of a workgroup's list
 
-template <int BROWS, int RT>
+template <int BROWS, int RT, int kSlots>
 __global__ void __launch_bounds__(kTileThreads, 1)
 grouped_tile_kernel(GroupedArgs a) {
   constexpr int WN = 4, CT = 4, WTN = 16 * CT, WTM = 16 * RT, BM = 2 * WTM, BN = kBN;
   constexpr int kRing = 4;
   constexpr int SB = (BM + BN) * kStageK;               // bytes of a slot
-  constexpr int kRegion = 16 * kTileThreads;            // 16 bytes of scales per lane
+  // scales: 16 bytes for each of BM rows and then BN columns, or blocks of them
+  constexpr int kScaleLanes = (BM + BN / BROWS + 63) / 64 * 64, kRegion = 16 * kScaleLanes;
   constexpr int kRowsPerInst = 1024 / kStageK;          // 8
   constexpr int kInstA = BM / (kRowsPerInst * kTileWaves), kInstB = BN / (kRowsPerInst * kTileWaves);
   constexpr int kDma = kInstA + kInstB;
@@ -143,10 +287,12 @@ grouped_tile_kernel(GroupedArgs a) {
   constexpr int kGroup = 4, kGroupM = 8;
   constexpr bool PF = BROWS == 128;                     // scales read a stage ahead
   static_assert(WTN * WN == BN && RT % kRing == 0 && kDma <= kTail, "tile");
-  static_assert(kBatch <= kTileThreads, "a lane works out a tile");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * SB + 2 * kRegion];
-  __shared__ int first_tile[kMaxSpans + 1];             // spans: row tiles before it
-  uint8_t* const regions = smem + 2 * SB;
+  constexpr int kYoung = (kSlots - 2) * (kDma + 1);     // loads younger than the next stage's
+  constexpr int kBatch = kSlots == 3 ? 32 : 128;        // tiles of a workgroup's list
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * SB +
+                                                            (kSlots + 1) * kRegion];
+  __shared__ int first_tile[BROWS == 128 ? kMaxSpans + 1 : 1];   // spans: row tiles before it
+  uint8_t* const regions = smem + kSlots * SB;          // kSlots, and one that nobody reads
 
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -161,22 +307,13 @@ grouped_tile_kernel(GroupedArgs a) {
 
   // the spans of rows: before the first expert, the experts, after the last
   const int spans = BROWS == 128 ? a.experts + 2 : a.experts;
-  auto span_of = [&](int i) -> Span {
-    if constexpr (BROWS == 128) {
-      if (i == 0) return {0, 0, expert_span(a.offsets, a.counts, 0, a.rows).first};
-      if (i == spans - 1) {
-        const int64_t b = expert_span(a.offsets, a.counts, a.experts - 1, a.rows).next;
-        return {b, b, a.rows};
-      }
-      return expert_span(a.offsets, a.counts, i - 1, a.rows);
-    } else {
-      return expert_span(a.offsets, a.counts, i, a.rows);
-    }
+  auto span = [&](int i) -> Span {
+    return BROWS == 128 ? span_of(a, i) : expert_span(a.offsets, a.counts, i, a.rows);
   };
   const int tiles_m = BROWS == 128 ? 0 : ((int)a.N + BM - 1) / BM;    // of an expert's gradient
   if constexpr (BROWS == 128) {
     for (int i = t; i < spans; i += kTileThreads) {
-      const Span s = span_of(i);
+      const Span s = span(i);
       first_tile[i + 1] = (int)((s.next - s.first + BM - 1) / BM);
     }
     if (t == 0) first_tile[0] = 0;
@@ -212,7 +349,7 @@ grouped_tile_kernel(GroupedArgs a) {
   };                                           // first K block
   __shared__ __attribute__((aligned(16))) Tile list[kBatch];
   auto make_tile = [&](int ti) __attribute__((always_inline)) {
-    const int id = ti * kTileWgs + wg;
+    const int id = (REV ? count - 1 - ti : ti) * kTileWgs + wg;
     Tile w;
     int i, local, mt;
     if constexpr (BROWS == 128) {
@@ -236,7 +373,7 @@ grouped_tile_kernel(GroupedArgs a) {
     const int m = (first + in % gs) * BM;
     w.n0 = in / gs * BN;
     w.ncols = min(cols - w.n0, BN);
-    const Span s = span_of(i);
+    const Span s = span(i);
     if constexpr (BROWS == 128) {
       w.e = i - 1;
       w.m0 = (int)s.first + m;
@@ -269,13 +406,13 @@ grouped_tile_kernel(GroupedArgs a) {
   const uint32_t lane_b = (uint32_t)lrow * ldb + 16u * lchunk;
   const uint32_t inst_a = (uint32_t)(kRowsPerInst * kTileWaves) * lda;
   const uint32_t inst_b = (uint32_t)(kRowsPerInst * kTileWaves) * ldb;
-  // lane p of the workgroup loads the scales of tile row p < BM, lane 256 + c those of column
-  // (or block of columns) c
+  // lane p of the workgroup loads the scales of tile row p < BM, lane BM + c those of column (or
+  // block of columns) c; waves past them load nothing, to the place where nobody reads
   const int p = 64 * wave + lane;
-  const bool sc_from_a = wave < 4;
+  const bool sc_from_a = 64 * wave < BM;
   uint32_t sc_lane = kOutOfRange;              // others are below 2^27
   if (p < BM) sc_lane = (uint32_t)p * (uint32_t)kblocks * 4u;
-  else if (p >= 256 && p < 256 + BN / BROWS) sc_lane = (uint32_t)(p - 256) * ldsb * 4u;
+  else if (p < BM + BN / BROWS) sc_lane = (uint32_t)(p - BM) * ldsb * 4u;
   struct Res { const void *a, *b, *s; uint32_t na, nb, ns; int nk; };  // bases, bytes, stages
   auto res_of = [&](int ti) __attribute__((always_inline)) -> Res {
     if (ti >= batch_end) return {a.x, a.x, a.x, 0, 0, 0, 0};          // nothing: reads zeros
@@ -317,8 +454,9 @@ grouped_tile_kernel(GroupedArgs a) {
   // the scales of K blocks kb .. kb + 3 into region rg (zeros if not `on`)
   auto dma_scales = [&](int rg, const Res& r, int kb, bool on) __attribute__((always_inline)) {
     const uint32_t off = on ? 4u * kb : kOutOfRange / 2;
-    dma16(make_rsrc(r.s, r.ns), sc_lane + off, lds_addr(regions) + (uint32_t)(rg * kRegion) +
-                                                   1024u * wave);
+    const uint32_t at = 64 * wave < kScaleLanes ? (uint32_t)(rg * kRegion) + 1024u * wave
+                                                : (uint32_t)(kSlots * kRegion);
+    dma16(make_rsrc(r.s, r.ns), sc_lane + off, lds_addr(regions) + at);
   };
 
   // ---- the multiplying side
@@ -349,7 +487,7 @@ grouped_tile_kernel(GroupedArgs a) {
     return rd(q.b0 + 16u * j * kStageK, q.b1 + 16u * j * kStageK);
   };
   const int pa_lane = wm * WTM + r16;
-  const int pb_lane = BROWS == 1 ? 256 + wn * WTN + 4 * g4 : 256 + wn * WTN / 128;
+  const int pb_lane = BROWS == 1 ? BM + wn * WTN + 4 * g4 : BM + wn * WTN / 128;
   typedef const __attribute__((address_space(3))) float lds_f32;
   float fa[RT], fn[PF ? RT : 1], fb[BROWS == 1 ? 4 * CT : 1];
   // the scales of the group's stage q: of the lane's rows, times the wave's B scale where there is
@@ -383,22 +521,28 @@ grouped_tile_kernel(GroupedArgs a) {
     }
   };
   Res cur, nxt;             // of this tile and of the next with products
-  int rg = 0;               // region of this stage's scales
-  // Stage s of a tile's `ns`, from slot `mine`; `other` holds the next one. FIRST (s = 0): the last
-  // tile's outputs were stored since the next stage's loads were issued, and may stay under way.
-  // There is no branch in it: folds that the compiler moves past one keep all products in registers.
-  auto stage = [&](auto FIRST_, int s, int ns, int nk, uint8_t* mine, uint8_t* other)
-                   __attribute__((always_inline)) {
+  int rg = 0;               // region of this stage's scales; a group of up to 4 stages takes the next
+  auto after = [&](int r) { return r + 1 == kSlots ? 0 : r + 1; };
+  uint8_t *mine = smem, *other = smem, *third = smem;    // the slots of this stage and the next two
+  auto turn = [&]() __attribute__((always_inline)) {
+    uint8_t* const m = mine;
+    mine = other, other = kSlots == 3 ? third : m, third = m;
+  };
+  // Stage s of a tile's `ns`, from slot `mine`; `other` holds the next one. STORED (s < kSlots - 1):
+  // the last tile's outputs were stored since the next stage's loads were issued, and may stay under
+  // way. There is no branch in it: folds that the compiler moves past one keep all products in
+  // registers.
+  auto stage = [&](auto FIRST_, auto STORED_, int s, int ns, int nk) __attribute__((always_inline)) {
     v4f P[L + 1];
     const v4f z = {};
     const Bases qm = bases(mine);
     Bases qo{};
-    if constexpr (!PF) rd_scales(fa, rg, (s < nk ? s : nk - 1) % kGroup);
+    if constexpr (!PF) rd_scales(fa, rg, min(s, nk - 1) % kGroup);
     // the next stage: of the same group of scales, the next group, or the next tile
-    const bool last = s + 1 == ns, turn = last || (s + 1) % kGroup == 0;
-    const int rg1 = turn ? rg ^ 1 : rg;
-    const int s2 = s + 2 < ns ? s + 2 : s + 2 - ns;      // the stage that is loaded
-    const Res r = s + 2 < ns ? cur : nxt;
+    const bool last = s + 1 == ns;
+    const int rg1 = last || (s + 1) % kGroup == 0 ? after(rg) : rg;
+    const int sl = s + kSlots < ns ? s + kSlots : s + kSlots - ns;   // the stage that is loaded
+    const Res r = s + kSlots < ns ? cur : nxt;
 #pragma unroll
     for (int x = 0; x < kMf; ++x) {
       const int i = x / CT, j = x % CT;
@@ -408,7 +552,7 @@ grouped_tile_kernel(GroupedArgs a) {
       if (x >= L) fold(FIRST_, x - L, P[(x - L) % (L + 1)]);
       if (j == 0 && i + 2 < RT) Aq[(i + 2) % kRing] = rdA(qm, i + 2);
       if (x == kBarrierAt - 1) {
-        wait_vm_lgkm<decltype(FIRST_)::value ? kStores : 0>();
+        wait_vm_lgkm<kYoung + (decltype(STORED_)::value ? kStores : 0)>();
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
         qo = bases(other);
@@ -416,9 +560,9 @@ grouped_tile_kernel(GroupedArgs a) {
       if (x >= kBarrierAt) {
         const int y = x - kBarrierAt;
 #pragma unroll
-        for (int d = y * kDma / kTail; d < (y + 1) * kDma / kTail; ++d) dma(d, mine, r, s2);
+        for (int d = y * kDma / kTail; d < (y + 1) * kDma / kTail; ++d) dma(d, mine, r, sl);
         if constexpr (PF)
-          if (y == 1) rd_scales(fn, rg1, last ? 0 : (s + 1 < nk ? s + 1 : s) % kGroup);
+          if (y == 1) rd_scales(fn, rg1, last ? 0 : min(s + 1, nk - 1) % kGroup);
         if (y == 0) Aq[0] = rdA(qo, 0);
         if (y == CT) Aq[1] = rdA(qo, 1);
         if (i == RT - 1) Bq[j] = rdB(qo, j);
@@ -431,9 +575,14 @@ grouped_tile_kernel(GroupedArgs a) {
 #pragma unroll
       for (int i = 0; i < RT; ++i) fa[i] = fn[i];
     }
-    // If stage s + 2 begins a group of scales, they go into the region that is not stage s + 1's
-    // (its last reads, of stage s, were done before this stage's barrier); else nobody reads there.
-    dma_scales(rg1 ^ 1, r, s2, s2 % kGroup == 0);
+    // If the loaded stage begins a group of scales, they go into the region after that of the stage
+    // before it: with kSlots regions that is neither stage s + 1's, which slower waves still read,
+    // nor one of the stages between. Else the load is an empty one, to where nobody reads.
+    int rgl = rg1;
+    if constexpr (kSlots == 3)
+      rgl = s + 2 == ns || (s + 2 < ns && (s + 2) % kGroup == 0) ? after(rg1) : rg1;
+    const bool begins = sl % kGroup == 0;
+    dma_scales(begins ? after(rgl) : kSlots, r, sl, begins);
     rg = rg1;
   };
 
@@ -494,18 +643,18 @@ grouped_tile_kernel(GroupedArgs a) {
       while (ti < batch_end && tile_of(ti).nk == 0) ++ti;
       return ti;
     };
-    // A tile has at least two stages, so that what is loaded two stages ahead is its own or the next
-    // tile's. The second of a tile of one block multiplies zeros with that block's scales.
-    uint8_t *mine = smem, *other = smem + SB;
+    // A tile has at least kSlots stages, so that what is loaded kSlots ahead is its own or the next
+    // tile's. Stages past its last block multiply zeros with that block's scales.
+    mine = smem, other = smem + SB, third = smem + (kSlots - 1) * SB;
     int ti = with_products(first), tn = with_products(ti + 1);
     cur = res_of(ti), nxt = res_of(tn);
     rg = 0;
     dma_scales(0, cur, 0, true);
 #pragma unroll
-    for (int d = 0; d < kDma; ++d) dma(d, mine, cur, 0);
+    for (int k = 0; k < kSlots; ++k)
 #pragma unroll
-    for (int d = 0; d < kDma; ++d) dma(d, other, cur, 1);
-    wait_vm<0>();           // both stages: the first barrier does not wait for the second
+      for (int d = 0; d < kDma; ++d) dma(d, smem + k * SB, cur, k);
+    wait_vm<0>();           // all of them: the first barriers do not wait for the others
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     {
@@ -517,15 +666,17 @@ grouped_tile_kernel(GroupedArgs a) {
       if constexpr (PF) rd_scales(fa, 0, 0);
     }
     while (ti < batch_end) {
-      const int nk = tile_of(ti).nk, ns = max(nk, 2);
-      stage(std::true_type{}, 0, ns, nk, mine, other);
-      for (int s = 1; s < ns; ++s) {
-        uint8_t* const m = mine;
-        mine = other, other = m;
-        stage(std::false_type{}, s, ns, nk, mine, other);
+      const int nk = tile_of(ti).nk, ns = max(nk, kSlots);
+      stage(std::true_type{}, std::true_type{}, 0, ns, nk);
+      turn();
+      if constexpr (kSlots == 3) {
+        stage(std::false_type{}, std::true_type{}, 1, ns, nk);
+        turn();
       }
-      uint8_t* const m = mine;
-      mine = other, other = m;
+      for (int s = kSlots - 1; s < ns; ++s) {
+        stage(std::false_type{}, std::false_type{}, s, ns, nk);
+        turn();
+      }
       epilogue(tile_of(ti));
       ti = tn, tn = with_products(tn + 1);
       cur = nxt, nxt = res_of(tn);
@@ -540,20 +691,17 @@ grouped_tile_kernel(GroupedArgs a) {
 }  // namespace
 
 hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
-  if (a.max_rows > 64) {
-    if (a.max_rows > 128)
-      hipLaunchKernelGGL((grouped_tile_kernel<128, 8>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
-    else
-      hipLaunchKernelGGL((grouped_tile_kernel<128, 4>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
-    return hipGetLastError();
-  }
-  hipLaunchKernelGGL(grouped_few_kernel, dim3((unsigned)(a.N / kFewCols), a.experts + 1),
-                     dim3(64 * kFewWaves), 0, s, a);
+  if (a.max_rows <= 8) return launch_few<1, 2, 8, 2>(a, s);
+  if (a.max_rows <= 64) return launch_few<1, 2, 16, 2>(a, s);
+  if (a.max_rows <= 256 || a.rows < 384 * (int64_t)a.experts)
+    hipLaunchKernelGGL((grouped_tile_kernel<128, 4, 3>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((grouped_tile_kernel<128, 8, 2>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((grouped_tile_kernel<1, 8>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
+  hipLaunchKernelGGL((grouped_tile_kernel<1, 8, 2>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
   return hipGetLastError();
 }
 
