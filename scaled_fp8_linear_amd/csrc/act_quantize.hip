@@ -40,21 +40,28 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 enum Act { kRelu = 0, kSilu = 1, kGelu = 2 };
 
-template <int CTRL> __device__ __forceinline__ float max_dpp(float v) {
-  return __builtin_fmaxf(v, dpp<CTRL>(v));
+// Maxima over lanes go by the bits of the magnitudes, which order as the numbers do (a lane's own
+// maximum is never NaN): float maxima of values from other lanes would first be made quiet.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp_bits(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
 }
-// maximum over 16 consecutive lanes
-__device__ __forceinline__ float row16_max(float v) {
-  return max_dpp<0x140>(max_dpp<0x141>(max_dpp<0x4E>(max_dpp<0xB1>(v))));
+// over 16 consecutive lanes, of several values step by step (a step has to wait for the last one)
+template <int N> __device__ __forceinline__ void row16_max(uint32_t (&m)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i] = max(m[i], dpp_bits<0xB1>(m[i]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i] = max(m[i], dpp_bits<0x4E>(m[i]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i] = max(m[i], dpp_bits<0x141>(m[i]));
+#pragma unroll
+  for (int i = 0; i < N; ++i) m[i] = max(m[i], dpp_bits<0x140>(m[i]));
 }
-// maximum over the 4 lanes that differ in bits 4 and 5
-__device__ __forceinline__ float col4_max(float v) {
-  const uint32_t u = __float_as_uint(v);
+// over the 4 lanes that differ in bits 4 and 5
+__device__ __forceinline__ uint32_t col4_max(uint32_t u) {
   const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  const uint32_t w = __float_as_uint(
-      __builtin_fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1])));
+  const uint32_t w = max((uint32_t)r[0], (uint32_t)r[1]);
   const auto s = __builtin_amdgcn_permlane32_swap(w, w, false, false);
-  return __builtin_fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+  return max((uint32_t)s[0], (uint32_t)s[1]);
 }
 
 // s(x) = 1 / (1 + exp(-x)); 0 and 1 where the exponential leaves float32
@@ -132,7 +139,7 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
 
 struct Lds {
   uint32_t tile[kAT * kAColDwords];          // transposed codes, 16 KiB
-  float col[kAWaves][kAT];                   // the waves' column maxima
+  uint32_t col[kAWaves][kAT];                // the waves' column maxima
   float mul[kAT];                            // the columns' multipliers
 };
 
@@ -141,48 +148,59 @@ __device__ __forceinline__ int tile_at(int c, int i) {
   return c * kAColDwords + (i ^ ((c >> 3) & (kAColDwords - 1)));
 }
 
-// Where a tile lies: its first row, the lane's first row and column chunk within it.
+// Where a tile lies, and the lane's rows in it: 4 from `row` on, at columns 8 cc.
 struct Place {
-  int64_t rows, row0, tr;
+  int64_t rows, row0, row, tr;
   int t, rg, cc;
+  bool whole;                                // all 128 rows are in the tensor
 };
 
 // One tile v (the lane's 4 x 8) quantized along its rows: codes q [rows, width], scales.
 __device__ __forceinline__ void emit_rows(const float (&v)[kARows][8], const Place& at, int64_t tc,
                                           int64_t width, uint8_t* q, float* scale) {
+  uint32_t m[kARows];
 #pragma unroll
   for (int i = 0; i < kARows; ++i) {
-    float m = 0.f;
+    float f = 0.f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = __builtin_fmaxf(m, __builtin_fabsf(v[i][j]));
-    const TileScale s = tile_scale(row16_max(m));
-    const int64_t r = at.row0 + kARows * at.rg + i;
-    if (r >= at.rows) continue;
-    st_stream8(q + r * width + tc * kAT + 8 * at.cc,
-               codes4(v[i][0], v[i][1], v[i][2], v[i][3], s.mul, s.mul, s.mul, s.mul),
-               codes4(v[i][4], v[i][5], v[i][6], v[i][7], s.mul, s.mul, s.mul, s.mul));
-    if (at.cc == 0) scale[r * (width / kAT) + tc] = s.scale;
+    for (int j = 0; j < 8; j += 2)
+      f = __builtin_fmaxf(__builtin_fmaxf(f, __builtin_fabsf(v[i][j])), __builtin_fabsf(v[i][j + 1]));
+    m[i] = __float_as_uint(f);
+  }
+  row16_max(m);
+  uint8_t* p = q + at.row * width + tc * kAT + 8 * at.cc;
+  const int64_t blocks = width / kAT;
+  float* s = scale + at.row * blocks + tc;
+#pragma unroll
+  for (int i = 0; i < kARows; ++i, p += width, s += blocks) {
+    const TileScale c = tile_scale(__uint_as_float(m[i]));
+    if (!at.whole && at.row + i >= at.rows) continue;
+    st_stream8(p, codes4(v[i][0], v[i][1], v[i][2], v[i][3], c.mul, c.mul, c.mul, c.mul),
+               codes4(v[i][4], v[i][5], v[i][6], v[i][7], c.mul, c.mul, c.mul, c.mul));
+    if (at.cc == 0) *s = c.scale;
   }
 }
 
 // The same tile quantized along its columns: q_t [width, rows], scales [width, rows / 128].
 __device__ __forceinline__ void emit_cols(const float (&v)[kARows][8], const Place& at, int64_t tc,
                                           uint8_t* q_t, float* scale_t, Lds& lds) {
+  static_assert(kARows == 4, "two steps of three");
   const int wave = at.t >> 6, lane = at.t & 63;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    float m = __builtin_fabsf(v[0][j]);
+    float f = 0.f;                           // NaN is no magnitude
 #pragma unroll
-    for (int i = 1; i < kARows; ++i) m = __builtin_fmaxf(m, __builtin_fabsf(v[i][j]));
-    m = col4_max(m);
+    for (int i = 0; i < 4; i += 2)
+      f = __builtin_fmaxf(__builtin_fmaxf(f, __builtin_fabsf(v[i][j])), __builtin_fabsf(v[i + 1][j]));
+    const uint32_t m = col4_max(__float_as_uint(f));
     if (lane < 16) lds.col[wave][8 * at.cc + j] = m;
   }
   __syncthreads();
   if (at.t < kAT) {
-    float m = 0.f;
+    uint32_t m = 0;
 #pragma unroll
-    for (int w = 0; w < kAWaves; ++w) m = __builtin_fmaxf(m, lds.col[w][at.t]);
-    const TileScale s = tile_scale(m);
+    for (int w = 0; w < kAWaves; ++w) m = max(m, lds.col[w][at.t]);
+    const TileScale s = tile_scale(__uint_as_float(m));
     lds.mul[at.t] = s.mul;
     scale_t[(tc * kAT + at.t) * (at.rows / kAT) + at.tr] = s.scale;
   }
@@ -202,25 +220,31 @@ __device__ __forceinline__ void emit_cols(const float (&v)[kARows][8], const Pla
     for (int j = 0; j < 4; ++j) lds.tile[tile_at(8 * at.cc + 4 * half + j, at.rg)] = c[j];
   }
   __syncthreads();
+  constexpr int kItems = kAT * kAT / 16 / kAThreads;     // 16 rows of a column each
+  const int c0 = at.t / 8, ch = at.t % 8;
+  uint8_t* out = q_t + (tc * kAT + c0) * at.rows + at.row0 + 16 * ch;
 #pragma unroll
-  for (int n = 0; n < kAT * kAT / 16 / kAThreads; ++n) {
-    const int item = n * kAThreads + at.t, c = item / 8, ch = item % 8;
+  for (int n = 0; n < kItems; ++n, out += (int64_t)(kAThreads / 8) * at.rows) {
+    const int c = n * (kAThreads / 8) + c0;
     uint4 o;
     o.x = lds.tile[tile_at(c, 4 * ch + 0)];
     o.y = lds.tile[tile_at(c, 4 * ch + 1)];
     o.z = lds.tile[tile_at(c, 4 * ch + 2)];
     o.w = lds.tile[tile_at(c, 4 * ch + 3)];
-    *reinterpret_cast<uint4*>(q_t + (tc * kAT + c) * at.rows + at.row0 + 16 * ch) = o;
+    *reinterpret_cast<uint4*>(out) = o;
   }
 }
 
-__device__ __forceinline__ Place place(int64_t rows, int64_t tiles_c, int64_t& tc) {
+__device__ __forceinline__ Place place(int64_t rows, int tiles_c, int64_t& tc) {
   Place at;
+  const int tr = (int)blockIdx.x / tiles_c;
   at.rows = rows;
-  at.tr = blockIdx.x / tiles_c;
-  tc = blockIdx.x % tiles_c;
-  at.row0 = at.tr * kAT;
+  at.tr = tr;
+  tc = (int)blockIdx.x - tr * tiles_c;
+  at.row0 = (int64_t)tr * kAT;
   at.t = threadIdx.x, at.rg = at.t >> 4, at.cc = at.t & 15;
+  at.row = at.row0 + kARows * at.rg;
+  at.whole = at.row0 + kAT <= rows;
   return at;
 }
 
@@ -229,21 +253,26 @@ __global__ void __launch_bounds__(kAThreads)
 act_quantize_kernel(const T* __restrict__ h, int64_t ldh, int64_t rows, int64_t valid,
                     int64_t cols, uint8_t* __restrict__ q, float* __restrict__ scale,
                     uint8_t* __restrict__ q_t, float* __restrict__ scale_t,
-                    uint8_t* __restrict__ hq, float* __restrict__ hscale, int64_t tiles_c) {
+                    uint8_t* __restrict__ hq, float* __restrict__ hscale, int tiles_c) {
   __shared__ __attribute__((aligned(16))) Lds lds;
   int64_t tc;
   const Place at = place(rows, tiles_c, tc);
-  const int64_t col = tc * kAT + 8 * at.cc;
   float v[kARows][8], u[kARows][8];
+  const T* p = h + at.row * ldh + tc * kAT + 8 * at.cc;
+  if (at.row0 + kAT <= valid) {
 #pragma unroll
-  for (int i = 0; i < kARows; ++i) {
-    const int64_t r = at.row0 + kARows * at.rg + i;
-    if (r < valid) {
-      load8(h + r * ldh + col, v[i]);
-      if constexpr (GATED) load8(h + r * ldh + cols + col, u[i]);
-    } else {
+    for (int i = 0; i < kARows; ++i, p += ldh) {
+      load8(p, v[i]);
+      if constexpr (GATED) load8(p + cols, u[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < kARows; ++i, p += ldh) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i][j] = 0.f, u[i][j] = 0.f;
+      if (at.row + i >= valid) continue;
+      load8(p, v[i]);
+      if constexpr (GATED) load8(p + cols, u[i]);
     }
   }
   if (hq) {
@@ -263,68 +292,85 @@ act_quantize_kernel(const T* __restrict__ h, int64_t ldh, int64_t rows, int64_t 
   if (q_t) emit_cols(v, at, tc, q_t, scale_t, lds);
 }
 
+typedef float act_f32x2 __attribute__((ext_vector_type(2)));
+
+// The 8 values of a row's codes (two dwords).
+__device__ __forceinline__ void decode8(fp8lin_u32x2 w, float scale, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const act_f32x2 p = (i & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i / 2], true)
+                                : __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i / 2], false);
+    f[2 * i] = p[0] * scale, f[2 * i + 1] = p[1] * scale;
+  }
+}
+
 template <typename T, int ACT, bool GATED>
 __global__ void __launch_bounds__(kAThreads)
 act_quantize_bwd_kernel(const T* __restrict__ da, int64_t ldda, int64_t rows, int64_t valid,
                         int64_t cols, const uint8_t* __restrict__ hq,
                         const float* __restrict__ hscale, uint8_t* __restrict__ q,
                         float* __restrict__ scale, uint8_t* __restrict__ q_t,
-                        float* __restrict__ scale_t, T* __restrict__ dh, int64_t tiles_c) {
+                        float* __restrict__ scale_t, T* __restrict__ dh, int tiles_c) {
   __shared__ __attribute__((aligned(16))) Lds lds;
   int64_t tc;
   const Place at = place(rows, tiles_c, tc);
   const int64_t col = tc * kAT + 8 * at.cc;
   const int64_t width = GATED ? 2 * cols : cols, blocks = width / kAT;
-  float v[kARows][8], u[kARows][8];
+  float v[kARows][8], u[kARows][8];            // first da and the values of u, then dg and du
+  fp8lin_u32x2 gq[kARows], uq[kARows];
+  float gs[kARows], us[kARows];
+  {
+    const T* p = da + at.row * ldda + col;
+    const uint8_t* ph = hq + at.row * width + col;
+    const float* ps = hscale + at.row * blocks + tc;
+    auto load = [&](int i) __attribute__((always_inline)) {
+      load8(p, v[i]);
+      gq[i] = __builtin_nontemporal_load(reinterpret_cast<const fp8lin_u32x2*>(ph));
+      gs[i] = *ps;
+      if constexpr (GATED) {
+        uq[i] = __builtin_nontemporal_load(reinterpret_cast<const fp8lin_u32x2*>(ph + cols));
+        us[i] = ps[tiles_c];
+      }
+    };
+    if (at.row0 + kAT <= valid) {
+#pragma unroll
+      for (int i = 0; i < kARows; ++i, p += ldda, ph += width, ps += blocks) load(i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kARows; ++i, p += ldda, ph += width, ps += blocks) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+        gq[i] = uq[i] = fp8lin_u32x2{0u, 0u};
+        gs[i] = us[i] = 0.f;
+        if (at.row + i < valid) load(i);
+      }
+    }
+  }
 #pragma unroll
   for (int i = 0; i < kARows; ++i) {
-    const int64_t r = at.row0 + kARows * at.rg + i;
-    if (r >= valid) {
+    float g[8];
+    decode8(gq[i], gs[i], g);
+    if constexpr (GATED) decode8(uq[i], us[i], u[i]);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f, u[i][j] = 0.f;
-      continue;
-    }
-    float d[8];
-    load8(da + r * ldda + col, d);
-    auto codes = [&](int64_t c) {
-      const fp8lin_u32x2 w =
-          __builtin_nontemporal_load(reinterpret_cast<const fp8lin_u32x2*>(hq + r * width + c));
-      return make_uint2(w[0], w[1]);
-    };
-    const uint2 gq = codes(col);
-    const float gs = hscale[r * blocks + tc];
-    uint2 uq = make_uint2(0, 0);
-    float us = 0.f;
-    if constexpr (GATED) uq = codes(cols + col), us = hscale[r * blocks + tiles_c + tc];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {              // two codes at a time
-      typedef float f32x2 __attribute__((ext_vector_type(2)));
-      const uint32_t g2 = w < 2 ? gq.x : gq.y, u2 = w < 2 ? uq.x : uq.y;
-      const f32x2 g = (w & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)g2, true)
-                              : __builtin_amdgcn_cvt_pk_f32_fp8((int)g2, false);
-      const f32x2 uu = (w & 1) ? __builtin_amdgcn_cvt_pk_f32_fp8((int)u2, true)
-                               : __builtin_amdgcn_cvt_pk_f32_fp8((int)u2, false);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int j = 2 * w + b;
-        float dy;
-        const float y = activate<ACT, true>(g[b] * gs, dy);
-        if constexpr (GATED) {
-          v[i][j] = d[j] * (uu[b] * us) * dy;
-          u[i][j] = d[j] * y;
-        } else {
-          v[i][j] = d[j] * dy;
-        }
+    for (int j = 0; j < 8; ++j) {
+      float d;
+      const float y = activate<ACT, true>(g[j], d);
+      if constexpr (GATED) {
+        const float da_j = v[i][j];
+        v[i][j] = da_j * u[i][j] * d;
+        u[i][j] = da_j * y;
+      } else {
+        v[i][j] *= d;
       }
     }
   }
   if (dh) {
+    T* p = dh + at.row * width + col;
 #pragma unroll
-    for (int i = 0; i < kARows; ++i) {
-      const int64_t r = at.row0 + kARows * at.rg + i;
-      if (r >= rows) continue;
-      store8(dh + r * width + col, v[i]);
-      if constexpr (GATED) store8(dh + r * width + cols + col, u[i]);
+    for (int i = 0; i < kARows; ++i, p += width) {
+      if (!at.whole && at.row + i >= rows) continue;
+      store8(p, v[i]);
+      if constexpr (GATED) store8(p + cols, u[i]);
     }
   }
   if (q) {
@@ -364,7 +410,7 @@ hipError_t launch_act_quantize(const ActArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((act_quantize_kernel<T, decltype(act)::value, decltype(gated)::value>),
                        dim3((unsigned)tiles), dim3(kAThreads), 0, s, static_cast<const T*>(a.x),
                        a.ldx, a.rows, a.valid, a.cols, a.q, a.scale, a.q_t, a.scale_t, a.hq,
-                       a.hscale, tiles_c);
+                       a.hscale, (int)tiles_c);
     return hipGetLastError();
   });
 }
@@ -376,7 +422,7 @@ hipError_t launch_act_quantize_bwd(const ActArgs& a, hipStream_t s) {
     hipLaunchKernelGGL((act_quantize_bwd_kernel<T, decltype(act)::value, decltype(gated)::value>),
                        dim3((unsigned)tiles), dim3(kAThreads), 0, s, static_cast<const T*>(a.x),
                        a.ldx, a.rows, a.valid, a.cols, a.hq, a.hscale, a.q, a.scale, a.q_t,
-                       a.scale_t, static_cast<T*>(a.dh), tiles_c);
+                       a.scale_t, static_cast<T*>(a.dh), (int)tiles_c);
     return hipGetLastError();
   });
 }
