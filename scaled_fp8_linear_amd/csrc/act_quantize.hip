@@ -235,17 +235,26 @@ __device__ __forceinline__ void emit_cols(const float (&v)[kARows][8], const Pla
   }
 }
 
-__device__ __forceinline__ Place place(int64_t rows, int tiles_c, int64_t& tc) {
-  Place at;
-  const int tr = (int)blockIdx.x / tiles_c;
+// Workgroups go round-robin over the 8 XCDs. CHUNKS: an XCD takes a run of tiles, so that the
+// neighbours whose scales share a line write it in one L2. The backward, which writes twice what it
+// reads, gains by it (17408 x 14336 gated: 462 us without, 433 with), the forward loses (366, 374).
+template <bool CHUNKS>
+__device__ __forceinline__ bool place(Place& at, int64_t rows, int tiles_c, int64_t& tc) {
+  int id = (int)blockIdx.x;
+  if constexpr (CHUNKS) {
+    const int total = (int)((rows + kAT - 1) / kAT) * tiles_c, per = (total + 7) / 8;
+    id = (id & 7) * per + (id >> 3);
+    if (((int)blockIdx.x >> 3) >= per || id >= total) return false;
+  }
+  const int tr = id / tiles_c;
   at.rows = rows;
   at.tr = tr;
-  tc = (int)blockIdx.x - tr * tiles_c;
+  tc = id - tr * tiles_c;
   at.row0 = (int64_t)tr * kAT;
   at.t = threadIdx.x, at.rg = at.t >> 4, at.cc = at.t & 15;
   at.row = at.row0 + kARows * at.rg;
   at.whole = at.row0 + kAT <= rows;
-  return at;
+  return true;
 }
 
 template <typename T, int ACT, bool GATED>
@@ -256,7 +265,8 @@ act_quantize_kernel(const T* __restrict__ h, int64_t ldh, int64_t rows, int64_t 
                     uint8_t* __restrict__ hq, float* __restrict__ hscale, int tiles_c) {
   __shared__ __attribute__((aligned(16))) Lds lds;
   int64_t tc;
-  const Place at = place(rows, tiles_c, tc);
+  Place at;
+  place<false>(at, rows, tiles_c, tc);
   float v[kARows][8], u[kARows][8];
   const T* p = h + at.row * ldh + tc * kAT + 8 * at.cc;
   if (at.row0 + kAT <= valid) {
@@ -313,7 +323,8 @@ act_quantize_bwd_kernel(const T* __restrict__ da, int64_t ldda, int64_t rows, in
                         float* __restrict__ scale_t, T* __restrict__ dh, int tiles_c) {
   __shared__ __attribute__((aligned(16))) Lds lds;
   int64_t tc;
-  const Place at = place(rows, tiles_c, tc);
+  Place at;
+  if (!place<true>(at, rows, tiles_c, tc)) return;
   const int64_t col = tc * kAT + 8 * at.cc;
   const int64_t width = GATED ? 2 * cols : cols, blocks = width / kAT;
   float v[kARows][8], u[kARows][8];            // first da and the values of u, then dg and du
@@ -420,8 +431,8 @@ hipError_t launch_act_quantize_bwd(const ActArgs& a, hipStream_t s) {
   return by_act(a, [&](auto tag, auto act, auto gated) {
     using T = decltype(tag);
     hipLaunchKernelGGL((act_quantize_bwd_kernel<T, decltype(act)::value, decltype(gated)::value>),
-                       dim3((unsigned)tiles), dim3(kAThreads), 0, s, static_cast<const T*>(a.x),
-                       a.ldx, a.rows, a.valid, a.cols, a.hq, a.hscale, a.q, a.scale, a.q_t,
+                       dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kAThreads), 0, s,
+                       static_cast<const T*>(a.x), a.ldx, a.rows, a.valid, a.cols, a.hq, a.hscale, a.q, a.scale, a.q_t,
                        a.scale_t, static_cast<T*>(a.dh), (int)tiles_c);
     return hipGetLastError();
   });
