@@ -21,8 +21,9 @@ from ._abi import (FP8_A_E5M2, FP8_AMAX_ACCUMULATE, FP8_BLOCK_1x128, FP8_E5M2, F
                    fp8_act_quantize_bwd, fp8_grouped_linear_fwd, fp8_grouped_linear_dgrad,
                    fp8_grouped_linear_wgrad)
 from .autograd import Fp8Linear, fp8_autocast, fp8_state
-from .experts import (ExpertBlock, ExpertPlan, LayerNorm, expert_combine, expert_dispatch,
-                      expert_plan, layer_norm)
+from .experts import (ExpertBlock, ExpertPlan, GroupedExpertBlock, LayerNorm, Routing,
+                      expert_combine, expert_dispatch, expert_mlp, expert_plan, expert_route,
+                      layer_norm)
 from .state import DelayedScalingLinear
 
 __all__ = ["fp8_quantize_amax", "fp8_scale_update", "fp8_linear_fwd", "fp8_linear_dgrad",
@@ -42,4 +43,5 @@ __all__ = ["fp8_quantize_amax", "fp8_scale_update", "fp8_linear_fwd", "fp8_linea
            "fp8_moe_route_workspace", "fp8_act_quantize", "fp8_act_quantize_bwd",
            "fp8_grouped_linear_fwd", "fp8_grouped_linear_dgrad", "fp8_grouped_linear_wgrad",
            "ExpertBlock", "ExpertPlan", "LayerNorm", "expert_combine", "expert_dispatch",
-           "expert_plan", "layer_norm"]
+           "expert_plan", "layer_norm", "GroupedExpertBlock", "Routing", "expert_mlp",
+           "expert_route"]
