@@ -46,102 +46,153 @@ __device__ __forceinline__ Span span_of(const GroupedArgs& a, int i) {
 constexpr int kMaxSpans = kMoeMaxExperts + 2;
 
 // ---------------------------------------------------------------------------
-// Few rows per expert, where the time is that of reading the weights once. An item is 16 NT columns
-// of 16 MT rows of an expert; a workgroup's 4 waves take a quarter of the K blocks each and add
-// their sums up through LDS. A wave streams its blocks through a ring of D slots of its own in LDS,
-// loaded straight from memory, so that neither registers nor barriers limit what is under way, and
-// goes on with the next item's blocks while an item is finished. (Loads into registers: a line
-// arrives in two halves, which the L1 cannot hold for long enough; 29 us for two experts' 14336 x
-// 4096 with 2 blocks ahead, 39 with 4.) XR: rows of x that a slot holds; lanes of rows past it
-// multiply another row's codes, for nobody.
-constexpr int kFewWaves = 4, kFewThreads = 64 * kFewWaves;
+// Streams: small pieces of the output, each by the 4 waves of a workgroup, for what the tiles below
+// do not fill the card with: an expert's few rows, where the time is that of reading the weights
+// once, and outputs of few tiles. An item is 32 rows of the first operand (columns of y; n) by XR of
+// the second (rows of y; in the weight gradient k). A wave takes a quarter of the item's K blocks
+// and streams them through a ring of D slots of its own in LDS, loaded straight from memory, so that
+// neither registers nor barriers limit what is under way, and goes on with the next item's blocks
+// while the waves' sums are added up through LDS. What bounds it: the weights from memory for few
+// rows (two experts' 14336 x 4096 for a token, 117 MB, 25.4 us: 4.6 TB/s; loaded to registers 29 us
+// with 2 blocks ahead, 39 with 4: a line arrives in two halves, which the L1 cannot hold for long
+// enough); else the way from L2 (64 rows of 128 codes for 32 x 32 sums, near 12 TB/s).
+//
+// XR 8, D 2, two workgroups a CU: up to 8 rows an expert. A slot holds 8 rows of x; lanes of rows
+// past them multiply another row's codes, for nobody. XR 32, D 1, three workgroups a CU: the rest.
+// One block under way a wave is enough there (12 waves a CU, 4.9 KB each): with D 2 and one
+// workgroup a CU 8192 rows of 4 experts took 21.4 us instead of 21.3 at 512 x 512, but 17.6 instead
+// of 16.4 at 1024 x 4096 with 75 rows an expert and 20.3 instead of 14.5 at 1024 x 1024 with 250;
+// with 16 rows an item 42.9 instead of 35.1 at 1024 x 4096 with 250 rows.
+constexpr int kStreamWaves = 4, kStreamThreads = 64 * kStreamWaves;
 
-template <int MT, int NT, int XR, int D>
-__global__ void __launch_bounds__(kFewThreads)
-grouped_few_kernel(GroupedArgs a) {
-  constexpr int kRows = MT > 1 ? 16 * MT : XR, kCols = 16 * NT;
-  constexpr int kW = kCols * kBlock, kX = kRows * kBlock, kSlot = kW + kX + 256;
-  constexpr int kInstW = kCols / 8, kInstX = kRows / 8, kPer = kInstW + kInstX + 1;
+template <int BROWS, int XR, int D>
+__global__ void __launch_bounds__(kStreamThreads)
+grouped_stream_kernel(GroupedArgs a) {
+  constexpr bool kGrad = BROWS == 1;                     // weight gradient
+  constexpr int MT = (XR + 15) / 16, NT = 2;             // 16x16 tiles
+  constexpr int kRows = XR, kCols = 16 * NT;
+  constexpr int kW = kCols * kBlock, kX = kRows * kBlock, kSc = 256;
+  constexpr int kSlot = kW + kX + (kGrad ? 2 : 1) * kSc;
+  constexpr int kInstW = kCols / 8, kInstX = kRows / 8;
+  constexpr int kPer = kInstW + kInstX + (kGrad ? 2 : 1);      // loads of a block
   constexpr int kPitch = kCols + 1;
-  static_assert(kRows <= 64 && (MT == 1 || XR == 16), "a lane a row's scale");
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kFewWaves * D * kSlot];
-  __shared__ float sums[kFewWaves][kRows * kPitch];
+  static_assert(kRows <= 64 && kCols <= 64 && (XR == 8 || XR % 16 == 0), "a lane a row's scale");
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kStreamWaves * D * kSlot];
+  __shared__ float sums[kStreamWaves][kRows * kPitch];
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const int col_blocks = (int)(a.N / kCols);
-  const int kblocks = (int)(a.K / kBlock);
-  const int kb0 = kblocks * wave / kFewWaves, nb = kblocks * (wave + 1) / kFewWaves - kb0;
+  const int row_blocks = kGrad ? (int)(a.K / kRows) : 0;      // of an expert's gradient
+  const int kblocks = (int)((kGrad ? a.rows : a.K) / kBlock); // of an operand's row
+  const uint32_t ldx = (uint32_t)(kGrad ? a.rows : a.K);      // bytes
+  const uint32_t ldw = (uint32_t)(kGrad ? a.rows : a.ldw);
   uint8_t* const ring = smem + wave * D * kSlot;
+  const int spans = kGrad ? a.experts : a.experts + 2;
 
   // The items in the order of spans, rows, columns; this workgroup's are every gridDim.x-th. A lane
   // holds one of 64 spans at a time.
   struct Item { int span, first, end, m0, n0; };         // span -1: no more
   struct Cursor {
-    int base, span;                                      // spans base .. base + 63 are in `l`
+    int base;                                            // spans base .. base + 63 are held
     Span l;
-    uint64_t left;                                       // those with rows, from `span` on
-    int at;                                              // ours within the items from `span` on
+    int items, upto;                                     // of the lane's span, and with those before
+    int at;                                              // ours within the 64 spans' items
   };
   auto spans_from = [&](Cursor& c, int base) __attribute__((always_inline)) {
     c.base = base;
     c.l = {0, 0, 0};
-    if (base + lane < a.experts + 2) c.l = span_of(a, base + lane);
-    c.left = __ballot(c.l.end > c.l.first);
+    const bool in = base + lane < spans;
+    if (in) c.l = kGrad ? expert_span(a.offsets, a.counts, base + lane, a.rows)
+                        : span_of(a, base + lane);
+    c.items = (kGrad ? (in ? row_blocks : 0) : (int)(c.l.end - c.l.first + kRows - 1) / kRows) *
+              col_blocks;
+    c.upto = c.items;
+#pragma unroll
+    for (int off = 1; off < 64; off *= 2) {
+      const int o = __shfl_up(c.upto, off, 64);
+      if (lane >= off) c.upto += o;
+    }
   };
   auto next_item = [&](Cursor& c) __attribute__((always_inline)) -> Item {
-    for (;;) {
-      while (c.left == 0) {
-        if (c.base + 64 >= a.experts + 2) return {-1, 0, 0, 0, 0};
-        spans_from(c, c.base + 64);
-      }
-      const int from = __builtin_ctzll(c.left);
-      const int first = __builtin_amdgcn_readlane((int)c.l.first, from);
-      const int end = __builtin_amdgcn_readlane((int)c.l.end, from);
-      const int items = (end - first + kRows - 1) / kRows * col_blocks;
-      if (c.at < items) {
-        const Item w = {c.base + from, first, end, first + c.at / col_blocks * kRows,
-                        c.at % col_blocks * kCols};
-        c.at += (int)gridDim.x;
-        return w;
-      }
-      c.at -= items;
-      c.left &= c.left - 1;
+    uint64_t later = __ballot(c.upto > c.at);
+    while (later == 0) {
+      if (c.base + 64 >= spans) return {-1, 0, 0, 0, 0};
+      c.at -= __builtin_amdgcn_readlane(c.upto, 63);
+      spans_from(c, c.base + 64);
+      later = __ballot(c.upto > c.at);
     }
+    const int from = __builtin_ctzll(later);
+    const int first = __builtin_amdgcn_readlane((int)c.l.first, from);
+    const int end = __builtin_amdgcn_readlane((int)c.l.end, from);
+    const int in = c.at - __builtin_amdgcn_readlane(c.upto - c.items, from);
+    c.at += (int)gridDim.x;
+    const int m = in / col_blocks * kRows;
+    return {c.base + from, first, end, kGrad ? m : first + m, in % col_blocks * kCols};
+  };
+  // an item's K blocks, and this wave's of them
+  struct Blocks { int first, all, from, n; };
+  auto blocks_of = [&](const Item& w) __attribute__((always_inline)) -> Blocks {
+    Blocks b = {0, kblocks, 0, 0};
+    if constexpr (kGrad) {
+      b.first = w.first / kBlock;
+      b.all = w.end > w.first ? (w.end + kBlock - 1) / kBlock - b.first : 0;
+    }
+    b.from = b.all * wave / kStreamWaves;
+    b.n = b.all * (wave + 1) / kStreamWaves - b.from;
+    return b;
   };
 
   const int lrow = lane >> 3;                            // 8 rows of 128 bytes an instruction
   auto chunk = [&](int row) { return 16u * ((lane & 7) ^ row_swizzle(row & 15)); };
-  v4i rsW, rsX, rsS;                                     // of the item that is loaded
-  int pb = 0;                                            // its next block of this wave's
+  v4i rsW, rsX, rsS, rsT;                                // of the item that is loaded
+  int pb = 0, pn = 0;                                    // its next block of this wave's, and the end
   Cursor pc, cc;                                         // the loading and the adding side's
-  pc.at = cc.at = (int)blockIdx.x;
-  auto seek = [&]() __attribute__((always_inline)) {
-    const Item w = next_item(pc);
-    pb = 0;
-    const int e = w.span - 1;
-    const uint32_t live = (uint32_t)min(w.end - w.m0, kRows);
-    const bool none = w.span < 0;
-    rsW = make_rsrc(none ? a.w : a.w + e * a.stride_w + w.n0 * a.ldw,
-                    none ? 0u : (uint32_t)(kCols - 1) * (uint32_t)a.ldw + (uint32_t)a.K);
-    rsX = make_rsrc(none ? a.x : a.x + (int64_t)w.m0 * a.K, none ? 0u : live * (uint32_t)a.K);
-    rsS = make_rsrc(none ? a.sx : a.sx + (int64_t)w.m0 * kblocks,
-                    none ? 0u : live * (uint32_t)kblocks * 4u);
+  auto seek = [&]() __attribute__((always_inline)) {     // the next item with blocks for this wave
+    Item w = next_item(pc);
+    Blocks b = blocks_of(w);
+    if constexpr (kGrad)
+      while (w.span >= 0 && b.n == 0) {
+        w = next_item(pc);
+        b = blocks_of(w);
+      }
+    const bool none = w.span < 0;                        // empty resources
+    pb = b.from, pn = none ? 0x7FFFFFFF : b.from + b.n;
+    if constexpr (kGrad) {
+      const uint32_t in_row = (uint32_t)b.all * kBlock;
+      const int64_t k0 = (int64_t)b.first * kBlock;
+      rsW = make_rsrc(a.w + w.n0 * a.rows + k0, none ? 0u : (uint32_t)(kCols - 1) * ldw + in_row);
+      rsX = make_rsrc(a.x + w.m0 * a.rows + k0, none ? 0u : (uint32_t)(kRows - 1) * ldx + in_row);
+      rsT = make_rsrc(a.sw + (int64_t)w.n0 * kblocks + b.first,
+                      none ? 0u : (uint32_t)((kCols - 1) * kblocks + b.all) * 4u);
+      rsS = make_rsrc(a.sx + (int64_t)w.m0 * kblocks + b.first,
+                      none ? 0u : (uint32_t)((kRows - 1) * kblocks + b.all) * 4u);
+    } else {
+      const uint32_t live = (uint32_t)min(w.end - w.m0, kRows);
+      const int e = none ? 0 : w.span - 1;
+      rsW = make_rsrc(a.w + e * a.stride_w + w.n0 * a.ldw,
+                      none ? 0u : (uint32_t)(kCols - 1) * ldw + (uint32_t)a.K);
+      rsX = make_rsrc(a.x + (int64_t)w.m0 * a.K, none ? 0u : live * ldx);
+      rsS = make_rsrc(a.sx + (int64_t)w.m0 * kblocks, none ? 0u : live * (uint32_t)kblocks * 4u);
+    }
   };
   auto load = [&](uint32_t lds) __attribute__((always_inline)) {
-    const uint32_t k0 = (uint32_t)(kb0 + pb) * kBlock;
+    const uint32_t k0 = (uint32_t)pb * kBlock;
 #pragma unroll
     for (int q = 0; q < kInstW; ++q) {
       const int row = 8 * q + lrow;
-      dma16_so(rsW, (uint32_t)row * (uint32_t)a.ldw + chunk(row), k0, lds + 1024u * q);
+      dma16_so(rsW, (uint32_t)row * ldw + chunk(row), k0, lds + 1024u * q);
     }
 #pragma unroll
     for (int q = 0; q < kInstX; ++q) {
       const int row = 8 * q + lrow;
-      dma16_so(rsX, (uint32_t)row * (uint32_t)a.K + chunk(row), k0, lds + kW + 1024u * q);
+      dma16_so(rsX, (uint32_t)row * ldx + chunk(row), k0, lds + kW + 1024u * q);
     }
-    dma4(rsS, ((uint32_t)lane * (uint32_t)kblocks + (uint32_t)(kb0 + pb)) * 4u, lds + kW + kX);
-    if (++pb >= nb) seek();
+    // a lane a row: lanes past the tile's rows read what nobody uses
+    const uint32_t at = ((uint32_t)lane * (uint32_t)kblocks + (uint32_t)pb) * 4u;
+    dma4(rsS, at, lds + kW + kX);
+    if constexpr (kGrad) dma4(rsT, at, lds + kW + kX + kSc);
+    if (++pb >= pn) seek();
   };
 
   const int xrow = XR < 16 ? r16 % XR : r16;
@@ -152,95 +203,119 @@ grouped_few_kernel(GroupedArgs a) {
     return v8i{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3],
                (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
   };
+  auto ldf = [&](uint32_t at) __attribute__((always_inline)) {
+    return *(const __attribute__((address_space(3))) float*)(uintptr_t)at;
+  };
 
   spans_from(pc, 0);
+  pc.at = (int)blockIdx.x;
   cc = pc;
-  cc.at = (int)blockIdx.x;
-  if (nb > 0) {
-    seek();
-    for (int d = 0; d < D; ++d) load(lds_addr(ring + d * kSlot));
-  }
+  seek();
+  for (int d = 0; d < D; ++d) load(lds_addr(ring + d * kSlot));
   uint32_t slot = 0;
   for (Item w = next_item(cc); w.span >= 0; w = next_item(cc)) {
+    const Blocks bl = blocks_of(w);
     // as constants, so that scalar loads fetch them, which do not count among the blocks' loads
     const auto* const wscale = (const __attribute__((address_space(4))) float*)(uintptr_t)(
-        a.sw + (int64_t)(w.span - 1) * a.stride_sw + w.n0 / kBlock * a.ldsw + kb0);
+        a.sw + (int64_t)(w.span - 1) * a.stride_sw + w.n0 / kBlock * a.ldsw + bl.from);
     v4f acc[MT][NT] = {};
-    for (int b = 0; b < nb; ++b) {
-      const float g = wscale[b];
+    for (int b = 0; b < bl.n; ++b) {
+      const float g = kGrad ? 1.f : wscale[b];
       wait_vm<(D - 1) * kPer>();
-      const uint32_t at = lds_addr(ring) + slot * kSlot;
+      const uint32_t at = lds_addr(ring) + slot * kSlot, sat = at + kW + kX;
       v8i W[NT], X[MT];
-      float f[MT];
+      float f[MT], h[kGrad ? 4 * NT : 1];
 #pragma unroll
       for (int j = 0; j < NT; ++j) W[j] = frag(at + 16 * j * kBlock, r16);
 #pragma unroll
-      for (int h = 0; h < MT; ++h) {
-        X[h] = frag(at + kW + 16 * h * kBlock, xrow);
-        f[h] = *(const __attribute__((address_space(3))) float*)(uintptr_t)(at + kW + kX + 64 * h +
-                                                                            4 * xrow) * g;
+      for (int i = 0; i < MT; ++i) {
+        X[i] = frag(at + kW + 16 * i * kBlock, xrow);
+        f[i] = ldf(sat + 64 * i + 4 * xrow) * g;
       }
+      if constexpr (kGrad)
+#pragma unroll
+        for (int j = 0; j < 4 * NT; ++j)
+          h[j] = ldf(sat + kSc + 64 * (j / 4) + 16 * g4 + 4 * (j % 4));
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the slot has been read
       load(at);
       slot = slot + 1 == D ? 0 : slot + 1;
 #pragma unroll
-      for (int h = 0; h < MT; ++h)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-          const v4f p = mfma(W[j], X[h]);
+          const v4f p = mfma(W[j], X[i]);
 #pragma unroll
-          for (int r = 0; r < 4; ++r) acc[h][j][r] = fmaf(p[r], f[h], acc[h][j][r]);
+          for (int r = 0; r < 4; ++r)
+            acc[i][j][r] = fmaf(p[r], kGrad ? f[i] * h[4 * j + r] : f[i], acc[i][j][r]);
         }
     }
-    if (XR == 16 || r16 < XR) {
+    if (XR % 16 == 0 || r16 < XR) {
 #pragma unroll
-      for (int h = 0; h < MT; ++h)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
           for (int r = 0; r < 4; ++r)
-            sums[wave][(16 * h + r16) * kPitch + 16 * j + 4 * g4 + r] = acc[h][j][r];
+            sums[wave][(16 * i + r16) * kPitch + 16 * j + 4 * g4 + r] = acc[i][j][r];
     }
     // barriers of LDS only: the next item's loads stay under way
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const int live = min(w.end - w.m0, kRows);
-    for (int q = 2 * t; q < live * kCols; q += 2 * kFewThreads) {
-      const int m = q / kCols, n = q % kCols;
+    const int live = kGrad ? kRows : min(w.end - w.m0, kRows);
+    for (int q = 2 * t; q < live * kCols; q += 2 * kStreamThreads) {
+      // two neighbours of a row of the output
+      const int m = kGrad ? q % kRows : q / kCols, n = kGrad ? q / kRows : q % kCols;
+      constexpr int kNext = kGrad ? kPitch : 1;
       float lo = 0.f, hi = 0.f;
 #pragma unroll
-      for (int v = 0; v < kFewWaves; ++v) lo += sums[v][m * kPitch + n], hi += sums[v][m * kPitch + n + 1];
-      *reinterpret_cast<uint32_t*>(a.y + (int64_t)(w.m0 + m) * a.N + w.n0 + n) = pack_bf16x2(lo, hi);
+      for (int v = 0; v < kStreamWaves; ++v)
+        lo += sums[v][m * kPitch + n], hi += sums[v][m * kPitch + n + kNext];
+      uint16_t* const y = kGrad ? a.y + ((int64_t)w.span * a.N + w.n0 + n) * a.K + w.m0 + m
+                                : a.y + (int64_t)(w.m0 + m) * a.N + w.n0 + n;
+      *reinterpret_cast<uint32_t*>(y) = pack_bf16x2(lo, hi);
     }
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }
-  // rows of nobody
-  for (int i = 0; i < a.experts + 2; i += 64) {
-    Cursor z;
-    spans_from(z, i);
-    for (uint64_t m = __ballot(z.l.next > z.l.end); m; m &= m - 1) {
-      const int from = __builtin_ctzll(m);
+  // rows of nobody: the waves, which are never fewer than the spans, share those that have some
+  if constexpr (!kGrad) {
+    const int me = (int)blockIdx.x * kStreamWaves + wave, waves = (int)gridDim.x * kStreamWaves;
+    for (int base = 0; base < spans; base += 64) {
+      Cursor z;
+      spans_from(z, base);
+      const bool has = z.l.next > z.l.end;
+      const uint64_t m = __ballot(has);
+      const int with = __builtin_popcountll(m);
+      if (with == 0) continue;
+      const int rank = __builtin_popcountll(m & ((1ull << lane) - 1));
+      const int from = __builtin_ctzll(__ballot(has && rank == me % with));
       const int end = __builtin_amdgcn_readlane((int)z.l.end, from);
       const int next = __builtin_amdgcn_readlane((int)z.l.next, from);
+      const int64_t sharers = (waves - me % with + with - 1) / with;
       uint4* const y = reinterpret_cast<uint4*>(a.y + (int64_t)end * a.N);
       const int64_t pieces = (int64_t)(next - end) * (a.N / 8);
-      for (int64_t q = (int64_t)blockIdx.x * kFewThreads + t; q < pieces;
-           q += (int64_t)gridDim.x * kFewThreads)
+      for (int64_t q = me / with * 64 + lane; q < pieces; q += sharers * 64)
         y[q] = make_uint4(0, 0, 0, 0);
     }
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // no load may land after exit
 }
 
-template <int MT, int NT, int XR, int D>
-hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
-  // two workgroups a CU, where there are items for them
-  const int64_t items = (a.N / (16 * NT)) * ((a.rows + 15) / 16);
-  hipLaunchKernelGGL((grouped_few_kernel<MT, NT, XR, D>), dim3((unsigned)min(items, (int64_t)512)),
-                     dim3(kFewThreads), 0, s, a);
+// Items of 32 columns by XR rows: with each expert's last one about half full in y.
+template <int BROWS, int XR>
+int64_t stream_items(const GroupedArgs& a) {
+  const int64_t rows = BROWS == 1 ? a.experts * (a.K / XR) : a.rows / XR + (a.experts + 1) / 2;
+  return a.N / 32 * rows;
+}
+
+template <int BROWS, int XR, int D>
+hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
+  constexpr int64_t kWgs = XR == 8 ? 512 : 768;
+  hipLaunchKernelGGL((grouped_stream_kernel<BROWS, XR, D>),
+                     dim3((unsigned)min(max(stream_items<BROWS, XR>(a), (int64_t)1), kWgs)),
+                     dim3(kStreamThreads), 0, s, a);
   return hipGetLastError();
 }
 
@@ -252,21 +327,22 @@ hipError_t launch_few(const GroupedArgs& a, hipStream_t s) {
 // into the stage, once all of its A rows are read, publishes stage s + 1 and frees the stage's slot
 // for stage s + 2.
 //
-// What differs is where the work comes from. A workgroup walks its tiles as one stream of stages:
-// a cursor two stages ahead issues the loads (of whichever tile they belong to, each with its own
-// buffer resources, so that experts may lie anywhere in 64 bits and a row past the expert's end
-// reads zeros), and the multiplying side only needs to know how many stages a tile has. That number
-// may be any, 1 included (an expert's few rows in the weight gradient). A row's scales of 4 stages
-// come in one 16-byte load a lane into one of two LDS regions when a tile reaches stage 4 i; where
-// less than 4 are left the load takes in what follows in memory, or zeros past the tensor's end
-// (the range check goes by dwords), and nobody reads that.
+// What differs is where the work comes from. A workgroup walks its tiles (listed in LDS, some at a
+// time) as one stream of stages: the loads run kSlots stages ahead of the multiplying side, of
+// whichever tile they belong to, each with its own buffer resources, so that experts may lie anywhere
+// in 64 bits and a row past the expert's end reads zeros. A tile has any number of stages; fewer than
+// kSlots are filled up with stages of zeros. A row's scales of 4 stages come in one 16-byte load a
+// lane into one of kSlots LDS regions when a tile reaches stage 4 i; where less than 4 are left the
+// load takes in what follows in memory, or zeros past the tensor's end (the range check goes by
+// dwords), and nobody reads that.
 //
 // BROWS 128: rows of experts times their weights (one B scale per 128 columns). Rows of no expert
 // are tiles without stages, whose outputs are 0. BROWS 1: weight gradients (a B scale per column).
+//
+// What bounds it: the matrix cores, as in the dense kernel; the in-order wait of a tile's first
+// stages for the last tile's stores costs a further 9 to 12 % (y of 16384 rows of 8 experts, 14336 x
+// 4096: 913 us, 2107 TFLOP/s, 856 in a copy without the stores; dw 1141, 1036 without).
 constexpr int kStageK = 128;
-#ifndef REV
-#define REV false
-#endif
 constexpr int kTileWgs = 256;                // one workgroup per CU
 constexpr int kBN = 256, kTileWaves = 8, kTileThreads = 64 * kTileWaves;
 
@@ -349,7 +425,7 @@ grouped_tile_kernel(GroupedArgs a) {
   };                                           // first K block
   __shared__ __attribute__((aligned(16))) Tile list[kBatch];
   auto make_tile = [&](int ti) __attribute__((always_inline)) {
-    const int id = (REV ? count - 1 - ti : ti) * kTileWgs + wg;
+    const int id = ti * kTileWgs + wg;
     Tile w;
     int i, local, mt;
     if constexpr (BROWS == 128) {
@@ -690,19 +766,48 @@ grouped_tile_kernel(GroupedArgs a) {
 
 }  // namespace
 
-hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
-  if (a.max_rows <= 8) return launch_few<1, 2, 8, 2>(a, s);
-  if (a.max_rows <= 64) return launch_few<1, 2, 16, 2>(a, s);
-  if (a.max_rows <= 256 || a.rows < 384 * (int64_t)a.experts)
-    hipLaunchKernelGGL((grouped_tile_kernel<128, 4, 3>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((grouped_tile_kernel<128, 8, 2>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
+template <int BROWS, int RT, int kSlots>
+hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((grouped_tile_kernel<BROWS, RT, kSlots>), dim3(kTileWgs), dim3(kTileThreads), 0,
+                     s, a);
   return hipGetLastError();
 }
 
+// Rounds of a CU with tiles of `bm` rows; an expert's last tile of y is about half full.
+template <int BROWS>
+int64_t rounds(const GroupedArgs& a, int bm) {
+  const int64_t m = BROWS == 1 ? a.experts * ((a.N + bm - 1) / bm)
+                               : a.rows / bm + (a.experts + 1) / 2;
+  const int64_t n = ((BROWS == 1 ? a.K : a.N) + kBN - 1) / kBN;
+  return (m * n + kTileWgs - 1) / kTileWgs;
+}
+
+// A round of 128-row tiles takes 5/8 of one of 256-row tiles (both measured: y of 1024 rows of 8
+// experts, 14336 x 4096, 147.4 us either way at 3 rounds to 2; of 4096 rows of 64, 2048 x 1408,
+// 59.4 to 76.8 at 3 to 2; of 32768 rows, 147.7 to 136.8 at 9 to 5; dw of 8 experts of 1024 x 1024 and
+// 1000 rows 22.2 to 31.7 at 1 to 1, of 64 of 512 x 512 and 250 rows 22.1 to 20.5 at 2 to 1).
+template <int BROWS>
+bool small_tiles(const GroupedArgs& a) {
+  return 5 * rounds<BROWS>(a, 128) <= 8 * rounds<BROWS>(a, 256);
+}
+
+// Up to 11 items of a stream a CU take less than a round of tiles (y of 8 experts' 250 rows: 35.1 us
+// to 38.7 at 1024 x 4096, 2112 items, 58.2 to 40.4 at 2048 x 4096, 4224; dw of 8 experts, 512 x 512,
+// 1000 rows: 14.4 to 20.6, 2048 items; of 4, 1024 x 1024, 4000 rows: 66.0 to 53.8, 4096).
+constexpr int64_t kStreamItems = 11 * 256;
+
+// Where an expert has up to 32 rows on average, a stream reads the weights about once, and faster
+// (8 experts, 14336 x 4096, 16 rows each: 102 us to 122).
+hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
+  if (a.max_rows <= 8) return launch_stream<128, 8, 2>(a, s);
+  if (a.rows <= 32 * (int64_t)a.experts || stream_items<128, 32>(a) <= kStreamItems)
+    return launch_stream<128, 32, 1>(a, s);
+  return small_tiles<128>(a) ? launch_tiles<128, 4, 3>(a, s) : launch_tiles<128, 8, 2>(a, s);
+}
+
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((grouped_tile_kernel<1, 8, 2>), dim3(kTileWgs), dim3(kTileThreads), 0, s, a);
-  return hipGetLastError();
+  if (stream_items<1, 32>(a) <= kStreamItems) return launch_stream<1, 32, 1>(a, s);
+  return small_tiles<1>(a) ? launch_tiles<1, 4, 2>(a, s) : launch_tiles<1, 8, 2>(a, s);
 }
 
 }  // namespace fp8lin

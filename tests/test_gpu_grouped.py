@@ -177,6 +177,37 @@ def test_wgrad(lib, counts):
         check_wgrad(lib, counts, N, K, extra=128 * (n % 2), lead=128 * (n // 2), seed=n)
 
 
+# outputs of one round of tiles and more, whose tiles are 128 or 256 rows high, and of few of them
+@pytest.mark.parametrize("counts,N,K", [([300, 1, 0, 129], 4352, 384), ([1100, 0, 130], 5120, 640),
+                                        ([2000, 130, 0], 8448, 128), ([4096], 6144, 256),
+                                        ([20, 0, 31, 1], 4352, 128), ([250, 90], 1024, 2176)],
+                         ids=lambda v: str(v))
+def test_products_of_many_tiles(lib, counts, N, K):
+    note(f"grouped counts={counts} N={N} K={K}")
+    check_products(lib, counts, N, K, 128, extra=128)
+    if N * K < 2 ** 21:
+        check_products(lib, counts, N, K, 8, extra=8, lead=8)
+
+
+@pytest.mark.parametrize("counts,N,K", [([130, 0, 400], 1152, 896), ([300, 0, 129, 640], 1664, 1920),
+                                        ([128, 0, 1], 2688, 2688), ([128, 0, 130, 1], 3200, 2048),
+                                        ([2000, 3], 256, 384)], ids=lambda v: str(v))
+def test_wgrad_of_many_tiles(lib, counts, N, K):
+    note(f"grouped wgrad counts={counts} N={N} K={K}")
+    check_wgrad(lib, counts, N, K, extra=128, lead=128)
+
+
+@pytest.mark.parametrize("experts", [62, 63, 130, 300])
+def test_many_experts(lib, experts):
+    """Spans of more than one wave's lanes, the last of them without rows."""
+    counts = [(7 * e * e + 3) % 41 if e % 5 else 0 for e in range(experts - 3)] + [0, 130, 0]
+    for max_rows in (8, None):
+        note(f"grouped {experts} experts max_rows={max_rows}")
+        check_products(lib, counts, 128, 256, 16, max_rows=max_rows)
+    note(f"grouped wgrad {experts} experts")
+    check_wgrad(lib, counts, 128, 256)
+
+
 def test_no_rows(lib):
     note("grouped without rows")
     g = torch.Generator().manual_seed(0)
