@@ -277,35 +277,43 @@ struct Out {
   PyObject* take() { PyObject* r = o; o = nullptr; return r; }
 };
 
-// New outputs of one call. Up to kShared bytes in all they share one allocation, an allocation being
-// 0.4 us of host time: a small call's outputs are a good part of it. Larger ones have their own, so
-// that keeping one of them does not keep the others' memory.
+// New outputs in one allocation, or, where the caller gave one of them, its stream or more than
+// `most` bytes, in one each. An allocation is 0.4 us of host time: of a small call's time the outputs
+// are a good part, and share one up to kShared bytes in all. Larger ones do not, so that keeping one
+// of them does not keep the others' memory.
+constexpr int64_t kShared = 32 * 1024;
 struct Wanted {
   Out* out;
   std::array<int64_t, 2> shape;
   int dims;
   at::ScalarType dtype;
+  bool wanted = true;
   at::IntArrayRef sizes() const { return {shape.data(), (size_t)dims}; }
 };
-void make_all(std::initializer_list<Wanted> outs, const at::Tensor& like, PyObject* stream) {
-  constexpr int64_t kShared = 32 * 1024, kAlign = 64;
+bool make_shared(std::initializer_list<Wanted> outs, const at::Tensor& like, PyObject* stream,
+                 int64_t most) {
+  constexpr int64_t kAlign = 64;
+  auto room = [](const Wanted& w) {
+    return w.wanted ? (bytes_of(w.sizes(), w.dtype) + kAlign - 1) / kAlign * kAlign : 0;
+  };
   int64_t total = 0;
   bool all = stream == Py_None;
-  for (const Wanted& w : outs) {
-    all = all && w.out->o == Py_None;
-    total += (bytes_of(w.sizes(), w.dtype) + kAlign - 1) / kAlign * kAlign;
-  }
-  if (!all || total > kShared) {
-    for (const Wanted& w : outs) w.out->make(w.sizes(), w.dtype, like, stream);
-    return;
-  }
+  for (const Wanted& w : outs) all = all && w.out->o == Py_None, total += room(w);
+  if (!all || total > most) return false;
   const c10::Storage storage = new_storage(total, like);
   int64_t at = 0;
   for (const Wanted& w : outs) {
+    if (!w.wanted) continue;
     w.out->hold(THPVariable_Wrap(in_storage(storage, at, w.sizes(), w.dtype)));
     w.out->ptr = static_cast<char*>(storage.mutable_data()) + at;
-    at += (bytes_of(w.sizes(), w.dtype) + kAlign - 1) / kAlign * kAlign;
+    at += room(w);
   }
+  return true;
+}
+void make_all(std::initializer_list<Wanted> outs, const at::Tensor& like, PyObject* stream,
+              int64_t most = kShared) {
+  if (make_shared(outs, like, stream, most)) return;
+  for (const Wanted& w : outs) w.out->make(w.sizes(), w.dtype, like, stream, w.wanted);
 }
 
 // A uint8 workspace of at least `bytes`.
@@ -612,12 +620,16 @@ void fits_pair(const Arg& q, const Arg& scale, int64_t r, int64_t c, at::Device 
   fits(q, {r, c}, kCodes, dev);
   fits(scale, {r, c / kTile}, {at::kFloat}, dev);
 }
+// Codes and their scales, which are used together and so share an allocation of any size.
 struct OutPair {
   Out q, scale;
   OutPair(PyObject* a, PyObject* b) : q(a), scale(b) {}
+  Wanted codes(int64_t r, int64_t c, bool wanted) { return {&q, {r, c}, 2, at::kByte, wanted}; }
+  Wanted scaling(int64_t r, int64_t c, bool wanted) {
+    return {&scale, {r, c / kTile}, 2, at::kFloat, wanted};
+  }
   void make(int64_t r, int64_t c, const at::Tensor& like, PyObject* stream, bool wanted) {
-    q.make({r, c}, at::kByte, like, stream, wanted);
-    scale.make({r, c / kTile}, at::kFloat, like, stream, wanted);
+    make_all({codes(r, c, wanted), scaling(r, c, wanted)}, like, stream, INT64_MAX);
   }
   float* scales() const { return static_cast<float*>(scale.ptr); }
 };
@@ -642,9 +654,14 @@ PyObject* act_quantize(PyObject* const* p) {
     bad("q_t needs rows to be a multiple of 128, got " + str(rows));
   void* s = launch_stream(*h.t, p[13]);
   OutPair q(p[4], p[5]), t(p[6], p[7]), c(p[8], p[9]);
-  q.make(rows, cols, *h.t, p[13], want_q);
-  t.make(cols, rows, *h.t, p[13], want_t);
-  c.make(rows, width, *h.t, p[13], want_h);
+  if (!make_shared({q.codes(rows, cols, want_q), q.scaling(rows, cols, want_q),
+                    t.codes(cols, rows, want_t), t.scaling(cols, rows, want_t),
+                    c.codes(rows, width, want_h), c.scaling(rows, width, want_h)},
+                   *h.t, p[13], kShared)) {
+    q.make(rows, cols, *h.t, p[13], want_q);
+    t.make(cols, rows, *h.t, p[13], want_t);
+    c.make(rows, width, *h.t, p[13], want_h);
+  }
   check("fp8_act_quantize",
         entry.act_quantize(h.ptr(), ld, rows, valid, cols, act, gated,
                            dt_code(h.t->scalar_type()), q.q.ptr, q.scales(), t.q.ptr, t.scales(),
@@ -675,9 +692,14 @@ PyObject* act_quantize_bwd(PyObject* const* p) {
   void* s = launch_stream(*da.t, p[14]);
   OutPair q(p[6], p[7]), t(p[8], p[9]);
   Out dh(p[10]);
-  q.make(rows, width, *da.t, p[14], want_q);
-  t.make(width, rows, *da.t, p[14], want_t);
-  dh.make({rows, width}, dt, *da.t, p[14], want_dh);
+  if (!make_shared({q.codes(rows, width, want_q), q.scaling(rows, width, want_q),
+                    t.codes(width, rows, want_t), t.scaling(width, rows, want_t),
+                    {&dh, {rows, width}, 2, dt, want_dh}},
+                   *da.t, p[14], kShared)) {
+    q.make(rows, width, *da.t, p[14], want_q);
+    t.make(width, rows, *da.t, p[14], want_t);
+    dh.make({rows, width}, dt, *da.t, p[14], want_dh);
+  }
   check("fp8_act_quantize_bwd",
         entry.act_quantize_bwd(da.ptr(), ld, hq.ptr(), static_cast<float*>(hscale.ptr()), rows,
                                valid, cols, act, gated, dt_code(dt), q.q.ptr, q.scales(), t.q.ptr,

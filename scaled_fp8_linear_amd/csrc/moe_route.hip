@@ -490,24 +490,32 @@ template <typename F> hipError_t by_dtype(int dtype, F f) {
   return f(0.0f);
 }
 
-// Workgroups of the forward: one, which also writes the losses, for up to two steps of tokens,
-// else up to 256.
-int64_t route_blocks(int64_t tokens, int32_t E) {
+// Steps of a workgroup's tokens.
+int64_t route_steps(int64_t tokens, int32_t E) {
   const int64_t per = kRouteThreads / (E <= 8 ? 8 : E <= 64 ? 16 : E <= 256 ? 32 : 64);
-  const int64_t steps = (tokens + per - 1) / per;
-  if (steps <= 2) return 1;
-  return steps < kRouteMaxBlocks ? steps : kRouteMaxBlocks;
+  return (tokens + per - 1) / per;
+}
+int64_t route_blocks(int64_t steps) {
+  return steps <= 2 ? 1 : steps < kRouteMaxBlocks ? steps : kRouteMaxBlocks;
+}
+// Whether one workgroup takes them all and writes the losses: a step's time goes with the choices,
+// that of a second launch is 4 to 5 us (7.3 us to 9.1 for 8 steps of 2 of 7 experts, 11.8 to 8.8 for
+// 16; 7.3 to 8.6 for 4 steps of 10 of 16, 9.9 to 8.8 for 6; 7.9 to 8.7 for 4 steps of 3 of 125, 10.9
+// to 8.8 for 4 of 8 of 64).
+bool one_workgroup(int64_t steps, int32_t E, int32_t k) {
+  return steps <= 2 || steps * (k + 2) <= (E <= 16 ? 48 : 24);
 }
 
 }  // namespace
 
 int64_t moe_route_workspace(int64_t tokens, int32_t experts) {
-  const int64_t blocks = route_blocks(tokens, experts);
+  const int64_t blocks = route_blocks(route_steps(tokens, experts));
   return blocks == 1 ? 0 : blocks * (experts * (int64_t)sizeof(Part) + 4) + (int64_t)sizeof(LossPart);
 }
 
 hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s) {
-  const int64_t blocks = route_blocks(a.tokens, a.experts);
+  const int64_t steps = route_steps(a.tokens, a.experts);
+  const int64_t blocks = one_workgroup(steps, a.experts, a.topk) ? 1 : route_blocks(steps);
   const double t = (double)(a.valid > 0 ? a.valid : 1);
   const float scale = (float)((double)a.experts / (t * t * a.topk));
   Part* const part = reinterpret_cast<Part*>(a.workspace);
