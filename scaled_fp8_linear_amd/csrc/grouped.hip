@@ -320,12 +320,14 @@ hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
 }
 
 // ---------------------------------------------------------------------------
-// Tiles: 256 x 256 (RT = 8) or 128 x 256 (RT = 4) elements of the output by 8 waves, two per SIMD,
-// each of RT x 4 16x16 tiles; a K stage of 128 codes per MFMA in one of kSlots LDS slots. Within a
-// stage, fragments, folds and loads go as in gemm_fp8_mx16bw_kernel: a wave holds the stage's 4 B
-// fragments and streams its A rows through a ring of 4, two ahead; the barrier comes RT - 2 rows
-// into the stage, once all of its A rows are read, publishes stage s + 1 and frees the stage's slot
-// for stage s + 2.
+// Tiles of the output by 8 waves, two per SIMD, each of RT x 4 16x16 tiles: 256 x 256 (RT = 8), or
+// 128 x 256 (RT = 4) with a third slot; or 128 x 128 by 4 waves, two workgroups a CU, for weight
+// gradients, whose scales leave no room for that slot (8 experts of 1024 x 1024 over 60000 rows 125
+// us to 141 with 128 x 256; of 27 experts of 6272 x 128 16.1 to 20.3). A K stage is 128 codes per
+// MFMA in one of kSlots LDS slots. Within a stage, fragments, folds and loads go as in
+// gemm_fp8_mx16bw_kernel: a wave holds the stage's 4 B fragments and streams its A rows through a
+// ring of 4, two ahead; the barrier comes RT - 2 rows into the stage, once all of its A rows are
+// read, publishes stage s + 1 and frees the stage's slot for stage s + kSlots.
 //
 // What differs is where the work comes from. A workgroup walks its tiles (listed in LDS, some at a
 // time) as one stream of stages: the loads run kSlots stages ahead of the multiplying side, of
@@ -343,13 +345,14 @@ hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
 // stages for the last tile's stores costs a further 9 to 12 % (y of 16384 rows of 8 experts, 14336 x
 // 4096: 913 us, 2107 TFLOP/s, 856 in a copy without the stores; dw 1141, 1036 without).
 constexpr int kStageK = 128;
-constexpr int kTileWgs = 256;                // one workgroup per CU
-constexpr int kBN = 256, kTileWaves = 8, kTileThreads = 64 * kTileWaves;
+constexpr int kCus = 256;
 
-template <int BROWS, int RT, int kSlots>
-__global__ void __launch_bounds__(kTileThreads, 1)
+template <int BROWS, int RT, int kSlots, int kTileWaves>
+__global__ void __launch_bounds__(64 * kTileWaves, 8 / kTileWaves)
 grouped_tile_kernel(GroupedArgs a) {
-  constexpr int WN = 4, CT = 4, WTN = 16 * CT, WTM = 16 * RT, BM = 2 * WTM, BN = kBN;
+  constexpr int kTileThreads = 64 * kTileWaves, kTileWgs = kCus * 8 / kTileWaves;
+  constexpr int WN = kTileWaves / 2, CT = 4, WTN = 16 * CT, WTM = 16 * RT, BM = 2 * WTM;
+  constexpr int BN = WTN * WN;
   constexpr int kRing = 4;
   constexpr int SB = (BM + BN) * kStageK;               // bytes of a slot
   // scales: 16 bytes for each of BM rows and then BN columns, or blocks of them
@@ -362,9 +365,9 @@ grouped_tile_kernel(GroupedArgs a) {
   constexpr int L = 2;                                  // fold lag (MFMAs)
   constexpr int kGroup = 4, kGroupM = 8;
   constexpr bool PF = BROWS == 128;                     // scales read a stage ahead
-  static_assert(WTN * WN == BN && RT % kRing == 0 && kDma <= kTail, "tile");
+  static_assert(RT % kRing == 0 && kDma <= kTail, "tile");
   constexpr int kYoung = (kSlots - 2) * (kDma + 1);     // loads younger than the next stage's
-  constexpr int kBatch = kSlots == 3 ? 32 : 128;        // tiles of a workgroup's list
+  constexpr int kBatch = kSlots == 3 || kTileWaves == 4 ? 32 : 128;        // tiles of a workgroup's list
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * SB +
                                                             (kSlots + 1) * kRegion];
   __shared__ int first_tile[BROWS == 128 ? kMaxSpans + 1 : 1];   // spans: row tiles before it
@@ -766,29 +769,33 @@ grouped_tile_kernel(GroupedArgs a) {
 
 }  // namespace
 
-template <int BROWS, int RT, int kSlots>
+template <int BROWS, int RT, int kSlots, int kWaves>
 hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((grouped_tile_kernel<BROWS, RT, kSlots>), dim3(kTileWgs), dim3(kTileThreads), 0,
-                     s, a);
+  hipLaunchKernelGGL((grouped_tile_kernel<BROWS, RT, kSlots, kWaves>), dim3(kCus * 8 / kWaves),
+                     dim3(64 * kWaves), 0, s, a);
   return hipGetLastError();
 }
 
-// Rounds of a CU with tiles of `bm` rows; an expert's last tile of y is about half full.
+// Rounds of the card, `per` workgroups of it, with tiles of bm x bn; an expert's last tile of y is
+// about half full.
 template <int BROWS>
-int64_t rounds(const GroupedArgs& a, int bm) {
+int64_t rounds(const GroupedArgs& a, int64_t bm, int64_t bn, int64_t per) {
   const int64_t m = BROWS == 1 ? a.experts * ((a.N + bm - 1) / bm)
                                : a.rows / bm + (a.experts + 1) / 2;
-  const int64_t n = ((BROWS == 1 ? a.K : a.N) + kBN - 1) / kBN;
-  return (m * n + kTileWgs - 1) / kTileWgs;
+  const int64_t n = ((BROWS == 1 ? a.K : a.N) + bn - 1) / bn;
+  return (m * n + per - 1) / per;
 }
 
-// A round of 128-row tiles takes 5/8 of one of 256-row tiles (both measured: y of 1024 rows of 8
-// experts, 14336 x 4096, 147.4 us either way at 3 rounds to 2; of 4096 rows of 64, 2048 x 1408,
-// 59.4 to 76.8 at 3 to 2; of 32768 rows, 147.7 to 136.8 at 9 to 5; dw of 8 experts of 1024 x 1024 and
-// 1000 rows 22.2 to 31.7 at 1 to 1, of 64 of 512 x 512 and 250 rows 22.1 to 20.5 at 2 to 1).
+// A round of the lower tiles takes 5/8 of one of 256 x 256. Measured, lower to higher in us: y of
+// 1024 rows of 8 experts, 14336 x 4096, 147 to 147 at 3 rounds to 2; of 4096 rows of 64, 2048 x 1408,
+// 59 to 77 at 3 to 2; of 32768 rows, 148 to 137 at 9 to 5. dw of 8 experts, 1024 x 1024 and 1000 rows
+// 22.4 to 31.2 at 1 to 1; of 27, 6272 x 128, 16.1 to 19.6 at 3 to 3; of 8, 2048 x 1024 and 7500 rows
+// 206 to 191 at 2 to 1.
 template <int BROWS>
-bool small_tiles(const GroupedArgs& a) {
-  return 5 * rounds<BROWS>(a, 128) <= 8 * rounds<BROWS>(a, 256);
+bool low_tiles(const GroupedArgs& a) {
+  const int64_t low = BROWS == 1 ? rounds<1>(a, 128, 128, 2 * kCus)
+                                 : rounds<128>(a, 128, 256, kCus);
+  return 5 * low <= 8 * rounds<BROWS>(a, 256, 256, kCus);
 }
 
 // Up to 11 items of a stream a CU take less than a round of tiles (y of 8 experts' 250 rows: 35.1 us
@@ -802,12 +809,12 @@ hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
   if (a.max_rows <= 8) return launch_stream<128, 8, 2>(a, s);
   if (a.rows <= 32 * (int64_t)a.experts || stream_items<128, 32>(a) <= kStreamItems)
     return launch_stream<128, 32, 1>(a, s);
-  return small_tiles<128>(a) ? launch_tiles<128, 4, 3>(a, s) : launch_tiles<128, 8, 2>(a, s);
+  return low_tiles<128>(a) ? launch_tiles<128, 4, 3, 8>(a, s) : launch_tiles<128, 8, 2, 8>(a, s);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
   if (stream_items<1, 32>(a) <= kStreamItems) return launch_stream<1, 32, 1>(a, s);
-  return small_tiles<1>(a) ? launch_tiles<1, 4, 2>(a, s) : launch_tiles<1, 8, 2>(a, s);
+  return low_tiles<1>(a) ? launch_tiles<1, 4, 2, 4>(a, s) : launch_tiles<1, 8, 2, 8>(a, s);
 }
 
 }  // namespace fp8lin

@@ -208,6 +208,41 @@ def test_many_experts(lib, experts):
     check_wgrad(lib, counts, 128, 256)
 
 
+def test_more_tiles_than_a_list(lib):
+    """A workgroup's tiles come in lists of some. A block of K alone has the same float32 products
+    whatever the order, so the forms for many rows and for few have to agree to the bit."""
+    note("grouped: 64 tiles a workgroup")
+    g = torch.Generator("cuda").manual_seed(5)
+    E, N, K, each = 512, 8192, 128, 34
+    x = torch.randint(0, 120, (E * each, K), generator=g, device="cuda", dtype=torch.uint8)
+    w = torch.randint(0, 120, (E, N, K), generator=g, device="cuda", dtype=torch.uint8)
+    sx = torch.rand(E * each, 1, generator=g, device="cuda")
+    sw = torch.rand(E, N // 128, 1, generator=g, device="cuda")
+    off = torch.arange(0, E * each + 1, each, device="cuda", dtype=torch.int32)
+    cnt = torch.full((E,), each, device="cuda", dtype=torch.int32)
+    cnt[7], cnt[300] = 0, 5
+    tiles = lib.fp8_grouped_linear_fwd(x, w, sx, sw, off, cnt)
+    few = lib.fp8_grouped_linear_fwd(x, w, sx, sw, off, cnt, max_rows=8)
+    assert torch.equal(tiles, few) and (tiles != 0).any()
+
+    note("grouped wgrad: 129 tiles a workgroup")
+    E, N, K = 65, 8192, 4096
+    gq = torch.randint(0, 120, (N, E * 128), generator=g, device="cuda", dtype=torch.uint8)
+    xq = torch.randint(0, 120, (K, E * 128), generator=g, device="cuda", dtype=torch.uint8)
+    gs = torch.rand(N, E, generator=g, device="cuda")
+    xs = torch.rand(K, E, generator=g, device="cuda")
+    off = torch.arange(0, E * 128 + 1, 128, device="cuda", dtype=torch.int32)
+    cnt = torch.full((E,), 128, device="cuda", dtype=torch.int32)
+    cnt[64] = 1
+    dw = lib.fp8_grouped_linear_wgrad(gq, xq, gs, xs, off, cnt)
+    for e in (0, 31, 63, 64):
+        r = slice(128 * e, 128 * e + 128)
+        alone = lib.fp8_grouped_linear_wgrad(gq[:, r].contiguous(), xq[:, r].contiguous(),
+                                             gs[:, e:e + 1].contiguous(), xs[:, e:e + 1].contiguous(),
+                                             off[:2], cnt[e:e + 1].clone())
+        assert torch.equal(dw[e:e + 1], alone) and (alone != 0).any()
+
+
 def test_no_rows(lib):
     note("grouped without rows")
     g = torch.Generator().manual_seed(0)
