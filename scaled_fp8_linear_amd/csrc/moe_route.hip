@@ -73,10 +73,10 @@ template <int LANES> __device__ __forceinline__ float lanes_max(float v) {
 template <typename B, B INF> __device__ __forceinline__ B order_key(B b) {
   constexpr B kSign = (B)((B)1 << (8 * sizeof(B) - 1));
   const B mag = (B)(b & (B)~kSign);
-  if (mag > INF) return (B)~(B)0;
-  if (b == (B)(kSign | INF)) return (B)0;
-  if (mag == 0) return kSign;
-  return (b & kSign) ? (B)~b : (B)(b | kSign);
+  B k = (b & kSign) ? (B)~b : (B)(b | kSign);
+  k = mag == 0 ? kSign : k;
+  k = b == (B)(kSign | INF) ? (B)0 : k;
+  return mag > INF ? (B)~(B)0 : k;
 }
 template <typename B> __device__ __forceinline__ B key_bits(B k) {   // of a key that is not 0
   constexpr B kSign = (B)((B)1 << (8 * sizeof(B) - 1));
@@ -160,14 +160,17 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
   using Bits = typename Logit<T>::Bits;
   constexpr bool k16 = sizeof(T) == 2;
   constexpr int kTokens = kRouteThreads / G;                    // of a step
-  __shared__ Part sums[kRouteWaves][G * NV];
+  __shared__ float sums[kRouteWaves][G * NV];
+  __shared__ int s_cnt[G * NV];                                 // pairs of an expert
+  __shared__ int s_choice[k16 ? 1 : kTokens][k16 ? 1 : L::kMaxK];   // a token's experts
   __shared__ float s_z[kRouteWaves], s_red[16];
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, gl = lane % G;
   float psum[NV];
-  int cnt[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) psum[i] = 0.f, cnt[i] = 0;
+  for (int i = 0; i < NV; ++i) psum[i] = 0.f;
   float zsum = 0.f;
+  for (int e = t; e < G * NV; e += kRouteThreads) s_cnt[e] = 0;
+  __syncthreads();
 
   // whole waves stay in the loop, so that the lane exchanges see every lane
   for (int64_t base = (int64_t)blockIdx.x * kTokens; base < tokens;
@@ -184,42 +187,56 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
       key[i] = order_key<Bits, Logit<T>::kInf>(__builtin_bit_cast(Bits, raw[i]));
       if (k16 && key[i]) key[i] = key[i] << 16 | (uint32_t)(0xFFFF - L::expert(gl, i));
     }
-    float top = -INFINITY;
-    int rec_e[L::kSlots];                      // this lane's choices j = s G + gl
-    float rec_v[L::kSlots];
+    uint32_t rec[L::kSlots], first = 0u;       // keys of this lane's choices j = s G + gl
 #pragma unroll
-    for (int s = 0; s < L::kSlots; ++s) rec_e[s] = -1, rec_v[s] = -INFINITY;
+    for (int s = 0; s < L::kSlots; ++s) rec[s] = 0u;
+    uint32_t above = 0u;                       // 16 bits: the last choice, keys below it are left
     for (int j = 0; j < k; ++j) {
-      uint32_t m = key[0];
+      // modulo 2^32 a key k < above has k - above >= 2^32 - above, one of at least `above` less
+      uint32_t m = key[0] - above;
 #pragma unroll
-      for (int i = 1; i < NV; ++i) m = max(m, key[i]);
-      const uint32_t gm = lanes_max_u32<G>(m);
-      int e;
-      float v;
+      for (int i = 1; i < NV; ++i) m = max(m, key[i] - above);
+      const uint32_t gm = lanes_max_u32<G>(m) + above;
+      if (j == 0) first = gm;
+#pragma unroll
+      for (int s = 0; s < L::kSlots; ++s)
+        if (j == s * G + gl) rec[s] = gm;
       if constexpr (k16) {
-        e = 0xFFFF - (int)(gm & 0xFFFFu);
-        v = to_f32(__builtin_bit_cast(T, key_bits((Bits)(gm >> 16))));
+        above = max(gm, 1u);
       } else {
-        // the lowest expert among the lanes that hold the maximum
+        // the lane's lowest expert with the maximum; where lanes share it, only the lowest of them
         uint32_t low = 0u;
 #pragma unroll
         for (int i = NV - 1; i >= 0; --i)
           if (key[i] == gm) low = (uint32_t)(0xFFFF - L::expert(gl, i));
-        e = 0xFFFF - (int)lanes_max_u32<G>(low);
-        v = __uint_as_float(key_bits(gm));
-      }
-      if (gm == 0) e = -1, v = -INFINITY;
-      if (j == 0) top = v;
+        if (__builtin_popcountll(__ballot(low != 0u)) != 64 / G)
+          low = lanes_max_u32<G>(low) == low ? low : 0u;
+        if (low != 0u && gm != 0u) s_choice[t / G][j] = 0xFFFF - (int)low;
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const bool mine = k16 ? key[i] == gm && gm != 0 : e == L::expert(gl, i);
-        if (mine) key[i] = 0u;
-        cnt[i] += mine ? 1 : 0;
+        for (int i = 0; i < NV; ++i)
+          key[i] = low == (uint32_t)(0xFFFF - L::expert(gl, i)) ? 0u : key[i];
       }
-#pragma unroll
-      for (int s = 0; s < L::kSlots; ++s)
-        if (j == s * G + gl) rec_e[s] = e, rec_v[s] = v;
     }
+    if constexpr (!k16) wave_lds_fence();
+    auto value = [](uint32_t q) __attribute__((always_inline)) {       // of a key of the loop
+      if (q == 0u) return -INFINITY;
+      if constexpr (k16) return to_f32(__builtin_bit_cast(T, key_bits((Bits)(q >> 16))));
+      else return __uint_as_float(key_bits(q));
+    };
+    const float top = value(first);
+    int rec_e[L::kSlots];
+    float rec_v[L::kSlots];
+#pragma unroll
+    for (int s = 0; s < L::kSlots; ++s) {
+      rec_v[s] = value(rec[s]);
+      rec_e[s] = -1;
+      if (rec[s] != 0u) {
+        if constexpr (k16) rec_e[s] = 0xFFFF - (int)(rec[s] & 0xFFFFu);
+        else rec_e[s] = s_choice[t / G][s * G + gl];
+        atomicAdd(&s_cnt[rec_e[s]], 1);
+      }
+    }
+    if constexpr (!k16) wave_lds_fence();      // read before the next step's choices are written
     const bool none = top == -INFINITY;        // no expert left (not so for NaN)
     float total = 0.f, wsum = 0.f, w[L::kSlots];
 #pragma unroll
@@ -257,11 +274,8 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
-    for (int off = 32; off >= G; off >>= 1) {
-      psum[i] += __shfl_xor(psum[i], off, 64);
-      cnt[i] += __shfl_xor(cnt[i], off, 64);
-    }
-    if (lane < G) sums[wave][L::expert(gl, i)] = {psum[i], cnt[i]};
+    for (int off = 32; off >= G; off >>= 1) psum[i] += __shfl_xor(psum[i], off, 64);
+    if (lane < G) sums[wave][L::expert(gl, i)] = psum[i];
   }
   zsum = lanes_sum<64>(zsum);
   if (lane == 0) s_z[wave] = zsum;
@@ -271,9 +285,9 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
   for (int w = 0; w < kRouteWaves; ++w) z += s_z[w];
   float cp = 0.f;
   for (int e = t; e < E; e += kRouteThreads) {
-    Part s = {0.f, 0};
+    Part s = {0.f, s_cnt[e]};
 #pragma unroll
-    for (int w = 0; w < kRouteWaves; ++w) s.p += sums[w][e].p, s.c += sums[w][e].c;
+    for (int w = 0; w < kRouteWaves; ++w) s.p += sums[w][e];
     if (gridDim.x == 1) {
       counts[e] = s.c;
       cp += (float)s.c * s.p;
