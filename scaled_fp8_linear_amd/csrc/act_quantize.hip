@@ -16,8 +16,8 @@
 // e4m3(v / scale). All values are float32 until then. The scale is m times the rounded 1/448 and
 // the multiplier the hardware's reciprocal of it: both within 2 units in the last place, against
 // codes that keep 3 bits; two correctly rounded divisions a tile would be some 30 instructions in
-// every lane. A product may so exceed 448 by 2^-21 of it, which still rounds to the code of 448. A NaN is coded as NaN and does not enter m; an infinity makes
-// its tile's scale infinite.
+// every lane. A product may so exceed 448 by 2^-21 of it, which still rounds to the code of 448. A
+// NaN is coded as NaN and does not enter m; an infinity makes its tile's scale infinite.
 //
 // A workgroup owns 128 x 128 elements of a: 512 lanes of 4 rows x 8 columns. Row maxima are DPP
 // steps over the 16 lanes of a row; column maxima go over the lanes and then through LDS, as do
@@ -432,8 +432,8 @@ hipError_t launch_act_quantize_bwd(const ActArgs& a, hipStream_t s) {
     using T = decltype(tag);
     hipLaunchKernelGGL((act_quantize_bwd_kernel<T, decltype(act)::value, decltype(gated)::value>),
                        dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kAThreads), 0, s,
-                       static_cast<const T*>(a.x), a.ldx, a.rows, a.valid, a.cols, a.hq, a.hscale, a.q, a.scale, a.q_t,
-                       a.scale_t, static_cast<T*>(a.dh), (int)tiles_c);
+                       static_cast<const T*>(a.x), a.ldx, a.rows, a.valid, a.cols, a.hq, a.hscale,
+                       a.q, a.scale, a.q_t, a.scale_t, static_cast<T*>(a.dh), (int)tiles_c);
     return hipGetLastError();
   });
 }

@@ -21,6 +21,7 @@ namespace fp8lin {
 namespace {
 
 constexpr int kBlock = 128;                  // codes per scale
+constexpr int kCus = 256;                    // compute units
 
 // The rows of expert e: first, one past the last, one past its padding.
 struct Span { int64_t first, end, next; };
@@ -279,7 +280,7 @@ grouped_stream_kernel(GroupedArgs a) {
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }
-  // rows of nobody: the waves, which are never fewer than the spans, share those that have some
+  // rows of nobody: the waves share the spans that have some
   if constexpr (!kGrad) {
     const int me = (int)blockIdx.x * kStreamWaves + wave, waves = (int)gridDim.x * kStreamWaves;
     for (int base = 0; base < spans; base += 64) {
@@ -287,34 +288,39 @@ grouped_stream_kernel(GroupedArgs a) {
       spans_from(z, base);
       const bool has = z.l.next > z.l.end;
       const uint64_t m = __ballot(has);
-      const int with = __builtin_popcountll(m);
-      if (with == 0) continue;
+      const int with = __builtin_popcountll(m), step = min(with, waves);
       const int rank = __builtin_popcountll(m & ((1ull << lane) - 1));
-      const int from = __builtin_ctzll(__ballot(has && rank == me % with));
-      const int end = __builtin_amdgcn_readlane((int)z.l.end, from);
-      const int next = __builtin_amdgcn_readlane((int)z.l.next, from);
-      const int64_t sharers = (waves - me % with + with - 1) / with;
-      uint4* const y = reinterpret_cast<uint4*>(a.y + (int64_t)end * a.N);
-      const int64_t pieces = (int64_t)(next - end) * (a.N / 8);
-      for (int64_t q = me / with * 64 + lane; q < pieces; q += sharers * 64)
-        y[q] = make_uint4(0, 0, 0, 0);
+      if (with == 0) continue;
+      const int64_t sharers = (waves - me % step + step - 1) / step;
+      for (int i = me % step; i < with; i += step) {
+        const int from = __builtin_ctzll(__ballot(has && rank == i));
+        const int end = __builtin_amdgcn_readlane((int)z.l.end, from);
+        const int next = __builtin_amdgcn_readlane((int)z.l.next, from);
+        uint4* const y = reinterpret_cast<uint4*>(a.y + (int64_t)end * a.N);
+        const int64_t pieces = (int64_t)(next - end) * (a.N / 8);
+        for (int64_t q = me / step * 64 + lane; q < pieces; q += sharers * 64)
+          y[q] = make_uint4(0, 0, 0, 0);
+      }
     }
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");   // no load may land after exit
 }
 
-// Items of 32 columns by XR rows: with each expert's last one about half full in y.
-template <int BROWS, int XR>
-int64_t stream_items(const GroupedArgs& a) {
-  const int64_t rows = BROWS == 1 ? a.experts * (a.K / XR) : a.rows / XR + (a.experts + 1) / 2;
-  return a.N / 32 * rows;
+// Pieces of bm rows that the output's rows come in, with an expert's last one about half full. In y,
+// rows that are a multiple of 128 are taken to have room for every expert's padding to that, which
+// nobody multiplies; `max_rows` may say that there are less.
+template <int BROWS>
+int64_t row_pieces(const GroupedArgs& a, int64_t bm) {
+  if (BROWS == 1) return a.experts * ((a.N + bm - 1) / bm);
+  const int64_t live = a.rows % 128 ? a.rows : max(a.rows - 127 * (int64_t)a.experts, a.rows / 128);
+  return min(live / bm + (a.experts + 1) / 2, a.experts * ((a.max_rows + bm - 1) / bm));
 }
 
 template <int BROWS, int XR, int D>
 hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
-  constexpr int64_t kWgs = XR == 8 ? 512 : 768;
-  hipLaunchKernelGGL((grouped_stream_kernel<BROWS, XR, D>),
-                     dim3((unsigned)min(max(stream_items<BROWS, XR>(a), (int64_t)1), kWgs)),
+  constexpr int64_t kWgs = XR == 8 ? 2 * kCus : 3 * kCus;
+  const int64_t items = a.N / 32 * (BROWS == 1 ? a.experts * (a.K / XR) : (a.rows + XR - 1) / XR);
+  hipLaunchKernelGGL((grouped_stream_kernel<BROWS, XR, D>), dim3((unsigned)min(items, kWgs)),
                      dim3(kStreamThreads), 0, s, a);
   return hipGetLastError();
 }
@@ -345,7 +351,6 @@ hipError_t launch_stream(const GroupedArgs& a, hipStream_t s) {
 // stages for the last tile's stores costs a further 9 to 12 % (y of 16384 rows of 8 experts, 14336 x
 // 4096: 913 us, 2107 TFLOP/s, 856 in a copy without the stores; dw 1141, 1036 without).
 constexpr int kStageK = 128;
-constexpr int kCus = 256;
 
 template <int BROWS, int RT, int kSlots, int kTileWaves>
 __global__ void __launch_bounds__(64 * kTileWaves, 8 / kTileWaves)
@@ -776,14 +781,11 @@ hipError_t launch_tiles(const GroupedArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Rounds of the card, `per` workgroups of it, with tiles of bm x bn; an expert's last tile of y is
-// about half full.
+// Rounds of the card, `per` workgroups of it, with tiles of bm x bn.
 template <int BROWS>
 int64_t rounds(const GroupedArgs& a, int64_t bm, int64_t bn, int64_t per) {
-  const int64_t m = BROWS == 1 ? a.experts * ((a.N + bm - 1) / bm)
-                               : a.rows / bm + (a.experts + 1) / 2;
   const int64_t n = ((BROWS == 1 ? a.K : a.N) + bn - 1) / bn;
-  return (m * n + per - 1) / per;
+  return (row_pieces<BROWS>(a, bm) * n + per - 1) / per;
 }
 
 // A round of the lower tiles takes 5/8 of one of 256 x 256. Measured, lower to higher in us: y of
@@ -791,29 +793,37 @@ int64_t rounds(const GroupedArgs& a, int64_t bm, int64_t bn, int64_t per) {
 // 59 to 77 at 3 to 2; of 32768 rows, 148 to 137 at 9 to 5. dw of 8 experts, 1024 x 1024 and 1000 rows
 // 22.4 to 31.2 at 1 to 1; of 27, 6272 x 128, 16.1 to 19.6 at 3 to 3; of 8, 2048 x 1024 and 7500 rows
 // 206 to 191 at 2 to 1.
+//
+// Where no expert has more than 256 rows a tile of 256 is at most one an expert's, and never the
+// faster one (8 experts, 14336 x 4096, 64 rows each: 127 us to 140).
 template <int BROWS>
 bool low_tiles(const GroupedArgs& a) {
+  if (BROWS != 1 && a.max_rows <= 256) return true;
   const int64_t low = BROWS == 1 ? rounds<1>(a, 128, 128, 2 * kCus)
                                  : rounds<128>(a, 128, 256, kCus);
   return 5 * low <= 8 * rounds<BROWS>(a, 256, 256, kCus);
 }
 
-// Up to 11 items of a stream a CU take less than a round of tiles (y of 8 experts' 250 rows: 35.1 us
+// Less than 10 items of a stream a CU take less than a round of tiles (y of 8 experts' 250 rows: 35.1 us
 // to 38.7 at 1024 x 4096, 2112 items, 58.2 to 40.4 at 2048 x 4096, 4224; dw of 8 experts, 512 x 512,
 // 1000 rows: 14.4 to 20.6, 2048 items; of 4, 1024 x 1024, 4000 rows: 66.0 to 53.8, 4096).
-constexpr int64_t kStreamItems = 11 * 256;
+template <int BROWS>
+bool few_items(const GroupedArgs& a) {
+  const int64_t columns = (BROWS == 1 ? a.K : a.N) / 32;
+  return row_pieces<BROWS>(a, 32) * columns < 10 * (int64_t)kCus;
+}
 
-// Where an expert has up to 32 rows on average, a stream reads the weights about once, and faster
-// (8 experts, 14336 x 4096, 16 rows each: 102 us to 122).
+// Where no expert has more than 64 rows a stream reads the weights about once, and faster (8 experts,
+// 14336 x 4096, 16 rows on average: 102 us to 122; 22 of 3456 x 384, 21 rows: 13.8 to 18.6).
 hipError_t launch_grouped_gemm(const GroupedArgs& a, hipStream_t s) {
   if (a.max_rows <= 8) return launch_stream<128, 8, 2>(a, s);
-  if (a.rows <= 32 * (int64_t)a.experts || stream_items<128, 32>(a) <= kStreamItems)
+  if (a.max_rows <= 64 || a.rows <= 32 * (int64_t)a.experts || few_items<128>(a))
     return launch_stream<128, 32, 1>(a, s);
   return low_tiles<128>(a) ? launch_tiles<128, 4, 3, 8>(a, s) : launch_tiles<128, 8, 2, 8>(a, s);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedArgs& a, hipStream_t s) {
-  if (stream_items<1, 32>(a) <= kStreamItems) return launch_stream<1, 32, 1>(a, s);
+  if (few_items<1>(a)) return launch_stream<1, 32, 1>(a, s);
   return low_tiles<1>(a) ? launch_tiles<1, 4, 2, 4>(a, s) : launch_tiles<1, 8, 2, 8>(a, s);
 }
 

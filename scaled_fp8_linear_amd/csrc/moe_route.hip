@@ -11,12 +11,18 @@
 // A logit of -inf is a masked expert: never chosen, p = 0. A row without any other has idx -1,
 // w 0, lse -inf, and adds nothing to P and to the losses. NaN ranks above every number.
 //
-// G consecutive lanes hold a token's logits, NV each (expert = lane NV + i), so the sums and
-// maxima are DPP steps of log2 G. A choice is the maximum of the unsigned keys that order like
-// the logits; for 16-bit types the key's lower half is the complement of the expert, which makes
-// the same maximum also break ties. The counts and sums of p stay in the lanes that own the
-// expert until a workgroup's tokens are done; the workgroups' partial sums are added by a second
-// launch in a fixed order (no atomics: the same inputs give the same bits).
+// G consecutive lanes hold a token's logits, NV each, so the sums and maxima are DPP steps of log2 G.
+// A choice is the maximum of the unsigned keys that order like the logits; for 16-bit types the key's
+// lower half is the complement of the expert, which makes the same maximum also break ties. The sums
+// of p stay in the lanes that own the expert until a workgroup's tokens are done, and pairs are counted
+// in LDS; the workgroups' partial sums are added by a second launch in a fixed order (integer atomics
+// alone: the same inputs give the same bits).
+//
+// What bounds it: up to some 2000 tokens the launches (64 tokens, 2 of 8 experts 4.6 us; two launches
+// 8.8). Beyond, the instructions of the choices rather than memory: 32768 tokens, 8 of 256, bf16 27.0
+// us, of which 6.4 are the bytes' and a launch's. A lane so keeps its keys unchanged (34 us when each
+// choice took its key out and counted the pair in registers), and a token has few lanes (the gradient,
+// which has no choices to make, has more).
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
