@@ -265,6 +265,9 @@ def expert_mlp(xs, w_up, w_down, plan: ExpertPlan, act: str = "silu", gated: boo
     for t, name in ((xs, "xs"), (w_up, "w_up"), (w_down, "w_down")):
         if t.dtype != torch.bfloat16:
             raise ValueError(f"{name} must be bfloat16, got {t.dtype}")
+    least = _abi.fp8_moe_rows(*plan.slot.shape, e, 128)
+    if xs.shape[0] < least:         # of another multiple: blocks of 128 rows would mix experts
+        raise ValueError(f"the plan has {xs.shape[0]} rows, with multiple=128 it has {least}")
     return _ExpertMlpFn.apply(xs.contiguous(), w_up, w_down, plan.offsets, plan.counts, act, gated,
                               plan.slot.shape[0])
 

@@ -217,6 +217,8 @@ def test_module_checks(lib):
     bad("w_up has shape", m.expert_mlp, xs, block.w_up[:, :256], block.w_down, plan)
     bad("the plan is for", m.expert_mlp, xs, block.w_up[:3], block.w_down[:3], plan)
     bad("bfloat16", m.expert_mlp, xs.float(), block.w_up, block.w_down, plan)
+    # 3 tokens to 2 of 4 experts padded to 128 need 512 rows: these were padded to less
+    bad("with multiple=128 it has 512", m.expert_mlp, xs, block.w_up, block.w_down, plan)
 
 
 # ---------------------------------------------------------------------- the oracles
