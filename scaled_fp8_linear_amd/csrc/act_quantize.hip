@@ -22,6 +22,10 @@
 // A workgroup owns 128 x 128 elements of a: 512 lanes of 4 rows x 8 columns. Row maxima are DPP
 // steps over the 16 lanes of a row; column maxima go over the lanes and then through LDS, as do
 // the transposed codes (4 rows in a dword).
+//
+// What bounds it: memory. 17408 x 14336 bf16 gated: forward 363 us, 2.0 GB (5.5 TB/s), backward
+// 424 us, 2.0 GB (4.7 TB/s; it writes twice what it reads). A token of 128 padding rows 5.4 us, most
+// of it the call.
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
@@ -235,17 +239,16 @@ __device__ __forceinline__ void emit_cols(const float (&v)[kARows][8], const Pla
   }
 }
 
-// Workgroups go round-robin over the 8 XCDs. CHUNKS: an XCD takes a run of tiles, so that the
-// neighbours whose scales share a line write it in one L2. The backward, which writes twice what it
-// reads, gains by it (17408 x 14336 gated: 462 us without, 433 with), the forward loses (366, 374).
-template <bool CHUNKS>
+// Workgroups go round-robin over the 8 XCDs. An XCD takes runs of 8 tiles, so that the neighbours
+// whose scales share 32 bytes write them in one L2 (17408 x 14336 gated, us: single tiles 370 forward
+// and 462 backward, runs of 8 364 and 423, of 16 and 32 360 and 431, an eighth of all 374 and 433;
+// 80 tiles and 224 take the same either way).
+constexpr int kRun = 8;
+int64_t act_workgroups(int64_t tiles) { return (tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun); }
 __device__ __forceinline__ bool place(Place& at, int64_t rows, int tiles_c, int64_t& tc) {
-  int id = (int)blockIdx.x;
-  if constexpr (CHUNKS) {
-    const int total = (int)((rows + kAT - 1) / kAT) * tiles_c, per = (total + 7) / 8;
-    id = (id & 7) * per + (id >> 3);
-    if (((int)blockIdx.x >> 3) >= per || id >= total) return false;
-  }
+  const int total = (int)((rows + kAT - 1) / kAT) * tiles_c, b = (int)blockIdx.x;
+  const int id = b / (8 * kRun) * (8 * kRun) + (b & 7) * kRun + (b >> 3) % kRun;
+  if (id >= total) return false;
   const int tr = id / tiles_c;
   at.rows = rows;
   at.tr = tr;
@@ -266,7 +269,7 @@ act_quantize_kernel(const T* __restrict__ h, int64_t ldh, int64_t rows, int64_t 
   __shared__ __attribute__((aligned(16))) Lds lds;
   int64_t tc;
   Place at;
-  place<false>(at, rows, tiles_c, tc);
+  if (!place(at, rows, tiles_c, tc)) return;
   float v[kARows][8], u[kARows][8];
   const T* p = h + at.row * ldh + tc * kAT + 8 * at.cc;
   if (at.row0 + kAT <= valid) {
@@ -324,7 +327,7 @@ act_quantize_bwd_kernel(const T* __restrict__ da, int64_t ldda, int64_t rows, in
   __shared__ __attribute__((aligned(16))) Lds lds;
   int64_t tc;
   Place at;
-  if (!place<true>(at, rows, tiles_c, tc)) return;
+  if (!place(at, rows, tiles_c, tc)) return;
   const int64_t col = tc * kAT + 8 * at.cc;
   const int64_t width = GATED ? 2 * cols : cols, blocks = width / kAT;
   float v[kARows][8], u[kARows][8];            // first da and the values of u, then dg and du
@@ -419,9 +422,9 @@ hipError_t launch_act_quantize(const ActArgs& a, hipStream_t s) {
   return by_act(a, [&](auto tag, auto act, auto gated) {
     using T = decltype(tag);
     hipLaunchKernelGGL((act_quantize_kernel<T, decltype(act)::value, decltype(gated)::value>),
-                       dim3((unsigned)tiles), dim3(kAThreads), 0, s, static_cast<const T*>(a.x),
-                       a.ldx, a.rows, a.valid, a.cols, a.q, a.scale, a.q_t, a.scale_t, a.hq,
-                       a.hscale, (int)tiles_c);
+                       dim3((unsigned)act_workgroups(tiles)), dim3(kAThreads), 0, s,
+                       static_cast<const T*>(a.x), a.ldx, a.rows, a.valid, a.cols, a.q, a.scale,
+                       a.q_t, a.scale_t, a.hq, a.hscale, (int)tiles_c);
     return hipGetLastError();
   });
 }
@@ -431,7 +434,7 @@ hipError_t launch_act_quantize_bwd(const ActArgs& a, hipStream_t s) {
   return by_act(a, [&](auto tag, auto act, auto gated) {
     using T = decltype(tag);
     hipLaunchKernelGGL((act_quantize_bwd_kernel<T, decltype(act)::value, decltype(gated)::value>),
-                       dim3((unsigned)((tiles + 7) / 8 * 8)), dim3(kAThreads), 0, s,
+                       dim3((unsigned)act_workgroups(tiles)), dim3(kAThreads), 0, s,
                        static_cast<const T*>(a.x), a.ldx, a.rows, a.valid, a.cols, a.hq, a.hscale,
                        a.q, a.scale, a.q_t, a.scale_t, static_cast<T*>(a.dh), (int)tiles_c);
     return hipGetLastError();
