@@ -59,11 +59,11 @@ constexpr int kMaxSpans = kMoeMaxExperts + 2;
 // enough); else the way from L2 (64 rows of 128 codes for 32 x 32 sums, near 12 TB/s).
 //
 // XR 8, D 2, two workgroups a CU: up to 8 rows an expert. A slot holds 8 rows of x; lanes of rows
-// past them multiply another row's codes, for nobody. XR 32, D 1, three workgroups a CU: the rest.
-// One block under way a wave is enough there (12 waves a CU, 4.9 KB each): with D 2 and one
-// workgroup a CU 8192 rows of 4 experts took 21.4 us instead of 21.3 at 512 x 512, but 17.6 instead
-// of 16.4 at 1024 x 4096 with 75 rows an expert and 20.3 instead of 14.5 at 1024 x 1024 with 250;
-// with 16 rows an item 42.9 instead of 35.1 at 1024 x 4096 with 250 rows.
+// past them multiply another row's codes, for nobody. XR 32, D 1, three workgroups a CU: the rest
+// (also for a token it reads the weights of 4096 x 14336 in 32.8 us to 27.5). One block under way a
+// wave is enough there (12 waves a CU, 8.4 KB each): with two and one workgroup a CU 17.6 us instead
+// of 16.4 at 1024 x 4096 with 75 rows an expert, 20.3 instead of 14.5 at 1024 x 1024 with 250; with
+// 16 rows an item 42.9 instead of 35.1 at 1024 x 4096 with 250 rows.
 constexpr int kStreamWaves = 4, kStreamThreads = 64 * kStreamWaves;
 
 template <int BROWS, int XR, int D>
