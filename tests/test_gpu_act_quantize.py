@@ -227,3 +227,27 @@ def test_large_tensor_against_slices(lib):
         assert torch.equal(dpart[0], out[0][r]) and torch.equal(dpart[2], out[2][:, r])
         assert torch.equal(dpart[3], out[3][:, i // 128:i // 128 + 1])
     assert (q[128:256] == 0).all() and (out[0][256:512] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [300, 384])
+def test_many_tiles_are_their_columns_calls(lib, rows):
+    """Tiles are independent: 210 of them in one call, and in calls of a few columns each."""
+    note(f"act_quantize {rows} rows of 70 tiles")
+    g = torch.Generator("cuda").manual_seed(rows)
+    cols, part, train = 70 * 128, 5 * 128, rows % 128 == 0
+    h = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    da = torch.randn(rows, cols, generator=g, device="cuda", dtype=torch.bfloat16)
+    whole = lib.fp8_act_quantize(h, "gelu", False, want_q_t=train, want_checkpoint=True)
+    back = lib.fp8_act_quantize_bwd(da, whole[4], whole[5], "gelu", False, want_q=True,
+                                    want_q_t=train, want_dh=True)
+    for c in range(0, cols, part):
+        s, st = slice(c, c + part), slice(c // 128, (c + part) // 128)
+        few = lib.fp8_act_quantize(h[:, s], "gelu", False, want_q_t=train, want_checkpoint=True)
+        fewb = lib.fp8_act_quantize_bwd(da[:, s], few[4], few[5], "gelu", False, want_q=True,
+                                        want_q_t=train, want_dh=True)
+        for got, at in ((whole, few), (back, fewb)):
+            assert torch.equal(got[0][:, s], at[0]) and torch.equal(got[1][:, st], at[1])
+            if train:
+                assert torch.equal(got[2][s], at[2]) and torch.equal(got[3][s], at[3])
+        assert torch.equal(whole[4][:, s], few[4]) and torch.equal(whole[5][:, st], few[5])
+        assert torch.equal(back[4][:, s], fewb[4])
