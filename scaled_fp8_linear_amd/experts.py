@@ -92,18 +92,25 @@ class LayerNorm(torch.nn.Module):
         return layer_norm(x, self.weight, self.bias, self.eps)
 
 
-class ExpertPlan(NamedTuple):
-    """Where every (token, choice) pair goes; the index tensors of fp8_moe_sort, on the device."""
+class _PlanTensors(NamedTuple):
     slot: torch.Tensor          # int32 [tokens, topk]: the pair's row, -1: dropped
     source: torch.Tensor        # int32 [rows]: the row's pair, -1: padding
     counts: torch.Tensor        # int32 [experts]
     offsets: torch.Tensor       # int32 [experts + 1]: the experts' first rows
 
 
+class ExpertPlan(_PlanTensors):
+    """Where every (token, choice) pair goes; the four index tensors of fp8_moe_sort, on the device.
+    ``multiple`` is what the plan was made with, None for a plan made of the tensors alone."""
+    multiple = None
+
+
 def expert_plan(expert_idx, experts: int, multiple: int = 16) -> ExpertPlan:
     """Sort the pairs of expert_idx [tokens, topk] (int32 or int64, outside [0, experts):
     dropped) by expert, every expert's rows padded to a multiple of ``multiple``."""
-    return ExpertPlan(*_abi.fp8_moe_sort(expert_idx, experts, multiple))
+    plan = ExpertPlan(*_abi.fp8_moe_sort(expert_idx, experts, multiple))
+    plan.multiple = multiple
+    return plan
 
 
 class _DispatchFn(torch.autograd.Function):
@@ -243,12 +250,28 @@ class _ExpertMlpFn(torch.autograd.Function):
         return dx, dup, ddown, None, None, None, None, None
 
 
+def _check_whole_blocks(plan: ExpertPlan):
+    """Refuse a plan whose experts do not begin at multiples of 128 rows. The row count cannot tell
+    (200 pairs of 2 experts take 384 rows with multiple 96 and with 128), so without the plan's
+    multiple the offsets are read back."""
+    if plan.multiple is not None:
+        whole = plan.multiple % 128 == 0
+    elif plan.offsets.is_cuda and torch.cuda.is_current_stream_capturing():
+        raise ValueError("a plan that expert_plan did not make cannot be checked during a capture")
+    else:
+        whole = not (plan.offsets % 128).any().item()
+    if not whole:
+        raise ValueError("an expert of the plan does not begin at a multiple of 128 rows: blocks of "
+                         "128 rows would mix experts (expert_plan with multiple=128)")
+
+
 def expert_mlp(xs, w_up, w_down, plan: ExpertPlan, act: str = "silu", gated: bool = True):
     """Every expert's two linears with the activation between them, on its rows of xs [rows, cols]
     (bf16, sorted by a plan with multiple 128), by the block recipe and without reading the row
     counts back: act(xs W_up^T) W_down^T, or with ``gated`` act(g) u of [g | u] = xs W_up^T. w_up
     [experts, hidden or 2 hidden, cols] and w_down [experts, cols, hidden] are bf16, cols and hidden
-    multiples of 128. Rows of no expert give 0. For the backward the activation's input is kept in 8
+    multiples of 128. The offsets of a plan that expert_plan did not make are read back once to check
+    that they are multiples of 128. Rows of no expert give 0. For the backward the activation's input is kept in 8
     bits. The gradient of ys has to be finite in padding rows (expert_combine's is 0 there)."""
     xs = _as_rows(xs)
     e, cols, hidden = w_down.shape
@@ -268,6 +291,7 @@ def expert_mlp(xs, w_up, w_down, plan: ExpertPlan, act: str = "silu", gated: boo
     least = _abi.fp8_moe_rows(*plan.slot.shape, e, 128)
     if xs.shape[0] < least:         # of another multiple: blocks of 128 rows would mix experts
         raise ValueError(f"the plan has {xs.shape[0]} rows, with multiple=128 it has {least}")
+    _check_whole_blocks(plan)
     return _ExpertMlpFn.apply(xs.contiguous(), w_up, w_down, plan.offsets, plan.counts, act, gated,
                               plan.slot.shape[0])
 
