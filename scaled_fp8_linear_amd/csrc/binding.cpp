@@ -1,17 +1,17 @@
 // CPython binding of the row operators (layer norm, router, expert exchange, activation) and of the
-// experts' products: the checks of tensors,
-// their addresses, and the call of the C entry point, in one native call. For one token the
-// kernels take 3 us and their launch 2.7 us of host time; the same checks in Python took 3.4
-// us more. Entry points come in as addresses (bind), so the library is loaded once, elsewhere.
+// experts' products: the checks of tensors, their addresses, and the call of the C entry point, in
+// one native call. For one token the kernels take 3 us and their launch 2.7 us of host time; the
+// same checks in Python took 3.4 us more. Entry points come in as addresses (bind), so the library
+// is loaded once, elsewhere.
 //
 // Every function raises ValueError before anything is enqueued if a tensor does not fit, and
 // the binding's own error for a status other than 0. Outputs that are None and wanted are
-// allocated by the caller's function (bind's "new"), in the pool of the stream that writes them.
+// allocated by torch in the call, in the pool of the stream that writes them: by at::empty on the
+// current stream, by the caller's function (bind's "new") on one that was passed.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
-#include <c10/core/Allocator.h>
 #include <c10/core/TensorImpl.h>
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -215,29 +215,6 @@ void* launch_stream(const at::Tensor& t, PyObject* stream) {
   return p;
 }
 
-// A dense tensor of the current device (the operands') in `storage`, at `offset` bytes. Made without
-// torch's dispatcher, which takes longer for a small output (0.8 us) than the rest of its call.
-at::Tensor in_storage(c10::Storage storage, int64_t offset, at::IntArrayRef shape,
-                      at::ScalarType dtype) {
-  const auto type = c10::scalarTypeToTypeMeta(dtype);
-  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
-      std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA), type);
-  t.unsafeGetTensorImpl()->set_storage_offset(offset / (int64_t)type.itemsize());
-  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
-  return t;
-}
-// torch's allocator of device memory, as one of its tensors names it.
-c10::Allocator* device_allocator(const at::Tensor& like) {
-  static c10::Allocator* const a =
-      at::empty({1}, like.options().dtype(at::kByte).requires_grad(false)).storage().allocator();
-  if (!a) throw std::runtime_error("torch's device tensors name no allocator");
-  return a;
-}
-c10::Storage new_storage(int64_t bytes, const at::Tensor& like) {
-  c10::Allocator* const a = device_allocator(like);
-  return c10::Storage(c10::Storage::use_byte_size_t(), (size_t)bytes, a->allocate((size_t)bytes), a,
-                      /*resizable=*/true);
-}
 int64_t bytes_of(at::IntArrayRef shape, at::ScalarType dtype) {
   int64_t n = (int64_t)c10::elementSize(dtype);
   for (int64_t s : shape) n *= s;
@@ -262,8 +239,7 @@ struct Out {
             bool wanted = true) {
     if (o == Py_None && wanted) {
       if (stream == Py_None) {
-        hold(THPVariable_Wrap(in_storage(new_storage(bytes_of(shape, dtype), like), 0, shape,
-                                         dtype)));
+        hold(THPVariable_Wrap(at::empty(shape, like.options().dtype(dtype).requires_grad(false))));
       } else {
         Ref sh(PyTuple_New((Py_ssize_t)shape.size()));
         for (size_t i = 0; i < shape.size(); ++i)
@@ -277,8 +253,20 @@ struct Out {
   PyObject* take() { PyObject* r = o; o = nullptr; return r; }
 };
 
+// A dense tensor of `storage`, at `offset` bytes; a tensor of its own rather than a view of the one
+// that was allocated.
+at::Tensor in_storage(c10::Storage storage, int64_t offset, at::IntArrayRef shape,
+                      at::ScalarType dtype) {
+  const auto type = c10::scalarTypeToTypeMeta(dtype);
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(
+      std::move(storage), c10::DispatchKeySet(c10::DispatchKey::CUDA), type);
+  t.unsafeGetTensorImpl()->set_storage_offset(offset / (int64_t)type.itemsize());
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
+}
+
 // New outputs in one allocation, or, where the caller gave one of them, its stream or more than
-// `most` bytes, in one each. An allocation is 0.4 us of host time: of a small call's time the outputs
+// `most` bytes, in one each. An allocation is 0.8 us of host time: of a small call's time the outputs
 // are a good part, and share one up to kShared bytes in all. Larger ones do not, so that keeping one
 // of them does not keep the others' memory.
 constexpr int64_t kShared = 32 * 1024;
@@ -300,12 +288,18 @@ bool make_shared(std::initializer_list<Wanted> outs, const at::Tensor& like, PyO
   bool all = stream == Py_None;
   for (const Wanted& w : outs) all = all && w.out->o == Py_None, total += room(w);
   if (!all || total > most) return false;
-  const c10::Storage storage = new_storage(total, like);
+  const at::Tensor t = at::empty({total}, like.options().dtype(at::kByte).requires_grad(false));
+  // under a dispatch mode it may be something else than plain device memory
+  if (t.unsafeGetTensorImpl()->is_python_dispatch() || t.device() != like.device() ||
+      t.scalar_type() != at::kByte || t.numel() != total || !t.is_contiguous() ||
+      t.storage_offset() != 0)
+    return false;
+  char* const base = static_cast<char*>(t.data_ptr());
   int64_t at = 0;
   for (const Wanted& w : outs) {
     if (!w.wanted) continue;
-    w.out->hold(THPVariable_Wrap(in_storage(storage, at, w.sizes(), w.dtype)));
-    w.out->ptr = static_cast<char*>(storage.mutable_data()) + at;
+    w.out->hold(THPVariable_Wrap(in_storage(t.storage(), at, w.sizes(), w.dtype)));
+    w.out->ptr = base + at;
     at += room(w);
   }
   return true;
