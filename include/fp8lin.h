@@ -524,6 +524,9 @@ int fp8_moe_combine_bwd(const void* dy, int64_t lddy, const void* ys, int64_t ld
  * tokens (fp8_moe_route), sorts and dispatches them (above), and runs every expert's linears on
  * its own rows, by the block recipe and without reading the row counts back to the host.
  *
+ * Outputs (and the workspace) may not share memory with an input or with each other; a call where
+ * they do is refused (FP8_ERR_UNSUPPORTED).
+ *
  * Source: [NeMo] (the mixture-of-experts runs, dp=2 ep=2; TE's "recipe=block").
  */
 

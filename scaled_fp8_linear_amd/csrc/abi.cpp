@@ -6,6 +6,8 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <initializer_list>
+
 #include "launch.h"
 
 namespace {
@@ -699,6 +701,38 @@ int check_pair(const char* fn, const char* what, const void* codes, const float*
   return FP8_OK;
 }
 
+// Memory of a tensor: rows of `bytes` each, `pitch` apart (one row: dense).
+struct Region {
+  const char* what;
+  const void* p;
+  int64_t bytes, rows = 1, pitch = 0;
+};
+
+// Whether the dense region d shares a byte with one of the rows of s.
+bool meet(const Region& d, const Region& s) {
+  if (!d.p || !s.p || d.bytes <= 0 || s.bytes <= 0 || s.rows <= 0) return false;
+  const int64_t at = static_cast<int64_t>(reinterpret_cast<uintptr_t>(d.p)) -
+                     static_cast<int64_t>(reinterpret_cast<uintptr_t>(s.p));
+  // the first row of s that ends behind d's start
+  const int64_t r = at < s.bytes ? 0 : s.rows > 1 ? (at - s.bytes) / s.pitch + 1 : 1;
+  return r < s.rows && r * s.pitch < at + d.bytes;
+}
+
+// Outputs are written by workgroups while others still read the inputs, so none of them (all dense)
+// may share memory with an input or another output.
+int check_apart(const char* fn, std::initializer_list<Region> outs,
+                std::initializer_list<Region> ins) {
+  for (const Region* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Region& i : ins)
+      if (meet(*o, i))
+        return fail(FP8_ERR_UNSUPPORTED, "%s: %s shares memory with %s", fn, o->what, i.what);
+    for (const Region* q = outs.begin(); q != o; ++q)
+      if (meet(*o, *q))
+        return fail(FP8_ERR_UNSUPPORTED, "%s: %s shares memory with %s", fn, o->what, q->what);
+  }
+  return FP8_OK;
+}
+
 constexpr int64_t kMaxGroupedRows = (int64_t)1 << 23;
 
 int check_act(const char* fn, int64_t rows, int64_t valid, int64_t cols, int act, int dtype) {
@@ -750,6 +784,21 @@ int grouped(const char* fn, const void* x, const void* w, int64_t ldw, int64_t s
   if (!x || !w || !sx || !sw || !y) return fail(FP8_ERR_NULL, "%s: NULL operand or scale pointer", fn);
   if (!aligned16(x) || !aligned16(w) || !aligned16(y) || !aligned_to(sx, 4) || !aligned_to(sw, 4))
     return fail(FP8_ERR_ALIGN, "%s: operands and output must be 16-byte aligned, scales 4-byte", fn);
+  if (int e = check_apart(fn, {{"the output", y, 2 * rows * N}},
+                          {{"the codes", x, rows * K}, {"their scales", sx, rows * K / 32},
+                           {"offsets", offsets, 4 * ((int64_t)experts + 1)},
+                           {"counts", counts, 4 * (int64_t)experts}}))
+    return e;
+  // the experts' rows may alternate in memory (ldw above stride_w): one by one if y is among them
+  const Region out = {"", y, 2 * rows * N};
+  const int64_t far = experts - 1;
+  if (meet(out, {"", w, far * stride_w + (N - 1) * ldw + K}) ||
+      meet(out, {"", sw, 4 * (far * stride_sw + (N / 128 - 1) * ldsw + K / 128)}))
+    for (int64_t i = 0; i < experts; ++i)
+      if (int e = check_apart(fn, {{"the output", y, 2 * rows * N}},
+                              {{"the weights", static_cast<const uint8_t*>(w) + i * stride_w, K, N, ldw},
+                               {"their scales", sw + i * stride_sw, K / 32, N / 128, 4 * ldsw}}))
+        return e;
   fp8lin::GroupedArgs a{};
   a.x = static_cast<const uint8_t*>(x), a.w = static_cast<const uint8_t*>(w), a.sx = sx, a.sw = sw;
   a.ldw = ldw, a.stride_w = stride_w, a.ldsw = ldsw, a.stride_sw = stride_sw;
@@ -783,6 +832,12 @@ int fp8_moe_route(const void* logits, int64_t ldl, int64_t tokens, int64_t token
   if (int e = check_out(fn, "losses", losses, 1, 4)) return e;
   const int64_t need = fp8lin::moe_route_workspace(tokens, experts);
   if (int e = check_workspace(fn, workspace, workspace_bytes, need)) return e;
+  const int64_t eb = elem_bytes(dtype), pairs = 4 * tokens * topk;
+  if (int e = check_apart(fn, {{"expert_idx", expert_idx, pairs}, {"weights", weights, pairs},
+                               {"lse", lse, 4 * tokens}, {"counts", counts, 4 * experts},
+                               {"losses", losses, 8}, {"workspace", workspace, need}},
+                          {{"logits", logits, experts * eb, tokens_valid, ldl * eb}}))
+    return e;
   fp8lin::MoeRouteArgs a{};
   a.logits = logits, a.ldl = ldl, a.tokens = tokens, a.valid = tokens_valid, a.experts = experts;
   a.topk = topk, a.dtype = dtype, a.normalize = normalize != 0, a.idx = expert_idx;
@@ -805,7 +860,13 @@ int fp8_moe_route_bwd(const void* logits, int64_t ldl, const float* lse, const i
     return fail(FP8_ERR_ALIGN, "%s: dweights and dlosses must be 4-byte aligned", fn);
   if (int e = check_out(fn, "dlogits", dlogits, tokens, elem_bytes(dtype))) return e;
   if (tokens == 0) return ok();
-  if (logits == dlogits) return fail(FP8_ERR_UNSUPPORTED, "%s: dlogits must not be logits", fn);
+  const int64_t eb = elem_bytes(dtype), pairs = 4 * tokens * topk;
+  if (int e = check_apart(fn, {{"dlogits", dlogits, tokens * experts * eb}},
+                          {{"logits", logits, experts * eb, tokens_valid, ldl * eb},
+                           {"lse", lse, 4 * tokens}, {"expert_idx", expert_idx, pairs},
+                           {"weights", weights, pairs}, {"counts", counts, 4 * experts},
+                           {"dweights", dweights, pairs}, {"dlosses", dlosses, 8}}))
+    return e;
   fp8lin::MoeRouteArgs a{};
   a.logits = logits, a.ldl = ldl, a.tokens = tokens, a.valid = tokens_valid, a.experts = experts;
   a.topk = topk, a.dtype = dtype, a.normalize = normalize != 0;
@@ -827,6 +888,12 @@ int fp8_act_quantize(const void* h, int64_t ldh, int64_t rows, int64_t rows_vali
   if (q_t && rows % 128)
     return fail(FP8_ERR_SHAPE, "%s: q_t needs rows %% 128 == 0 (got %lld)", fn, (long long)rows);
   if (rows == 0 || (!q && !q_t && !hq)) return ok();
+  const int64_t width = gated ? 2 * cols : cols, eb = elem_bytes(dtype);
+  if (int e = check_apart(fn, {{"q", q, rows * cols}, {"scale", scale, rows * cols / 32},
+                               {"q_t", q_t, rows * cols}, {"scale_t", scale_t, rows * cols / 32},
+                               {"hq", hq, rows * width}, {"hscale", hscale, rows * width / 32}},
+                          {{"h", h, width * eb, rows_valid, ldh * eb}}))
+    return e;
   fp8lin::ActArgs a{};
   a.x = h, a.ldx = ldh, a.rows = rows, a.valid = rows_valid, a.cols = cols, a.act = act;
   a.gated = gated != 0, a.dtype = dtype, a.q = static_cast<uint8_t*>(q), a.scale = scale;
@@ -850,9 +917,14 @@ int fp8_act_quantize_bwd(const void* da, int64_t ldda, const void* hq, const flo
     return fail(FP8_ERR_ALIGN, "%s: dh is not aligned to its elements", fn);
   if (q_t && rows % 128)
     return fail(FP8_ERR_SHAPE, "%s: q_t needs rows %% 128 == 0 (got %lld)", fn, (long long)rows);
-  if ((q && q == hq) || (dh && dh == da))
-    return fail(FP8_ERR_UNSUPPORTED, "%s: outputs must not be inputs", fn);
   if (rows == 0 || (!q && !q_t && !dh)) return ok();
+  const int64_t width = gated ? 2 * cols : cols, eb = elem_bytes(dtype);
+  if (int e = check_apart(fn, {{"q", q, rows * width}, {"scale", scale, rows * width / 32},
+                               {"q_t", q_t, rows * width}, {"scale_t", scale_t, rows * width / 32},
+                               {"dh", dh, rows * width * eb}},
+                          {{"da", da, cols * eb, rows_valid, ldda * eb},
+                           {"hq", hq, rows_valid * width}, {"hscale", hscale, rows_valid * width / 32}}))
+    return e;
   fp8lin::ActArgs a{};
   a.x = da, a.ldx = ldda, a.rows = rows, a.valid = rows_valid, a.cols = cols, a.act = act;
   a.gated = gated != 0, a.dtype = dtype, a.q = static_cast<uint8_t*>(q), a.scale = scale;
@@ -894,6 +966,12 @@ int fp8_grouped_linear_wgrad(const void* qg_t, const void* qx_t, const float* sg
   if (!aligned16(qg_t) || !aligned16(qx_t) || !aligned16(dw) || !aligned_to(sg_t, 4) ||
       !aligned_to(sx_t, 4))
     return fail(FP8_ERR_ALIGN, "%s: operands and output must be 16-byte aligned, scales 4-byte", fn);
+  if (int e = check_apart(fn, {{"dw", dw, 2 * experts * N * K}},
+                          {{"qg_t", qg_t, N * rows}, {"sg_t", sg_t, N * rows / 32},
+                           {"qx_t", qx_t, K * rows}, {"sx_t", sx_t, K * rows / 32},
+                           {"offsets", offsets, 4 * ((int64_t)experts + 1)},
+                           {"counts", counts, 4 * (int64_t)experts}}))
+    return e;
   fp8lin::GroupedArgs a{};
   a.w = static_cast<const uint8_t*>(qg_t), a.x = static_cast<const uint8_t*>(qx_t);
   a.sw = sg_t, a.sx = sx_t, a.offsets = offsets, a.counts = counts, a.experts = experts;
