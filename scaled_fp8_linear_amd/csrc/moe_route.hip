@@ -560,6 +560,9 @@ hipError_t launch_moe_route(const MoeRouteArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+// A launch has fewer than 2^32 threads: more tokens (2^25 of more than 128 experts) take several.
+constexpr int64_t kRouteBwdMaxBlocks = (int64_t)1 << 23;
+
 hipError_t launch_moe_route_bwd(const MoeRouteArgs& a, hipStream_t s) {
   const double t = (double)(a.valid > 0 ? a.valid : 1);
   const float sa = (float)((double)a.experts / (t * t * a.topk)), sb = (float)(2.0 / t);
@@ -567,13 +570,17 @@ hipError_t launch_moe_route_bwd(const MoeRouteArgs& a, hipStream_t s) {
     using T = decltype(tag);
     return by_experts<true>(a.experts, [&](auto g, auto nv) {
       constexpr int G = decltype(g)::value, kTokens = kRouteBwdThreads / G;
-      hipLaunchKernelGGL((moe_route_bwd_kernel<T, G, decltype(nv)::value>),
-                         dim3((unsigned)((a.tokens + kTokens - 1) / kTokens)),
-                         dim3(kRouteBwdThreads), 0, s, static_cast<const T*>(a.logits), a.ldl,
-                         a.tokens, a.valid, a.experts, a.topk, a.normalize, a.lse, a.idx,
-                         a.weights, a.counts, a.dweights, a.dlosses, sa, sb,
-                         static_cast<T*>(a.dlogits));
-      return hipGetLastError();
+      for (int64_t t0 = 0; t0 < a.tokens; t0 += kRouteBwdMaxBlocks * kTokens) {
+        const int64_t n = min(a.tokens - t0, kRouteBwdMaxBlocks * kTokens), pairs = t0 * a.topk;
+        hipLaunchKernelGGL((moe_route_bwd_kernel<T, G, decltype(nv)::value>),
+                           dim3((unsigned)((n + kTokens - 1) / kTokens)), dim3(kRouteBwdThreads), 0, s,
+                           static_cast<const T*>(a.logits) + t0 * a.ldl, a.ldl, n, a.valid - t0,
+                           a.experts, a.topk, a.normalize, a.lse + t0, a.idx + pairs,
+                           a.weights + pairs, a.counts, a.dweights ? a.dweights + pairs : nullptr,
+                           a.dlosses, sa, sb, static_cast<T*>(a.dlogits) + t0 * a.experts);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+      }
+      return hipSuccess;
     });
   });
 }
