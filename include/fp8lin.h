@@ -545,13 +545,14 @@ int fp8_moe_route_workspace(int64_t tokens, int32_t experts, int64_t* bytes);
  *                equal ones by the lower index. A logit of -inf is never chosen; where a row has
  *                fewer others, -1 (which fp8_moe_sort drops). NaN ranks above every number.
  *   weights      float32 [tokens, topk] out: p of the choice, with normalize != 0 divided by the
- *                sum over the token's choices; 0 where expert_idx is -1.
- *   lse          float32 [tokens] out: log(sum exp(logits)); -inf for a row without a finite logit,
- *                0 for padding.
+ *                sum over the token's choices; 0 where expert_idx is -1. The choices of a row with NaN
+ *                or +inf have NaN, and so do the losses then.
+ *   lse          float32 [tokens] out: log(sum exp(logits)); -inf for a row of nothing but -inf, 0
+ *                for padding, NaN for a row with NaN or +inf.
  *   counts       int32 [experts] out: the pairs that chose the expert.
  *   losses       float32 [2] out: the balance loss experts / (T topk) sum_e counts[e] mean_t p[t, e]
- *                (1 where evenly used) and the z-loss mean_t lse[t]^2 (rows without a finite logit
- *                add nothing); both 0 for T = 0.
+ *                (1 where evenly used) and the z-loss mean_t lse[t]^2 (rows of nothing but -inf add
+ *                nothing); both 0 for T = 0.
  *   workspace    at least fp8_moe_route_workspace() bytes, 4-byte aligned; NULL if that is 0.
  * All sums are float32, in a fixed order.
  */
@@ -565,7 +566,8 @@ int fp8_moe_route(const void* logits, int64_t ldl, int64_t tokens, int64_t token
  *   logits, lse, expert_idx, weights, counts   as of the forward, with the same sizes.
  *   dweights     float32 [tokens, topk] or NULL (0); entries of dropped choices are not used.
  *   dlosses      float32 [2] or NULL (0).
- *   dlogits      [tokens, experts] of `dtype` out, dense; 0 for padding and for logits of -inf.
+ *   dlogits      [tokens, experts] of `dtype` out, dense; 0 for padding and for logits of -inf,
+ *                whatever the rest of the row or dlosses hold.
  */
 int fp8_moe_route_bwd(const void* logits, int64_t ldl, const float* lse, const int32_t* expert_idx,
                       const float* weights, const int32_t* counts, const float* dweights,

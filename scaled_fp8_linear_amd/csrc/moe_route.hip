@@ -9,7 +9,8 @@
 //     losses       { E / (T k) sum_e counts[e] P[e],  (1/T) sum_t lse[t]^2 }
 //
 // A logit of -inf is a masked expert: never chosen, p = 0. A row without any other has idx -1,
-// w 0, lse -inf, and adds nothing to P and to the losses. NaN ranks above every number.
+// w 0, lse -inf, and adds nothing to P and to the losses. NaN ranks above every number; a row with it
+// or with +inf has NaN for p of every expert that is not masked.
 //
 // G consecutive lanes hold a token's logits, NV each, so the sums and maxima are DPP steps of log2 G.
 // A choice is the maximum of the unsigned keys that order like the logits; for 16-bit types the key's
@@ -269,7 +270,7 @@ moe_route_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, int6
         const int j = s * G + gl;
         if (j < k) {
           idx[tok * k + j] = rec_e[s];
-          weights[tok * k + j] = w[s] * f;
+          weights[tok * k + j] = rec_e[s] < 0 ? 0.f : w[s] * f;     // f may be NaN
         }
       }
       if (gl == 0) lse[tok] = live ? row_lse : 0.f;
@@ -460,6 +461,9 @@ moe_route_bwd_kernel(const T* __restrict__ logits, int64_t ldl, int64_t tokens, 
 #pragma unroll
     for (int i = 0; i < NV; ++i) d[i] = p[i] * inv * rest;
   }
+  // a masked expert's is 0 also where the rest of the row is not finite
+#pragma unroll
+  for (int i = 0; i < NV; ++i) d[i] = to_f32(x[i]) == -INFINITY ? 0.f : d[i];
   if (dweights) {
 #pragma unroll
     for (int i = 0; i < NV; i += L::V)
