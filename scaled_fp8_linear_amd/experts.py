@@ -213,15 +213,17 @@ class _ExpertMlpFn(torch.autograd.Function):
     a gated h 3 bytes an element of a, against 5 with h in bf16."""
 
     @staticmethod
-    def forward(ctx, xs, w_up, w_down, offsets, counts, act, gated, max_rows):
-        grad = any(ctx.needs_input_grad[:3])
-        qx, sx, qx_t, sx_t = _quantize_rows(xs, grad and ctx.needs_input_grad[1])
-        (q1, s1), up_t = _quantize_experts(w_up, grad and ctx.needs_input_grad[0])
+    def forward(ctx, xs, w_up, w_down, offsets, counts, act, gated, max_rows, grad):
+        # `grad`: whether the graph is recorded, which needs_input_grad does not tell
+        want_x, want_up, want_down = (grad and need for need in ctx.needs_input_grad[:3])
+        want_h = want_x or want_up
+        qx, sx, qx_t, sx_t = _quantize_rows(xs, want_up)
+        (q1, s1), up_t = _quantize_experts(w_up, want_x)
         h = _abi.fp8_grouped_linear_fwd(qx, q1, sx, s1, offsets, counts, max_rows=max_rows)
-        qa, sa, qa_t, sa_t, hq, hs = _abi.fp8_act_quantize(
-            h, act, gated, want_q_t=grad and ctx.needs_input_grad[2], want_checkpoint=grad)
+        qa, sa, qa_t, sa_t, hq, hs = _abi.fp8_act_quantize(h, act, gated, want_q_t=want_down,
+                                                           want_checkpoint=want_h)
         del h
-        (q2, s2), down_t = _quantize_experts(w_down, grad)
+        (q2, s2), down_t = _quantize_experts(w_down, want_h)
         ys = _abi.fp8_grouped_linear_fwd(qa, q2, sa, s2, offsets, counts, max_rows=max_rows)
         ctx.save_for_backward(qx_t, sx_t, *up_t, qa_t, sa_t, hq, hs, *down_t, offsets, counts)
         ctx.args = (act, gated, max_rows)
@@ -247,7 +249,7 @@ class _ExpertMlpFn(torch.autograd.Function):
             if want_x:
                 dx = _abi.fp8_grouped_linear_dgrad(qh, q1_t, sh, s1_t, offsets, counts,
                                                    max_rows=max_rows)
-        return dx, dup, ddown, None, None, None, None, None
+        return dx, dup, ddown, None, None, None, None, None, None
 
 
 def _check_whole_blocks(plan: ExpertPlan):
@@ -293,7 +295,7 @@ def expert_mlp(xs, w_up, w_down, plan: ExpertPlan, act: str = "silu", gated: boo
         raise ValueError(f"the plan has {xs.shape[0]} rows, with multiple=128 it has {least}")
     _check_whole_blocks(plan)
     return _ExpertMlpFn.apply(xs.contiguous(), w_up, w_down, plan.offsets, plan.counts, act, gated,
-                              plan.slot.shape[0])
+                              plan.slot.shape[0], torch.is_grad_enabled())
 
 
 class ExpertBlock(torch.nn.Module):
