@@ -195,17 +195,24 @@ def _quantize_rows(x, transposed: bool):
     return q, scale, q_t, scale_t
 
 
+# The products take weights whose rows are fewer codes than this apart.
+_ROW_STRIDE_LIMIT = 1 << 23
+
+
 def _quantize_experts(w, transposed: bool):
     """Stacked weights [experts, n, k] in 128x128 tiles: codes and scales [experts, n, k], and
-    transposed as [experts, k, n]."""
+    transposed as [experts, k, n]. The transposed rows of all experts alternate in memory; a stack
+    whose rows would be too far apart for the products is copied expert by expert."""
     e, n, k = w.shape
     q, q_t, _, scale, scale_t = _abi.fp8_quantize_amax(
         w.reshape(e * n, k), gran=_abi.FP8_BLOCK_128x128, want_q_t=transposed, want_amax=False)
     first = (q.view(e, n, k), scale.view(e, n // 128, k // 128))
     if not transposed:
         return first, (None, None)
-    return first, (q_t.view(k, e, n).transpose(0, 1),
-                   scale_t.view(k // 128, e, n // 128).transpose(0, 1))
+    q_t = q_t.view(k, e, n).transpose(0, 1)
+    if e * n >= _ROW_STRIDE_LIMIT:
+        q_t = q_t.contiguous()
+    return first, (q_t, scale_t.view(k // 128, e, n // 128).transpose(0, 1))
 
 
 class _ExpertMlpFn(torch.autograd.Function):
