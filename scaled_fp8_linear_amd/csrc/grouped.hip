@@ -376,7 +376,7 @@ grouped_tile_kernel(GroupedArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kSlots * SB +
                                                             (kSlots + 1) * kRegion];
   __shared__ int first_tile[BROWS == 128 ? kMaxSpans + 1 : 1];   // spans: row tiles before it
-  uint8_t* const regions = smem + kSlots * SB;          // kSlots, and one that nobody reads
+  uint8_t* const regions = smem + kSlots * SB;          // kSlots, and one of zeros
 
   const int t = threadIdx.x, lane = t & 63;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -395,6 +395,8 @@ grouped_tile_kernel(GroupedArgs a) {
     return BROWS == 128 ? span_of(a, i) : expert_span(a.offsets, a.counts, i, a.rows);
   };
   const int tiles_m = BROWS == 128 ? 0 : ((int)a.N + BM - 1) / BM;    // of an expert's gradient
+  for (int i = t; i < kRegion / 16; i += kTileThreads)
+    reinterpret_cast<uint4*>(regions + kSlots * kRegion)[i] = make_uint4(0, 0, 0, 0);
   if constexpr (BROWS == 128) {
     for (int i = t; i < spans; i += kTileThreads) {
       const Span s = span(i);
@@ -491,7 +493,7 @@ grouped_tile_kernel(GroupedArgs a) {
   const uint32_t inst_a = (uint32_t)(kRowsPerInst * kTileWaves) * lda;
   const uint32_t inst_b = (uint32_t)(kRowsPerInst * kTileWaves) * ldb;
   // lane p of the workgroup loads the scales of tile row p < BM, lane BM + c those of column (or
-  // block of columns) c; waves past them load nothing, to the place where nobody reads
+  // block of columns) c; waves past them load nothing, which writes zeros, to the region of zeros
   const int p = 64 * wave + lane;
   const bool sc_from_a = 64 * wave < BM;
   uint32_t sc_lane = kOutOfRange;              // others are below 2^27
@@ -574,10 +576,11 @@ grouped_tile_kernel(GroupedArgs a) {
   const int pb_lane = BROWS == 1 ? BM + wn * WTN + 4 * g4 : BM + wn * WTN / 128;
   typedef const __attribute__((address_space(3))) float lds_f32;
   float fa[RT], fn[PF ? RT : 1], fb[BROWS == 1 ? 4 * CT : 1];
-  // the scales of the group's stage q: of the lane's rows, times the wave's B scale where there is
-  // one, else also of its columns
-  auto rd_scales = [&](float* fs, int rg, int q) __attribute__((always_inline)) {
-    const uint32_t r = lds_addr(regions) + (uint32_t)(rg * kRegion) + 4u * q;
+  // the scales of a tile's stage s in region rg: of the lane's rows, times the wave's B scale where
+  // there is one, else also of its columns; zeros past the last block
+  auto rd_scales = [&](float* fs, int rg, int s, int nk) __attribute__((always_inline)) {
+    const uint32_t r = lds_addr(regions) + (uint32_t)((s < nk ? rg : kSlots) * kRegion) +
+                       4u * (s % kGroup);
     uint32_t ba = r + 16u * pa_lane, bb = r + 16u * pb_lane;
     asm volatile("" : "+v"(ba), "+v"(bb));
 #pragma unroll
@@ -621,7 +624,7 @@ grouped_tile_kernel(GroupedArgs a) {
     const v4f z = {};
     const Bases qm = bases(mine);
     Bases qo{};
-    if constexpr (!PF) rd_scales(fa, rg, min(s, nk - 1) % kGroup);
+    if constexpr (!PF) rd_scales(fa, rg, s, nk);
     // the next stage: of the same group of scales, the next group, or the next tile
     const bool last = s + 1 == ns;
     const int rg1 = last || (s + 1) % kGroup == 0 ? after(rg) : rg;
@@ -646,7 +649,7 @@ grouped_tile_kernel(GroupedArgs a) {
 #pragma unroll
         for (int d = y * kDma / kTail; d < (y + 1) * kDma / kTail; ++d) dma(d, mine, r, sl);
         if constexpr (PF)
-          if (y == 1) rd_scales(fn, rg1, last ? 0 : min(s + 1, nk - 1) % kGroup);
+          if (y == 1) rd_scales(fn, rg1, last ? 0 : s + 1, nk);
         if (y == 0) Aq[0] = rdA(qo, 0);
         if (y == CT) Aq[1] = rdA(qo, 1);
         if (i == RT - 1) Bq[j] = rdB(qo, j);
@@ -661,7 +664,7 @@ grouped_tile_kernel(GroupedArgs a) {
     }
     // If the loaded stage begins a group of scales, they go into the region after that of the stage
     // before it: with kSlots regions that is neither stage s + 1's, which slower waves still read,
-    // nor one of the stages between. Else the load is an empty one, to where nobody reads.
+    // nor one of the stages between. Else the load is an empty one, to the region of zeros.
     int rgl = rg1;
     if constexpr (kSlots == 3)
       rgl = s + 2 == ns || (s + 2 < ns && (s + 2) % kGroup == 0) ? after(rg1) : rg1;
@@ -728,7 +731,7 @@ grouped_tile_kernel(GroupedArgs a) {
       return ti;
     };
     // A tile has at least kSlots stages, so that what is loaded kSlots ahead is its own or the next
-    // tile's. Stages past its last block multiply zeros with that block's scales.
+    // tile's. Stages past its last block multiply zeros with zeros for scales (a scale may be infinite).
     mine = smem, other = smem + SB, third = smem + (kSlots - 1) * SB;
     int ti = with_products(first), tn = with_products(ti + 1);
     cur = res_of(ti), nxt = res_of(tn);
@@ -747,7 +750,7 @@ grouped_tile_kernel(GroupedArgs a) {
       for (int j = 0; j < CT; ++j) Bq[j] = rdB(q, j);
       Aq[0] = rdA(q, 0);
       Aq[1] = rdA(q, 1);
-      if constexpr (PF) rd_scales(fa, 0, 0);
+      if constexpr (PF) rd_scales(fa, 0, 0, 1);
     }
     while (ti < batch_end) {
       const int nk = tile_of(ti).nk, ns = max(nk, kSlots);
