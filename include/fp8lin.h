@@ -582,7 +582,8 @@ typedef enum fp8_act { FP8_ACT_RELU = 0, FP8_ACT_SILU = 1, FP8_ACT_GELU = 2 } fp
  * tiles as it is made, and its input kept in 8 bits for the backward.
  *
  *   h            [rows, cols] of `dtype`, or with gated != 0 [rows, 2 cols] = [g | u]; row stride
- *                ldh. cols a positive multiple of 128, below 2^17; rows below 2^23.
+ *                ldh. cols a positive multiple of 128, below 2^17; rows below 2^23; at most
+ *                2^23 - 64 tiles of 128 x 128 in rows x cols.
  *   rows_valid   rows at or past it are padding: not read, taken as zeros.
  *   act          FP8_ACT_RELU, FP8_ACT_SILU (x / (1 + exp(-x))) or FP8_ACT_GELU (the form with
  *                tanh). a = act(h), or act(g) u.

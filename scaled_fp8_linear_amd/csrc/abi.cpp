@@ -741,6 +741,9 @@ int check_act(const char* fn, int64_t rows, int64_t valid, int64_t cols, int act
                 "%lld)", fn, (long long)rows, (long long)cols);
   if (rows >= kMaxGroupedRows || cols >= kMaxContraction)
     return fail(FP8_ERR_UNSUPPORTED, "%s: 2^23 rows or 2^17 columns or more", fn);
+  // a workgroup of 512 threads a tile, in sixty-fours, and fewer than 2^32 threads in a launch
+  if ((rows + 127) / 128 * (cols / 128) > ((int64_t)1 << 23) - 64)
+    return fail(FP8_ERR_UNSUPPORTED, "%s: more than 2^23 - 64 tiles of 128 x 128", fn);
   if (valid < 0 || valid > rows)
     return fail(FP8_ERR_SHAPE, "%s: rows_valid=%lld outside [0, %lld]", fn, (long long)valid,
                 (long long)rows);
