@@ -259,14 +259,17 @@ class _ExpertMlpFn(torch.autograd.Function):
         return dx, dup, ddown, None, None, None, None, None, None
 
 
-def _check_whole_blocks(plan: ExpertPlan):
+def _check_whole_blocks(plan: ExpertPlan, weight_grads: bool):
     """Refuse a plan whose experts do not begin at multiples of 128 rows. The row count cannot tell
     (200 pairs of 2 experts take 384 rows with multiple 96 and with 128), so without the plan's
-    multiple the offsets are read back."""
+    multiple the offsets are read back, if weights have gradients: only those take whole blocks."""
     if plan.multiple is not None:
         whole = plan.multiple % 128 == 0
+    elif not weight_grads:
+        return
     elif plan.offsets.is_cuda and torch.cuda.is_current_stream_capturing():
-        raise ValueError("a plan that expert_plan did not make cannot be checked during a capture")
+        raise ValueError("the offsets of a plan that expert_plan did not make cannot be read back "
+                         "during a capture")
     else:
         whole = not (plan.offsets % 128).any().item()
     if not whole:
@@ -279,8 +282,8 @@ def expert_mlp(xs, w_up, w_down, plan: ExpertPlan, act: str = "silu", gated: boo
     (bf16, sorted by a plan with multiple 128), by the block recipe and without reading the row
     counts back: act(xs W_up^T) W_down^T, or with ``gated`` act(g) u of [g | u] = xs W_up^T. w_up
     [experts, hidden or 2 hidden, cols] and w_down [experts, cols, hidden] are bf16, cols and hidden
-    multiples of 128. The offsets of a plan that expert_plan did not make are read back once to check
-    that they are multiples of 128. Rows of no expert give 0. For the backward the activation's input is kept in 8
+    multiples of 128. Where a weight has a gradient, the offsets of a plan that expert_plan did not
+    make are read back to check that they are multiples of 128. Rows of no expert give 0. For the backward the activation's input is kept in 8
     bits. The gradient of ys has to be finite in padding rows (expert_combine's is 0 there)."""
     xs = _as_rows(xs)
     e, cols, hidden = w_down.shape
@@ -300,9 +303,10 @@ def expert_mlp(xs, w_up, w_down, plan: ExpertPlan, act: str = "silu", gated: boo
     least = _abi.fp8_moe_rows(*plan.slot.shape, e, 128)
     if xs.shape[0] < least:         # of another multiple: blocks of 128 rows would mix experts
         raise ValueError(f"the plan has {xs.shape[0]} rows, with multiple=128 it has {least}")
-    _check_whole_blocks(plan)
+    grad = torch.is_grad_enabled()
+    _check_whole_blocks(plan, grad and (w_up.requires_grad or w_down.requires_grad))
     return _ExpertMlpFn.apply(xs.contiguous(), w_up, w_down, plan.offsets, plan.counts, act, gated,
-                              plan.slot.shape[0], torch.is_grad_enabled())
+                              plan.slot.shape[0], grad)
 
 
 class ExpertBlock(torch.nn.Module):

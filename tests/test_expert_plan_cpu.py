@@ -40,10 +40,10 @@ def called(monkeypatch):
     return calls
 
 
-def mlp(plan, experts):
+def mlp(plan, experts, up=True, down=True):
     xs = torch.zeros(plan.source.numel(), 128, dtype=BF)
-    return m.expert_mlp(xs, torch.zeros(experts, 256, 128, dtype=BF),
-                        torch.zeros(experts, 128, 128, dtype=BF), plan)
+    return m.expert_mlp(xs, torch.zeros(experts, 256, 128, dtype=BF, requires_grad=up),
+                        torch.zeros(experts, 128, 128, dtype=BF, requires_grad=down), plan)
 
 
 # an expert's pairs and a multiple whose row count is a multiple of 128 and not below that of
@@ -62,7 +62,17 @@ def test_row_counts_do_not_tell(called, per_expert, multiple):
     for p in (plan, copy.copy(plan), pickle.loads(pickle.dumps(plan)), bare):
         with pytest.raises(ValueError, match="mix experts"):
             mlp(p, len(per_expert))
+    for up, down in ((True, False), (False, True)):
+        with pytest.raises(ValueError, match="mix experts"):
+            mlp(bare, len(per_expert), up, down)
     assert not called
+    # the products alone take any offsets, and nothing is read back
+    mlp(bare, len(per_expert), False, False)
+    with torch.no_grad():
+        mlp(bare, len(per_expert))
+        with pytest.raises(ValueError, match="mix experts"):
+            mlp(plan, len(per_expert))
+    assert len(called) == 2
 
 
 @pytest.mark.parametrize("multiple", [128, 256, 384])
