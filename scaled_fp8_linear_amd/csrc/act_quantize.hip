@@ -23,9 +23,11 @@
 // steps over the 16 lanes of a row; column maxima go over the lanes and then through LDS, as do
 // the transposed codes (4 rows in a dword).
 //
-// What bounds it: memory. 17408 x 14336 bf16 gated: forward 363 us, 2.0 GB (5.5 TB/s), backward
-// 424 us, 2.0 GB (4.7 TB/s; it writes twice what it reads). A token of 128 padding rows 5.4 us, most
-// of it the call.
+// What bounds it: memory. 17408 x 14336 bf16 gated, calls over three sets of inputs: forward 393 us,
+// 2.0 GB (5.1 TB/s), backward 430 us, 2.0 GB (4.7 TB/s). Either reads about as much as it writes, and
+// writes 10 to 13 % more than that, since a tile's scales are 4 bytes of a line that other tiles write
+// too. Why the backward is the slower one is not known. A token of 128 padding rows 5.5 us, most of it
+// the call.
 #include "common.h"
 #include "launch.h"
 #include "rows.h"
@@ -240,9 +242,9 @@ __device__ __forceinline__ void emit_cols(const float (&v)[kARows][8], const Pla
 }
 
 // Workgroups go round-robin over the 8 XCDs. An XCD takes runs of 8 tiles, so that the neighbours
-// whose scales share 32 bytes write them in one L2 (17408 x 14336 gated, us: single tiles 370 forward
-// and 462 backward, runs of 8 364 and 423, of 16 and 32 360 and 431, an eighth of all 374 and 433;
-// 80 tiles and 224 take the same either way).
+// whose scales share 32 bytes write them in one L2 (17408 x 14336 gated, us: single tiles 410 forward
+// and 472 backward, runs of 8 393 and 430, of 16 387 and 432, of 32 387 and 437; 80 tiles and 224 take
+// the same either way).
 constexpr int kRun = 8;
 int64_t act_workgroups(int64_t tiles) { return (tiles + 8 * kRun - 1) / (8 * kRun) * (8 * kRun); }
 __device__ __forceinline__ bool place(Place& at, int64_t rows, int tiles_c, int64_t& tc) {

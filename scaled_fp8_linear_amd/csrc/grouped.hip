@@ -809,7 +809,12 @@ bool low_tiles(const GroupedArgs& a) {
 
 // Less than 10 items of a stream a CU take less than a round of tiles (y of 8 experts' 250 rows: 35.1 us
 // to 38.7 at 1024 x 4096, 2112 items, 58.2 to 40.4 at 2048 x 4096, 4224; dw of 8 experts, 512 x 512,
-// 1000 rows: 14.4 to 20.6, 2048 items; of 4, 1024 x 1024, 4000 rows: 66.0 to 53.8, 4096).
+// 1000 rows: 14.4 to 20.6, 2048 items; of 4, 1024 x 1024, 4000 rows: 66.0 to 53.8, 4096). The
+// contraction's length is not in it, over which the streams read the weights again for every 32 rows.
+// Few columns favour them all the same (y of 5 experts' 1104 rows, 768 x 13952, 54 to 104; of 16
+// experts' 500, 1024 x 8192, 57 to 76); many do not, and next to the limit the rule then takes the
+// slower side: y of 2 experts' 136 rows, 9088 x 10496, 2556 items, 164 to 100; of 4 experts' 100 tokens
+// with two choices, 8192 x 4096, 47.0 to 46.3.
 template <int BROWS>
 bool few_items(const GroupedArgs& a) {
   const int64_t columns = (BROWS == 1 ? a.K : a.N) / 32;
