@@ -282,9 +282,10 @@ def expert_mlp(xs, w_up, w_down, plan: ExpertPlan, act: str = "silu", gated: boo
     (bf16, sorted by a plan with multiple 128), by the block recipe and without reading the row
     counts back: act(xs W_up^T) W_down^T, or with ``gated`` act(g) u of [g | u] = xs W_up^T. w_up
     [experts, hidden or 2 hidden, cols] and w_down [experts, cols, hidden] are bf16, cols and hidden
-    multiples of 128. Where a weight has a gradient, the offsets of a plan that expert_plan did not
-    make are read back to check that they are multiples of 128. Rows of no expert give 0. For the backward the activation's input is kept in 8
-    bits. The gradient of ys has to be finite in padding rows (expert_combine's is 0 there)."""
+    multiples of 128. Rows of no expert give 0. For the backward the activation's input is kept in 8
+    bits. The gradient of ys has to be finite in padding rows (expert_combine's is 0 there). Where a
+    weight has a gradient, the offsets of a plan that expert_plan did not make are read back to check
+    that they are multiples of 128."""
     xs = _as_rows(xs)
     e, cols, hidden = w_down.shape
     width = 2 * hidden if gated else hidden
